@@ -1,0 +1,199 @@
+// Selective scan with one decay per head over packed requests
+// (include/ssfwd_packed.h): the form that takes every type and size, token by
+// token in fp32. Per request and head, with S (headdim x dstate):
+//   S = exp(dt A) S + dt x B^T;  y = S C + D x;  out = y silu(z).
+//
+// One CTA carries 64 rows of one head's state in registers through one block of
+// a request (16 lanes a row, 4 rows a lane), and stages 16 tokens at a time in
+// shared memory. It is bound by the fp32 operations, three for every state value
+// and token. When requests may have several blocks, a first launch brings every
+// block but the last from zero (the first one from the request's start) to its
+// end; the second folds the ends of the earlier blocks, each with the decay
+// since, into its start.
+#include "ss_fwd_kernel.cuh"
+#include "ss_packed.h"
+
+namespace ssk {
+namespace {
+
+constexpr int kLanes = 16, kRowsPerLane = 4, kRows = 64, kTokens = 16;
+constexpr int kScanThreads = kLanes * kRows / kRowsPerLane;
+
+template <typename T, int NPL, bool SUMMARY>
+__global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid_constant__ HeadScanParams p) {
+  constexpr int V = NPL < 4 ? NPL : 4, Q = NPL / V, NP = kLanes * NPL;
+  __shared__ __align__(16) float xs[kTokens][kRows];
+  __shared__ __align__(16) float bs[kTokens][NP];
+  __shared__ __align__(16) float cs[SUMMARY ? 1 : kTokens][NP];
+  __shared__ float ys[SUMMARY ? 1 : kTokens][kRows];
+  __shared__ float dts[kTokens], keeps[kTokens];
+  const int tid = threadIdx.x, j = tid % kLanes, rg = tid / kLanes;
+  const int ptiles = (p.headdim + kRows - 1) / kRows;
+  const int h = blockIdx.y / ptiles, p0 = (blockIdx.y % ptiles) * kRows;
+  const int prow = min(kRows, p.headdim - p0);
+  const int g = h / p.hpg;
+  T *out = static_cast<T *>(p.out) + h * p.so[1] + p0;
+  if ((int)blockIdx.x == p.t.max_blocks) {  // past the last token: zeros
+    if (!SUMMARY) {
+      for (int t = p.t.counts[0]; t < p.t.tokens; ++t)
+        for (int i = tid; i < prow; i += kScanThreads) out[t * p.so[0] + i] = from_f<T>(0.f);
+    }
+    return;
+  }
+  const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blockIdx.x];
+  const int r = row.x, first = row.y, size = row.z, index = row.w;
+  if (r < 0) return;
+  const int len = p.t.offsets[r + 1] - p.t.offsets[r];
+  const int last = (len - 1) / p.t.block;  // index of the request's last block
+  const int slot0 = p.state ? p.t.slot_map[r] : -1;
+  const bool kept = slot0 >= 0 && slot0 < p.slots;
+  const bool goes_on = kept && p.t.context && p.t.context[r] > 0;
+  float *cache = kept ? p.state + slot0 * p.ss[0] + h * p.ss[1] + (long long)p0 * p.dstate : nullptr;
+  const long long pn = (long long)p.headdim * p.dstate;
+  auto entry = [&](int i) {  // summary of the request's block i
+    return p.ws_state + ((long long)(blockIdx.x - index + i) * p.heads + h) * pn + (long long)p0 * p.dstate;
+  };
+  auto decay_of = [&](int i) { return p.ws_decay + (long long)(blockIdx.x - index + i) * p.heads + h; };
+  if (SUMMARY && last == 0) return;
+
+  float s[kRowsPerLane][NPL];
+  auto each = [&](auto f) {  // f(row, state, register) over the lane's values
+#pragma unroll
+    for (int u = 0; u < kRowsPerLane; ++u)
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int pr = rg * kRowsPerLane + u, n = V * (j + kLanes * q) + i;
+          f(pr < prow && n < p.dstate, (long long)pr * p.dstate + n, s[u][q * V + i]);
+        }
+  };
+  auto load = [&](const float *src) {
+    each([&](bool in, long long at, float &v) { v = src && in ? src[at] : 0.f; });
+  };
+  auto store = [&](float *dst) {
+    each([&](bool in, long long at, float &v) { if (in) dst[at] = v; });
+  };
+  if (SUMMARY) {
+    if (index == last) {  // keeps the start, which the cache loses when the last block ends
+      if (goes_on) {
+        load(cache);
+        store(entry(last));
+      }
+      return;
+    }
+    load(index == 0 && goes_on ? cache : nullptr);
+  } else if (index == 0) {
+    load(goes_on ? (last > 0 ? entry(last) : cache) : nullptr);
+  } else {
+    load(entry(0));
+    for (int i = 1; i < index; ++i) {
+      const float keep = ex2(*decay_of(i) * kLog2e);
+      const float *e = entry(i);
+      each([&](bool in, long long at, float &v) { v = in ? fmaf(keep, v, e[at]) : 0.f; });
+    }
+  }
+
+  const float A = p.A[h], bias = p.bias ? p.bias[h] : 0.f, skip = p.D ? p.D[h] : 0.f;
+  const T *x = static_cast<const T *>(p.x) + h * p.sx[1] + p0;
+  const T *z = p.z ? static_cast<const T *>(p.z) + h * p.sz[1] + p0 : nullptr;
+  const T *B = static_cast<const T *>(p.B) + g * p.sB[1], *C = static_cast<const T *>(p.C) + g * p.sC[1];
+  float decay = 0.f;
+  for (int base = 0; base < size; base += kTokens) {
+    const int n_tok = min(kTokens, size - base);
+    const long long t0 = first + base;
+    __syncthreads();
+    for (int i = tid; i < kTokens * kRows; i += kScanThreads) {
+      const int t = i / kRows, k = i % kRows;
+      xs[t][k] = t < n_tok && k < prow ? to_f<T>(x[(t0 + t) * p.sx[0] + k]) : 0.f;
+    }
+    for (int i = tid; i < kTokens * NP; i += kScanThreads) {
+      const int t = i / NP, k = i % NP;
+      const bool in = t < n_tok && k < p.dstate;
+      bs[t][k] = in ? to_f<T>(B[(t0 + t) * p.sB[0] + k]) : 0.f;
+      if (!SUMMARY) cs[t][k] = in ? to_f<T>(C[(t0 + t) * p.sC[0] + k]) : 0.f;
+    }
+    if (tid < n_tok) {
+      const long long at = (t0 + tid) * p.sdt[0] + h * p.sdt[1];
+      float dt = bias + (p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]));
+      if (p.softplus) dt = softplus_f(dt);
+      dts[tid] = dt;
+      keeps[tid] = dt * A;
+    }
+    __syncthreads();
+    for (int t = 0; t < n_tok; ++t) {
+      const float dt = dts[t], keep = ex2(keeps[t] * kLog2e);
+      float b[NPL], c[NPL], y[kRowsPerLane], in[kRowsPerLane];
+      decay += keeps[t];
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          b[q * V + i] = bs[t][V * (j + kLanes * q) + i];
+          if (!SUMMARY) c[q * V + i] = cs[t][V * (j + kLanes * q) + i];
+        }
+#pragma unroll
+      for (int u = 0; u < kRowsPerLane; ++u) {
+        in[u] = dt * xs[t][rg * kRowsPerLane + u];
+        y[u] = 0.f;
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) {
+          s[u][k] = fmaf(keep, s[u][k], in[u] * b[k]);
+          if (!SUMMARY) y[u] = fmaf(c[k], s[u][k], y[u]);
+        }
+      }
+      if (!SUMMARY) {
+#pragma unroll
+        for (int u = 0; u < kRowsPerLane; ++u)
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) y[u] += __shfl_xor_sync(0xffffffffu, y[u], o);
+#pragma unroll
+        for (int u = 0; u < kRowsPerLane; ++u)
+          if (j == u) ys[t][rg * kRowsPerLane + u] = y[u];
+      }
+    }
+    if (!SUMMARY) {
+      __syncthreads();
+      for (int i = tid; i < n_tok * kRows; i += kScanThreads) {
+        const int t = i / kRows, k = i % kRows;
+        if (k < prow) {
+          float v = fmaf(skip, xs[t][k], ys[t][k]);
+          if (z) v *= silu_f(to_f<T>(z[(t0 + t) * p.sz[0] + k]));
+          out[(t0 + t) * p.so[0] + k] = from_f<T>(v);
+        }
+      }
+    }
+  }
+  if (SUMMARY) {
+    store(entry(index));
+    if (tid == 0 && p0 == 0) *decay_of(index) = decay;
+  } else if (index == last && kept) {
+    store(cache);
+  }
+}
+
+template <typename T, int NPL>
+void go(const HeadScanParams &p, cudaStream_t s) {
+  const dim3 grid(p.t.max_blocks + 1, p.heads * ((p.headdim + kRows - 1) / kRows));
+  if (p.split) ss_head_scan_kernel<T, NPL, true><<<grid, kScanThreads, 0, s>>>(p);
+  ss_head_scan_kernel<T, NPL, false><<<grid, kScanThreads, 0, s>>>(p);
+}
+template <typename T>
+void by_states(const HeadScanParams &p, cudaStream_t s) {
+  if (p.dstate > 128) go<T, 16>(p, s);
+  else if (p.dstate > 64) go<T, 8>(p, s);
+  else if (p.dstate > 32) go<T, 4>(p, s);
+  else if (p.dstate > 16) go<T, 2>(p, s);
+  else go<T, 1>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s) {
+  if (dtype == 0) by_states<float>(p, s);
+  else if (dtype == 1) by_states<__half>(p, s);
+  else by_states<__nv_bfloat16>(p, s);
+  return cudaGetLastError();
+}
+
+}  // namespace ssk

@@ -1,0 +1,77 @@
+// Kernel parameters and launchers of the packed operators (include/ssfwd_packed.h).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ssk {
+
+// The library's error word on the current device (nullptr on failure).
+int32_t *packed_error_word();
+
+struct TablesParams {
+  int requests, tokens, block, max_blocks, free;
+  const int32_t *lengths, *context, *slots, *free_slots;
+  int32_t *offsets, *token_request, *token_position, *blocks, *slot_map, *counts;
+};
+cudaError_t launch_request_tables(const TablesParams &p, cudaStream_t s);
+
+struct Tables {
+  int requests, tokens, block, max_blocks;
+  const int32_t *offsets, *token_request, *blocks, *slot_map, *counts, *context;
+};
+
+struct PackedConvParams {
+  int dim, width, act;
+  int vec;  // 16-byte accesses of x, out rows and windows allowed
+  long long slots, sx, so, ss;
+  const void *x;
+  const float *weight, *bias;
+  void *state, *out;
+  Tables t;
+};
+cudaError_t launch_packed_conv(int dtype, const PackedConvParams &p, cudaStream_t s);
+
+struct PackedConvUpdateParams {
+  int requests, dim, width, act, vec;
+  long long slots, sx, so, ss;
+  const void *x;
+  const float *weight, *bias;
+  const int32_t *slot_map;
+  void *state, *out;
+};
+cudaError_t launch_packed_conv_update(int dtype, const PackedConvUpdateParams &p, cudaStream_t s);
+
+struct HeadUpdateParams {
+  int requests, heads, headdim, dstate, hpg;  // hpg: heads per group
+  int softplus, dt_f32, vec, bcvec;           // vec: 16-byte state accesses; bcvec: 4 B/C values in one access
+  long long slots;
+  const void *x, *dt, *B, *C, *z;
+  const float *A, *D, *bias;
+  const int32_t *slot_map;
+  float *state;
+  void *out;
+  long long sx[2], sdt[2], sB[2], sC[2], sz[2], so[2], ss[2];
+};
+cudaError_t launch_head_update(int dtype, const HeadUpdateParams &p, cudaStream_t s);
+
+struct HeadScanParams {
+  int heads, headdim, dstate, hpg;
+  int softplus, dt_f32;
+  int split;  // a request may have several blocks: ws holds their summaries
+  long long slots;
+  const void *x, *dt, *B, *C, *z;
+  const float *A, *D, *bias;
+  float *state;
+  void *out;
+  long long sx[2], sdt[2], sB[2], sC[2], sz[2], so[2], ss[2];
+  // Summaries (split): per block of the table and head, the state it ends in
+  // from zero (the request's first block: from its start state), headdim x
+  // dstate, and the logarithm of its whole decay. The entry of a request's last
+  // block, whose end nothing continues, keeps the request's start state.
+  float *ws_state, *ws_decay;
+  int32_t *err;
+  Tables t;
+};
+cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s);
+
+}  // namespace ssk

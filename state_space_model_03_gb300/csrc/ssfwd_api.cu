@@ -1423,6 +1423,14 @@ int launch_cx(const ss_fwd_complex_params *p, cudaStream_t stream) {
 
 }  // namespace
 
+namespace ssk {
+// The error word of the current device, for the packed operators' launches.
+int32_t *packed_error_word() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? error_word_ptr(dev) : nullptr;
+}
+}  // namespace ssk
+
 extern "C" {
 
 int ss_abi_version(void) { return SS_ABI_VERSION; }
