@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libssfwd.so")
 SOURCES = ["ssfwd_api.cu", "ss_fwd_f32.cu", "ss_fwd_f16.cu", "ss_fwd_bf16.cu", "ss_fwd_lane.cu", "ss_state_update.cu", "ss_conv1d.cu", "ss_bwd.cu", "ss_fwd_complex.cu",
-           "ss_packed_api.cu", "ss_packed_tables.cu", "ss_packed_conv1d.cu", "ss_head_update.cu", "ss_head_scan.cu"]
+           "ss_packed_api.cu", "ss_packed_tables.cu", "ss_packed_conv1d.cu", "ss_head_update.cu", "ss_head_scan.cu",
+           "ss_head_scan_tc.cu"]
 HEADERS = ["ss_dispatch.h", "ss_fwd_kernel.cuh", "ss_fwd_instances.cuh", "ss_packed.h"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-lineinfo",

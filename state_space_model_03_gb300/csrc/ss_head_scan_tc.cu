@@ -1,0 +1,770 @@
+// Selective scan with one decay per head over packed requests, 16-bit operands,
+// on the tensor cores (include/ssfwd_packed.h; ss_head_scan.cu has the form for
+// every type and size).
+//
+// Mathematics. With a_t = dt_t A and L_t its running sum, inside a chunk of 128
+// tokens of one request that starts with state S (headdim x dstate):
+//   Y   = (C B^T * M) X + e^L (C S^T),   M[t,s] = e^(L_t - L_s) dt_s for s <= t, else 0
+//   S'  = e^(L_end) S + (w X)^T B,       w_s = e^(L_end - L_s) dt_s
+// so a chunk is four products of 128-row matrices, and only S goes from chunk to
+// chunk. Exponents are never split so that a factor can exceed 1: M takes the
+// exponential of a difference inside its diagonal blocks of 32, and elsewhere
+// the product of (row: since the end of the column's block) and (column: to the
+// end of its block), each a sum of terms of one sign.
+//
+// One CTA carries 128 (head, p) columns, two heads of 64 or one of 128, through
+// one block of a request. C B^T and the operands C and B are shared by its heads.
+//   warp 8       loads the chunks by TMA (boxes of 128 tokens x 64 values)
+//   warp 9       issues the products (tcgen05, accumulators in tensor memory)
+//   warps 0 - 7  scale: C B^T to its masked form, X to w X, S to the next chunk's
+//                start, and finish the output. Thread = row t for the first and
+//                the last (one warpgroup per 64 columns), thread = column p for
+//                the others.
+// Tensor memory, 512 columns: C B^T, overlaid by the masked form as the product's
+// A operand (128); Y (128); S (128); w X as A operand (128).
+//
+// Rounding. C B^T takes the stored B and C; its masked form and the S that C
+// multiplies are rounded to 16 bits, about what rounding the output costs. S
+// itself stays in fp32 from chunk to chunk: w X enters in three bf16 terms (24
+// bits, exact) or two fp16 terms (22 bits, w scaled by a power of two per chunk
+// and head so that the smaller one does not underflow).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "ss_fwd_kernel.cuh"
+#include "ss_packed.h"
+
+namespace ssk {
+namespace {
+
+constexpr int kBox = 16384;      // 128 rows of 128 bytes
+constexpr int kRing = 10;        // boxes in flight; even, so that a pair is adjacent
+constexpr int kTcThreads = 320;  // 8 scaling warps, TMA warp, MMA warp
+constexpr uint32_t kColG = 0, kColY = 128, kColS = 256, kColX = 384;
+constexpr int32_t kErrTcWait = 16;
+
+struct TcMaps {
+  CUtensorMap x, B, C, z;
+};
+
+struct Shared {
+  uint64_t full[kRing], empty[kRing];
+  uint64_t xw0, xw0_done, masked, y_done, xw1, s_done, s_ready, gy_done;
+  uint32_t tmem;
+  int dead;
+  float tot[2][4];           // log2 decay of each 32 tokens
+  float top[2][4];           // largest |w| of each 32 tokens (fp16)
+  alignas(16) float2 ldt[2][128];        // (log2 decay since the start of the 32, dt)
+  alignas(16) float colf[2][128];        // dt times the decay to the end of the 32
+  alignas(16) float w[2][128];           // dt times the decay to the end of the chunk
+};
+
+__device__ __forceinline__ bool wait_tc(uint64_t *bar, uint32_t parity, volatile int *dead, int32_t *err) {
+  for (uint32_t i = 0; i < kMaxWaitIters; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*dead) return false;
+  }
+  *dead = 1;
+  atomicCAS(err, 0, kErrTcWait);
+  return false;
+}
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);  // 128-byte swizzle
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of the warp's 32 lanes (thread = lane); the load is complete on return.
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+      "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
+      "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Barrier of the 8 scaling warps.
+__device__ __forceinline__ void sync_scalers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// One arrival per warp, after all its lanes.
+__device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Two fp32 values as 16-bit terms of decreasing size, packed: hi + mid (+ lo).
+template <typename T> struct Terms;
+template <> struct Terms<__nv_bfloat16> {
+  static constexpr int N = 3;  // by truncation, 8 bits each
+  static __device__ __forceinline__ void split(float2 v, uint32_t (&t)[3]) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      t[k] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+      v.x -= __uint_as_float(__float_as_uint(v.x) & 0xffff0000u);
+      v.y -= __uint_as_float(__float_as_uint(v.y) & 0xffff0000u);
+    }
+  }
+};
+template <> struct Terms<__half> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void split(float2 v, uint32_t (&t)[2]) {
+    t[0] = pack2<__half>(v.x, v.y);
+    const float2 h = unpack2<__half>(t[0]);
+    t[1] = pack2<__half>(v.x - h.x, v.y - h.y);
+  }
+};
+
+// PW: columns of a head in the tile (64: two heads, 128: one). NS: padded dstate.
+template <typename T, int PW, int NS, bool SUMMARY, bool GATE>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    ss_head_scan_tc_kernel(const __grid_constant__ HeadScanParams p, const __grid_constant__ TcMaps maps) {
+  constexpr int HT = 128 / PW;
+  constexpr int NB = NS / 64;                           // boxes of B (and of C)
+  constexpr int oC = 0, oB = SUMMARY ? 0 : NB, oX = oB + NB, oZ = oX + 2;
+  constexpr int BPC = GATE ? oZ + 2 : oZ;               // ring places per chunk
+  constexpr int NT = Terms<T>::N;
+  constexpr int NH = NS / 2;                            // states per thread of a column
+  // a product reads two boxes as one operand: such pairs start on an even place
+  static_assert(SUMMARY ? NB == 1 || BPC % 2 == 0 : BPC % 2 == 0 && oX % 2 == 0, "pairs of boxes are adjacent");
+  extern __shared__ unsigned char raw[];
+  unsigned char *ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  unsigned char *s16 = ring + kRing * kBox;             // S in 16 bits: [NB][128 p][64 n], swizzled
+  Shared &sh = *reinterpret_cast<Shared *>(s16 + NB * kBox);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tpg = (p.hpg + HT - 1) / HT;                // tiles per group
+  const int tiles = p.heads / p.hpg * tpg;
+  const int tile = blockIdx.x % tiles, blk = blockIdx.x / tiles;
+  const int grp = tile / tpg, h0 = grp * p.hpg + (tile % tpg) * HT;
+  const int hend = (grp + 1) * p.hpg;                   // heads of the group end here
+  T *out = static_cast<T *>(p.out);
+  if (blk == p.t.max_blocks) {                          // past the last token: zeros
+    if (!SUMMARY) {
+      const int cols = min(HT, hend - h0) * p.headdim;
+      for (int t = p.t.counts[0] + warp; t < p.t.tokens; t += kTcThreads / 32)
+        for (int i = lane; i < cols; i += 32)
+          out[t * p.so[0] + (h0 + i / p.headdim) * p.so[1] + i % p.headdim] = from_f<T>(0.f);
+    }
+    return;
+  }
+  const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blk];
+  const int r = row.x, first = row.y, size = row.z, index = row.w;
+  if (r < 0) return;
+  const int len = p.t.offsets[r + 1] - p.t.offsets[r];
+  const int last = (len - 1) / p.t.block;
+  if (SUMMARY && last == 0) return;
+  const int slot = p.state ? p.t.slot_map[r] : -1;
+  const bool kept = slot >= 0 && slot < p.slots;
+  const bool goes_on = kept && p.t.context && p.t.context[r] > 0;
+
+  // thread = column: its head, row of the state and half of the states
+  const int wg = (warp >> 2) & 1, wq = warp & 3;
+  const int pc = wq * 32 + lane, hs = HT == 2 ? pc >> 6 : 0, pp = HT == 2 ? pc & 63 : pc;
+  const bool pin = warp < 8 && h0 + hs < hend && pp < p.headdim;
+  const int n0 = wg * NH, nv = min(max(p.dstate - n0, 0), NH);  // a multiple of 8
+  const long long pn = (long long)p.headdim * p.dstate;
+  float *cache = kept ? p.state + slot * p.ss[0] + (h0 + hs) * p.ss[1] + (long long)pp * p.dstate + n0 : nullptr;
+  auto entry = [&](int i) {
+    return p.ws_state + ((long long)(blk - index + i) * p.heads + h0 + hs) * pn + (long long)pp * p.dstate + n0;
+  };
+  auto decay_of = [&](int i) { return p.ws_decay + (long long)(blk - index + i) * p.heads + h0 + hs; };
+
+  if (SUMMARY && index == last) {  // keeps the start, which the cache loses when the last block ends
+    if (goes_on && pin)
+      for (int n = 0; n < nv; n += 4) *reinterpret_cast<float4 *>(entry(last) + n) = *reinterpret_cast<const float4 *>(cache + n);
+    return;
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.xw0, 8);
+    mbar_init(&sh.xw1, 8);
+    mbar_init(&sh.masked, 8);
+    mbar_init(&sh.s_ready, 8);
+    mbar_init(&sh.xw0_done, 1);
+    mbar_init(&sh.y_done, 1);
+    mbar_init(&sh.s_done, 1);
+    mbar_init(&sh.gy_done, 1);
+    sh.dead = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = sh.tmem;
+  volatile int *dead = &sh.dead;
+  const int chunks = (size + 127) / 128;
+  auto box = [&](int c, int o) { return ring + ((c * BPC + o) % kRing) * kBox; };
+
+  if (warp == 8) {
+    // ---- TMA ----
+    if (lane == 0) {
+      int issued = 0;
+      for (int c = 0; c < chunks && !*dead; ++c) {
+        const int t = first + c * 128;
+        for (int o = 0; o < BPC; ++o) {
+          const int i = c * BPC + o, place = i % kRing, use = i / kRing;
+          if (use > 0 && !wait_tc(&sh.empty[place], (use - 1) & 1, dead, p.err)) break;
+          unsigned char *dst = ring + place * kBox;
+          mbar_arrive_expect_tx(&sh.full[place], kBox);
+          issued = i + 1;
+          if (o >= oX) {
+            const int k = (o - oX) & 1;
+            const CUtensorMap *m = o >= oZ ? &maps.z : &maps.x;
+            tma_load_3d(dst, m, &sh.full[place], HT == 2 ? 0 : 64 * k, HT == 2 ? h0 + k : h0, t);
+          } else if (o >= oB) {
+            tma_load_3d(dst, &maps.B, &sh.full[place], 64 * (o - oB), grp, t);
+          } else {
+            tma_load_3d(dst, &maps.C, &sh.full[place], 64 * (o - oC), grp, t);
+          }
+        }
+      }
+      // nothing of this block's copies is left in flight, whatever became of the rest
+      for (int i = max(0, issued - kRing); i < issued; ++i) {
+        const uint32_t parity = (i / kRing) & 1;
+        for (uint32_t k = 0; k < kMaxWaitIters; ++k)
+          if (mbar_try_wait(&sh.full[i % kRing], parity)) break;
+      }
+    }
+  } else if (warp == 9) {
+    // ---- products ----
+    if (lane == 0) {
+      constexpr uint32_t ty = sizeof(T) == 2 && NT == 3 ? 1u : 0u;  // bf16 : fp16
+      constexpr uint32_t base = (1u << 4) | (ty << 7) | (ty << 10) | (8u << 24);
+      constexpr uint32_t id_g = base | (128u / 8 << 17);                             // C B^T and C S^T: both K-major, N = 128
+      constexpr uint32_t id_y = base | (1u << 16) | ((uint32_t)PW / 8 << 17);        // masked x X: X is N-major
+      constexpr uint32_t id_s = base | (1u << 16) | ((uint32_t)NS / 8 << 17);        // w X x B: B is N-major
+      const uint32_t s16a = smem_u32(s16);
+      auto full = [&](int c, int o) {
+        const int i = c * BPC + o;
+        wait_tc(&sh.full[i % kRing], (i / kRing) & 1, dead, p.err);
+      };
+      auto gain = [&](int c, int round) {  // two quarters of 32 tokens into S
+        const uint32_t b = smem_u32(box(c, oB));
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < NT; ++e)
+              mma_ts(tm + kColS, tm + kColX + 64 * q + 16 * e + 8 * k,
+                     smem_desc(b + (round * 64 + q * 32 + k * 16) * 128, kBox, 1024), id_s, true);
+      };
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t ph = c & 1;
+        for (int o = 0; o < NB; ++o) full(c, oB + o);
+        if (!SUMMARY) {
+          for (int o = 0; o < NB; ++o) full(c, oC + o);
+          if (c > 0) wait_tc(&sh.y_done, ph ^ 1, dead, p.err);  // the masked form's columns are free again
+          fence_after();
+          const uint32_t ca = smem_u32(box(c, oC)), ba = smem_u32(box(c, oB));
+          if (!*dead) {
+#pragma unroll
+            for (int k = 0; k < NS / 16; ++k) {
+              const uint32_t at = (k / 4) * kBox + (k % 4) * 32;
+              mma_ss(tm + kColG, smem_desc(ca + at, 16, 1024), smem_desc(ba + at, 16, 1024), id_g, k > 0);
+            }
+          }
+          wait_tc(&sh.s_ready, ph, dead, p.err);
+          fence_after();
+          if (!*dead) {
+#pragma unroll
+            for (int k = 0; k < NS / 16; ++k) {
+              const uint32_t at = (k / 4) * kBox + (k % 4) * 32;
+              mma_ss(tm + kColY, smem_desc(ca + at, 16, 1024), smem_desc(s16a + at, 16, 1024), id_g, k > 0);
+            }
+            commit(&sh.gy_done);
+          }
+        } else {
+          wait_tc(&sh.s_ready, ph, dead, p.err);
+        }
+        wait_tc(&sh.xw0, ph, dead, p.err);
+        fence_after();
+        if (!*dead) {
+          gain(c, 0);
+          commit(&sh.xw0_done);
+        }
+        if (!SUMMARY) {
+          full(c, oX);
+          full(c, oX + 1);
+          wait_tc(&sh.masked, ph, dead, p.err);
+          fence_after();
+          if (!*dead) {
+            for (int h = 0; h < HT; ++h) {
+              const uint32_t xa = smem_u32(box(c, oX + h));
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_ts(tm + kColY + 64 * h, tm + kColG + 64 * h + 8 * k, smem_desc(xa + k * 2048, kBox, 1024), id_y, true);
+            }
+            commit(&sh.y_done);
+          }
+        }
+        wait_tc(&sh.xw1, ph, dead, p.err);
+        fence_after();
+        if (!*dead) {
+          gain(c, 1);
+          commit(&sh.s_done);
+        }
+      }
+    }
+  } else {
+    // ---- scaling warps ----
+    const int hr = HT == 2 ? wg : 0;                    // thread = row: its head
+    const bool hin = h0 + hr < hend;
+    const int hh = hin ? h0 + hr : h0;
+    const float A2 = p.A[hh] * kLog2e, bias = p.bias ? p.bias[hh] : 0.f, skip = p.D ? p.D[hh] : 0.f;
+    const int trow = wq * 32 + lane;
+    const uint32_t lane_at = (uint32_t)(wq * 32) << 16;
+    const long long dt_at = hh * p.sdt[1];
+    auto load_dt = [&](int c) -> float {
+      const int t = c * 128 + trow;
+      if (t >= size) return 0.f;
+      const long long at = (long long)(first + t) * p.sdt[0] + dt_at;
+      return p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]);
+    };
+    float l = 0.f, since = 0.f;       // log2 decay since the start of the 32 tokens, of the chunk
+    float decay = 0.f, scale = 1.f;   // of this column's head: log2 decay so far; w's scale in this chunk
+    // dt and the decays of chunk c
+    auto prepare = [&](int c, float raw_dt) {
+      float dt = raw_dt + bias;
+      if (p.softplus) dt = softplus_f(dt);
+      if (c * 128 + trow >= size) dt = 0.f;
+      const float a = dt * A2;
+      l = a;
+      float to_end = a;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float up = __shfl_up_sync(0xffffffffu, l, o), dn = __shfl_down_sync(0xffffffffu, to_end, o);
+        if (lane >= o) l += up;
+        if (lane + o < 32) to_end += dn;
+      }
+      if (lane == 31) sh.tot[wg][wq] = l;
+      // what follows this token, without the token itself
+      const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
+      to_end = lane < 31 ? nx : 0.f;
+      sync_scalers();
+      float before = 0.f, after = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float t = sh.tot[wg][k];
+        if (k < wq) before += t;
+        if (k > wq) after += t;
+      }
+      since = before + l;
+      const float w = dt * ex2(to_end + after);
+      sh.ldt[wg][trow] = make_float2(l, dt);
+      sh.colf[wg][trow] = dt * ex2(to_end);
+      sh.w[wg][trow] = w;
+      if (NT == 2) {
+        float m = fabsf(w);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) sh.top[wg][wq] = m;
+      }
+      sync_scalers();
+    };
+    auto total = [&]() { return (sh.tot[hs][0] + sh.tot[hs][1]) + (sh.tot[hs][2] + sh.tot[hs][3]); };
+    // power of two that brings this chunk's largest w to [1/2, 1)
+    auto w_scale = [&]() -> float {
+      if (NT != 2) return 1.f;
+      const float m = fmaxf(fmaxf(sh.top[hs][0], sh.top[hs][1]), fmaxf(sh.top[hs][2], sh.top[hs][3]));
+      const int e = (int)(__float_as_uint(m) >> 23);
+      return e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
+    };
+    // S (in v, true values): its 16-bit form for the next chunk's product, and its
+    // decayed, scaled form as the accumulator
+    auto hand_on = [&](float (&v)[NH]) {
+      const float t = total();
+      decay += t;
+      scale = w_scale();
+      const float keep = ex2(t) * scale;
+      if (!SUMMARY) {
+#pragma unroll
+        for (int q = 0; q < NH / 8; ++q) {
+          const int n = n0 + 8 * q;  // a 16-byte piece of the row
+          uint4 w4;
+          w4.x = pack2<T>(v[8 * q], v[8 * q + 1]);
+          w4.y = pack2<T>(v[8 * q + 2], v[8 * q + 3]);
+          w4.z = pack2<T>(v[8 * q + 4], v[8 * q + 5]);
+          w4.w = pack2<T>(v[8 * q + 6], v[8 * q + 7]);
+          *reinterpret_cast<uint4 *>(s16 + (n / 64) * kBox + swz(pc, (n % 64) * 2)) = w4;
+        }
+        fence_proxy_async();
+      }
+#pragma unroll
+      for (int q = 0; q < NH / 32; ++q) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[32 * q + i] * keep);
+        tm_st32(tm + lane_at + kColS + n0 + 32 * q, w);
+      }
+      wait_st();
+      fence_before();
+      arrive_warp(&sh.s_ready, lane);
+    };
+
+    float raw_dt = load_dt(0);
+    {
+      float v[NH];
+#pragma unroll
+      for (int i = 0; i < NH; ++i) v[i] = 0.f;
+      auto fold = [&](const float *src, float keep) {
+#pragma unroll
+        for (int n = 0; n < NH; n += 4)
+          if (n < nv) {
+            const float4 q = *reinterpret_cast<const float4 *>(src + n);
+            v[n] = fmaf(keep, v[n], q.x);
+            v[n + 1] = fmaf(keep, v[n + 1], q.y);
+            v[n + 2] = fmaf(keep, v[n + 2], q.z);
+            v[n + 3] = fmaf(keep, v[n + 3], q.w);
+          }
+      };
+      if (pin) {
+        if (index == 0) {
+          if (goes_on) fold(!SUMMARY && last > 0 ? entry(last) : cache, 0.f);
+        } else if (!SUMMARY) {
+          fold(entry(0), 0.f);
+          for (int i = 1; i < index; ++i) fold(entry(i), ex2(*decay_of(i)));
+        }
+      }
+      prepare(0, raw_dt);
+      hand_on(v);
+    }
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = c & 1;
+      const int valid = min(128, size - c * 128);
+      raw_dt = load_dt(c + 1);
+      auto full = [&](int o) {
+        const int i = c * BPC + o;
+        wait_tc(&sh.full[i % kRing], (i / kRing) & 1, dead, p.err);
+      };
+      full(oX);
+      full(oX + 1);
+      if (valid < 128) {  // rows of the next request, or of nothing: 0 x anything must be 0
+        for (int o = 0; o < NB; ++o) full(oB + o);
+        const int todo = (128 - valid) * 8;
+        for (int i = tid; i < todo * (2 + NB); i += 256) {
+          const int o = i / todo, k = i % todo;
+          unsigned char *b = o < 2 ? box(c, oX + o) : box(c, oB + o - 2);
+          *reinterpret_cast<uint4 *>(b + (valid + k / 8) * 128 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        sync_scalers();
+      }
+      // w X of 32 tokens as the product's A operand: thread = column
+      auto weigh = [&](int round) {
+        const int s0 = round * 64 + wg * 32;
+        const unsigned char *col = box(c, oX + (pc >> 6)) + (pc & 7) * 2;
+        const int piece = (pc & 63) >> 3;
+        uint32_t t[NT][16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float4 w = *reinterpret_cast<const float4 *>(&sh.w[hs][s0 + i]);
+          if (NT == 2) { w.x *= scale; w.y *= scale; w.z *= scale; w.w *= scale; }
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int s = s0 + i + k;
+            x[k] = to_f<T>(*reinterpret_cast<const T *>(col + s * 128 + ((piece ^ (s & 7)) << 4)));
+          }
+          uint32_t a[NT], b[NT];
+          Terms<T>::split(make_float2(x[0] * w.x, x[1] * w.y), a);
+          Terms<T>::split(make_float2(x[2] * w.z, x[3] * w.w), b);
+#pragma unroll
+          for (int e = 0; e < NT; ++e) {
+            t[e][i / 2] = a[e];
+            t[e][i / 2 + 1] = b[e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < NT; ++e) tm_st16(tm + lane_at + kColX + 64 * wg + 16 * e, t[e]);
+        wait_st();
+        fence_before();
+        arrive_warp(round ? &sh.xw1 : &sh.xw0, lane);
+      };
+      weigh(0);
+
+      if (!SUMMARY) {
+        // the masked form of C B^T, and Y = e^L (C S^T): thread = row
+        wait_tc(&sh.gy_done, ph, dead, p.err);
+        fence_after();
+        const float2 *ldt = sh.ldt[wg];
+        const float *colf = sh.colf[wg];
+        auto masked_block = [&](int j, uint32_t (&m)[16]) {  // columns 32 j .. 32 j + 31
+          if (j > wq) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m[i] = 0;
+            return;
+          }
+          uint32_t g[32];
+          tm_ld32(tm + lane_at + kColG + 32 * j, g);
+          if (j < wq) {
+            float e = l;
+            for (int k = j + 1; k < wq; ++k) e += sh.tot[wg][k];
+            const f2 rf = pk(ex2(e), ex2(e));
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 cf = *reinterpret_cast<const float4 *>(colf + 32 * j + i);
+              const float2 a = upk(mul2(mul2(pk(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), rf), pk(cf.x, cf.y)));
+              const float2 b = upk(mul2(mul2(pk(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3])), rf), pk(cf.z, cf.w)));
+              m[i / 2] = pack2<T>(a.x, a.y);
+              m[i / 2 + 1] = pack2<T>(b.x, b.y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float4 q = *reinterpret_cast<const float4 *>(ldt + 32 * j + i);  // (l, dt) of two tokens
+              const float a = __uint_as_float(g[i]) * (ex2(l - q.x) * q.y), b = __uint_as_float(g[i + 1]) * (ex2(l - q.z) * q.w);
+              m[i / 2] = pack2<T>(i <= lane ? a : 0.f, i + 1 <= lane ? b : 0.f);
+            }
+          }
+        };
+        const float e = ex2(since);
+        auto scale_y = [&]() {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t y[32];
+            const uint32_t at = tm + lane_at + kColY + 64 * wg + 32 * q;
+            tm_ld32(at, y);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * e);
+            tm_st32(at, y);
+          }
+        };
+        if constexpr (HT == 2) {
+          uint32_t m[4][16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) masked_block(j, m[j]);
+          fence_before();
+          sync_scalers();  // all of C B^T is read before any of it is overlaid
+          fence_after();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tm_st16(tm + lane_at + kColG + 64 * wg + 16 * j, m[j]);
+        } else {
+          const int j0 = wg, j1 = 3 - wg;  // blocks 0 and 3, or 1 and 2: equal work below the diagonal
+          uint32_t m[2][16];
+          masked_block(j0, m[0]);
+          masked_block(j1, m[1]);
+          fence_before();
+          sync_scalers();
+          fence_after();
+          tm_st16(tm + lane_at + kColG + 16 * j0, m[0]);
+          tm_st16(tm + lane_at + kColG + 16 * j1, m[1]);
+        }
+        scale_y();
+        wait_st();
+        fence_before();
+        arrive_warp(&sh.masked, lane);
+      }
+
+      wait_tc(&sh.xw0_done, ph, dead, p.err);
+      fence_after();
+      weigh(1);
+      sync_scalers();  // X is read by columns no more: its rows become the output's
+
+      if (!SUMMARY) {
+        if (GATE) {
+          full(oZ);
+          full(oZ + 1);
+        }
+        wait_tc(&sh.y_done, ph, dead, p.err);
+        fence_after();
+        unsigned char *xr = box(c, oX + wg);
+        const unsigned char *zr = box(c, oZ + wg);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t y[32];
+          tm_ld32(tm + lane_at + kColY + 64 * wg + 32 * q, y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int at = swz(trow, 64 * q + 16 * k);
+            const uint4 xq = *reinterpret_cast<const uint4 *>(xr + at);
+            const uint32_t xw[4] = {xq.x, xq.y, xq.z, xq.w};
+            uint4 zq = make_uint4(0, 0, 0, 0);
+            if (GATE) zq = *reinterpret_cast<const uint4 *>(zr + at);
+            const uint32_t zw[4] = {zq.x, zq.y, zq.z, zq.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 xv = unpack2<T>(xw[i]);
+              float a = fmaf(skip, xv.x, __uint_as_float(y[8 * k + 2 * i])), b = fmaf(skip, xv.y, __uint_as_float(y[8 * k + 2 * i + 1]));
+              if (GATE) {
+                const float2 zv = unpack2<T>(zw[i]);
+                a *= silu_f(zv.x);
+                b *= silu_f(zv.y);
+              }
+              o[i] = pack2<T>(a, b);
+            }
+            *reinterpret_cast<uint4 *>(xr + at) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        __syncwarp();
+        // the warp's 32 rows leave as whole 128-byte lines
+        if (hin && !*dead) {
+          const int piece = lane & 7, col = (HT == 2 ? 0 : 64 * wg) + 8 * piece;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int t = wq * 32 + i * 4 + (lane >> 3);
+            if (t < valid && col < p.headdim)
+              *reinterpret_cast<uint4 *>(out + (long long)(first + c * 128 + t) * p.so[0] + hh * p.so[1] + col) =
+                  *reinterpret_cast<const uint4 *>(xr + swz(t, 16 * piece));
+          }
+        }
+        fence_before();
+        fence_proxy_async();  // before the next copy into these boxes
+      }
+      const bool more = c + 1 < chunks;
+      const float unscale = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / scale, a power of two
+      if (more) prepare(c + 1, raw_dt);
+      else sync_scalers();
+      wait_tc(&sh.s_done, ph, dead, p.err);
+      fence_after();
+      if (tid == 0)
+        for (int o = 0; o < BPC; ++o) mbar_arrive(&sh.empty[(c * BPC + o) % kRing]);
+      float v[NH];
+#pragma unroll
+      for (int q = 0; q < NH / 32; ++q) {
+        uint32_t s[32];
+        tm_ld32(tm + lane_at + kColS + n0 + 32 * q, s);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[32 * q + i] = NT == 2 ? __uint_as_float(s[i]) * unscale : __uint_as_float(s[i]);
+      }
+      if (more) {
+        hand_on(v);
+      } else if (pin && !*dead && (SUMMARY || (index == last && kept))) {
+        float *dst = SUMMARY ? entry(index) : cache;
+#pragma unroll
+        for (int n = 0; n < NH; n += 4)
+          if (n < nv) *reinterpret_cast<float4 *>(dst + n) = make_float4(v[n], v[n + 1], v[n + 2], v[n + 3]);
+        if (SUMMARY && pp == 0 && wg == 0) *decay_of(index) = decay;
+      }
+    }
+    fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+  }
+}
+
+template <typename T, int PW, int NS, bool GATE>
+cudaError_t go(const HeadScanParams &p, const TcMaps &maps, cudaStream_t s) {
+  constexpr int smem = kRing * kBox + NS / 64 * kBox + (int)sizeof(Shared) + 1024;
+  const int ht = 128 / PW;
+  const long long tiles = (long long)(p.heads / p.hpg) * ((p.hpg + ht - 1) / ht);
+  const long long ctas = tiles * (p.t.max_blocks + 1);
+  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  auto sum = ss_head_scan_tc_kernel<T, PW, NS, true, false>;
+  auto fwd = ss_head_scan_tc_kernel<T, PW, NS, false, GATE>;
+  static bool set[64] = {};  // the attribute is per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !set[dev]) {
+    e = cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev] = true;
+  }
+  if (p.split) sum<<<(unsigned)ctas, kTcThreads, smem, s>>>(p, maps);
+  fwd<<<(unsigned)ctas, kTcThreads, smem, s>>>(p, maps);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t by_size(const HeadScanParams &p, const TcMaps &m, cudaStream_t s) {
+  if (p.headdim <= 64) {
+    if (p.dstate <= 64) return p.z ? go<T, 64, 64, true>(p, m, s) : go<T, 64, 64, false>(p, m, s);
+    return p.z ? go<T, 64, 128, true>(p, m, s) : go<T, 64, 128, false>(p, m, s);
+  }
+  if (p.dstate <= 64) return p.z ? go<T, 128, 64, true>(p, m, s) : go<T, 128, 64, false>(p, m, s);
+  return p.z ? go<T, 128, 128, true>(p, m, s) : go<T, 128, 128, false>(p, m, s);
+}
+
+bool map3(TensorMapEncode enc, CUtensorMap *m, const void *base, int width, int rows, int tokens, const long long *st) {
+  // (width, rows, tokens); a dimension of one element may have any stride
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {rows > 1 ? (cuuint64_t)st[1] * 2 : 16, tokens > 1 ? (cuuint64_t)st[0] * 2 : 16};
+  const cuuint32_t bx[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(enc)(
+             m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, bx, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// Whether the operands suit the tensor-core form: 16-bit, TMA's alignments, and
+// sizes that its tiles hold.
+bool head_scan_tc_fits(int dtype, const HeadScanParams &p) {
+  if (dtype == 0 || p.headdim > 128 || p.dstate > 128 || p.headdim % 8 || p.dstate % 8) return false;
+  auto rows = [&](const void *base, const long long *st, int n) {
+    if (!base) return true;
+    const bool a = reinterpret_cast<uintptr_t>(base) % 16 == 0;
+    return a && (n == 1 || (st[1] % 8 == 0 && st[1] > 0)) && (p.t.tokens == 1 || (st[0] % 8 == 0 && st[0] > 0));
+  };
+  const int groups = p.heads / p.hpg;
+  return rows(p.x, p.sx, p.heads) && rows(p.z, p.sz, p.heads) && rows(p.out, p.so, p.heads) && rows(p.B, p.sB, groups) &&
+         rows(p.C, p.sC, groups) &&
+         (!p.state || (reinterpret_cast<uintptr_t>(p.state) % 16 == 0 && (p.heads == 1 || p.ss[1] % 4 == 0) &&
+                       (p.slots <= 1 || p.ss[0] % 4 == 0)));
+}
+
+cudaError_t launch_head_scan_tc(int dtype, const HeadScanParams &p, TensorMapEncode enc, cudaStream_t s) {
+  TcMaps m;
+  const int groups = p.heads / p.hpg;
+  if (!map3(enc, &m.x, p.x, p.headdim, p.heads, p.t.tokens, p.sx) || !map3(enc, &m.B, p.B, p.dstate, groups, p.t.tokens, p.sB) ||
+      !map3(enc, &m.C, p.C, p.dstate, groups, p.t.tokens, p.sC) ||
+      !map3(enc, &m.z, p.z ? p.z : p.x, p.headdim, p.heads, p.t.tokens, p.z ? p.sz : p.sx))
+    return cudaErrorInvalidValue;
+  return dtype == 1 ? by_size<__half>(p, m, s) : by_size<__nv_bfloat16>(p, m, s);
+}
+
+}  // namespace ssk

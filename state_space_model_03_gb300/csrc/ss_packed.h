@@ -74,4 +74,10 @@ struct HeadScanParams {
 };
 cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s);
 
+// The same on the tensor cores, for 16-bit operands that TMA can describe.
+typedef void *TensorMapEncode;  // the driver's cuTensorMapEncodeTiled
+TensorMapEncode packed_map_encode();
+bool head_scan_tc_fits(int dtype, const HeadScanParams &p);
+cudaError_t launch_head_scan_tc(int dtype, const HeadScanParams &p, TensorMapEncode enc, cudaStream_t s);
+
 }  // namespace ssk

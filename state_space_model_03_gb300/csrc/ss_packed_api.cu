@@ -342,6 +342,11 @@ int ss_head_scan(const ss_head_scan_params *p, void *stream) {
   k.err = ssk::packed_error_word();
   if (!k.err) return SS_ERR_CUDA;
   k.t = tables_of(p->tables);
+  if (ssk::head_scan_tc_fits(p->dtype, k)) {
+    const ssk::TensorMapEncode enc = ssk::packed_map_encode();
+    if (!enc) return SS_ERR_CUDA;
+    return launched(ssk::launch_head_scan_tc(p->dtype, k, enc, static_cast<cudaStream_t>(stream)));
+  }
   return launched(ssk::launch_head_scan(p->dtype, k, static_cast<cudaStream_t>(stream)));
 }
 

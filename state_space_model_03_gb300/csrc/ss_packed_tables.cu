@@ -58,10 +58,10 @@ __global__ void __launch_bounds__(kThreads) ss_request_tables_kernel(const __gri
 
   // offsets, cut at the number of tokens; lengths are added in 64 bits
   long long mine = 0, total;
-  int errors = 0;
+  int negative = 0;
   for (int r = r0; r < r1; ++r) {
     const int n = p.lengths[r];
-    errors |= n < 0 ? 2 : 0;
+    negative |= n < 0;
     mine += max(n, 0);
   }
   long long run = block_exclusive(mine, sums, total);
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) ss_request_tables_kernel(const __gri
     run += max(p.lengths[r], 0);
   }
   if (tid == 0) off[p.requests] = (int)min(total, (long long)p.tokens);
-  errors |= total > p.tokens ? 1 : 0;
+  int errors = total > p.tokens ? 1 : 0;
   __syncthreads();
   // first block of each request (low half), requests that need a slot (high half)
   mine = 0;
@@ -99,14 +99,14 @@ __global__ void __launch_bounds__(kThreads) ss_request_tables_kernel(const __gri
     }
   }
   if (wanted > p.free || (wanted > 0 && !p.free_slots)) errors |= 4;
-  const int any = __syncthreads_or(errors);
+  if (__syncthreads_or(negative)) errors |= 2;
   const int live = off[p.requests];
   if (blockIdx.x == 0 && tid == 0) {
     p.offsets[p.requests] = live;
     p.counts[0] = live;
     p.counts[1] = nblocks;
     p.counts[2] = min(wanted, p.free_slots ? p.free : 0);
-    p.counts[3] = any;
+    p.counts[3] = errors;
   }
 
   const int step = gridDim.x * kThreads;

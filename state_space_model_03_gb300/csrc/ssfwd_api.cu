@@ -13,6 +13,7 @@
 
 #include "ss_dispatch.h"
 #include "ss_fwd_kernel.cuh"
+#include "ss_packed.h"
 #include "ssfwd.h"
 
 namespace {
@@ -1428,6 +1429,10 @@ namespace ssk {
 int32_t *packed_error_word() {
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess ? error_word_ptr(dev) : nullptr;
+}
+TensorMapEncode packed_map_encode() {
+  std::call_once(g_encode_once, load_encode);
+  return reinterpret_cast<TensorMapEncode>(g_encode);
 }
 }  // namespace ssk
 
