@@ -14,14 +14,16 @@
 //
 // One CTA carries 128 (head, p) columns, two heads of 64 or one of 128, through
 // one block of a request. C B^T and the operands C and B are shared by its heads.
-//   warp 8       loads the chunks by TMA (boxes of 128 tokens x 64 values)
-//   warp 9       issues the products (tcgen05, accumulators in tensor memory)
-//   warps 0 - 7  scale: C B^T to its masked form, X to w X, S to the next chunk's
-//                start, and finish the output. Thread = row t for the first and
-//                the last (one warpgroup per 64 columns), thread = column p for
-//                the others.
-// Tensor memory, 512 columns: C B^T, overlaid by the masked form as the product's
-// A operand (128); Y (128); S (128); w X as A operand (128).
+//   warps 0 - 7   mask: C B^T to its masked form, C S^T by e^L (thread = row t),
+//                 and the decays of the next chunk
+//   warps 8 - 15  weigh: X to w X, S to the next chunk's start (thread = column p),
+//                 then finish the output (thread = row t)
+//   warp 16       loads the chunks by TMA (boxes of 128 tokens x 64 values)
+//   warp 17       issues the products for Y, warp 18 those for S (tcgen05,
+//                 accumulators in tensor memory)
+// The masking warps run on chunk c+1 while the weighing warps finish chunk c.
+// Tensor memory, 512 columns: C B^T, overlaid block by block by the masked forms
+// as the product's A operand (128); Y (128); S (128); w X as A operand (128).
 //
 // Rounding. C B^T takes the stored B and C; its masked form and the S that C
 // multiplies are rounded to 16 bits, about what rounding the output costs. S
@@ -39,7 +41,7 @@ namespace {
 
 constexpr int kBox = 16384;      // 128 rows of 128 bytes
 constexpr int kRing = 10;        // boxes in flight; even, so that a pair is adjacent
-constexpr int kTcThreads = 320;  // 8 scaling warps, TMA warp, MMA warp
+constexpr int kTcThreads = 608;  // 8 masking warps, 8 weighing warps, TMA warp, 2 MMA warps
 constexpr uint32_t kColG = 0, kColY = 128, kColS = 256, kColX = 384;
 constexpr int32_t kErrTcWait = 16;
 
@@ -49,17 +51,21 @@ struct TcMaps {
 
 struct Shared {
   uint64_t full[kRing], empty[kRing];
-  uint64_t xw0, xw0_done, masked, y_done, xw1, s_done, s_ready, gy_done;
+  uint64_t prepared, xw0, xw0_done, masked, y_done, y_free, xw1, s_done, s_ready, gy_done;
   uint32_t tmem;
   int dead;
-  float tot[2][4];           // log2 decay of each 32 tokens
-  float top[2][4];           // largest |w| of each 32 tokens (fp16)
-  alignas(16) float2 ldt[2][128];        // (log2 decay since the start of the 32, dt)
-  alignas(16) float colf[2][128];        // dt times the decay to the end of the 32
-  alignas(16) float w[2][128];           // dt times the decay to the end of the chunk
+  // of chunk c in stage c % 2, by head of the tile
+  float tot[2][2][4];                   // log2 decay of each 32 tokens
+  float top[2][2][4];                   // largest |colf| of each 32 tokens (fp16)
+  alignas(16) float2 ldt[2][2][128];    // (log2 decay since the start of the 32, dt)
+  alignas(16) float colf[2][2][128];    // dt times the decay to the end of the 32
 };
 
-__device__ __forceinline__ bool wait_tc(uint64_t *bar, uint32_t parity, volatile int *dead, int32_t *err) {
+// The code runs once per chunk in several roles at once, so its size counts (the
+// first, fully unrolled form spent half of its time waiting for instructions):
+// loops over pieces of 16 columns stay rolled, and what a wait does when the
+// barrier is not there yet is not inlined.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *dead, int32_t *err) {
   for (uint32_t i = 0; i < kMaxWaitIters; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*dead) return false;
@@ -67,6 +73,9 @@ __device__ __forceinline__ bool wait_tc(uint64_t *bar, uint32_t parity, volatile
   *dead = 1;
   atomicCAS(err, 0, kErrTcWait);
   return false;
+}
+__device__ __forceinline__ bool wait_tc(uint64_t *bar, uint32_t parity, volatile int *dead, int32_t *err) {
+  return mbar_test(bar, parity) || wait_long(bar, parity, dead, err);
 }
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -92,27 +101,14 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 columns of the warp's 32 lanes (thread = lane); the load is complete on return.
-__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t (&v)[32]) {
+// 16 columns of the warp's 32 lanes (thread = lane); the load is complete on return.
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
-      "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
-      "r"(v[31])
       : "memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&v)[16]) {
@@ -122,9 +118,18 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&v)[16]) 
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tm_st4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
 
-// Barrier of the 8 scaling warps.
-__device__ __forceinline__ void sync_scalers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Barrier of the 8 weighing warps.
+__device__ __forceinline__ void sync_weighers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // One arrival per warp, after all its lanes.
 __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
   __syncwarp();
@@ -152,6 +157,10 @@ template <> struct Terms<__half> {
     t[1] = pack2<__half>(v.x - h.x, v.y - h.y);
   }
 };
+
+// Instruction descriptor of a product of two T operands into fp32, M = 128.
+template <typename T>
+constexpr uint32_t kIdesc = (1u << 4) | ((Terms<T>::N == 3 ? 1u : 0u) << 7) | ((Terms<T>::N == 3 ? 1u : 0u) << 10) | (8u << 24);
 
 // PW: columns of a head in the tile (64: two heads, 128: one). NS: padded dstate.
 template <typename T, int PW, int NS, bool SUMMARY, bool GATE>
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // thread = column: its head, row of the state and half of the states
   const int wg = (warp >> 2) & 1, wq = warp & 3;
   const int pc = wq * 32 + lane, hs = HT == 2 ? pc >> 6 : 0, pp = HT == 2 ? pc & 63 : pc;
-  const bool pin = warp < 8 && h0 + hs < hend && pp < p.headdim;
+  const bool pin = warp >= 8 && warp < 16 && h0 + hs < hend && pp < p.headdim;
   const int n0 = wg * NH, nv = min(max(p.dstate - n0, 0), NH);  // a multiple of 8
   const long long pn = (long long)p.headdim * p.dstate;
   float *cache = kept ? p.state + slot * p.ss[0] + (h0 + hs) * p.ss[1] + (long long)pp * p.dstate + n0 : nullptr;
@@ -219,10 +228,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
+    mbar_init(&sh.prepared, 8);
     mbar_init(&sh.xw0, 8);
     mbar_init(&sh.xw1, 8);
     mbar_init(&sh.masked, 8);
     mbar_init(&sh.s_ready, 8);
+    mbar_init(&sh.y_free, 8);
     mbar_init(&sh.xw0_done, 1);
     mbar_init(&sh.y_done, 1);
     mbar_init(&sh.s_done, 1);
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     sh.dead = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     fence_before();
@@ -238,11 +249,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tm = sh.tmem;
+  const uint32_t lane_at = (uint32_t)(wq * 32) << 16;
   volatile int *dead = &sh.dead;
   const int chunks = (size + 127) / 128;
   auto box = [&](int c, int o) { return ring + ((c * BPC + o) % kRing) * kBox; };
+  auto full = [&](int c, int o) {
+    const int i = c * BPC + o;
+    wait_tc(&sh.full[i % kRing], (i / kRing) & 1, dead, p.err);
+  };
+  auto release = [&](int c, int o, int n) {
+    for (int k = 0; k < n; ++k) mbar_arrive(&sh.empty[(c * BPC + o + k) % kRing]);
+  };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ---- TMA ----
     if (lane == 0) {
       int issued = 0;
@@ -272,94 +291,84 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (mbar_try_wait(&sh.full[i % kRing], parity)) break;
       }
     }
-  } else if (warp == 9) {
-    // ---- products ----
-    if (lane == 0) {
-      constexpr uint32_t ty = sizeof(T) == 2 && NT == 3 ? 1u : 0u;  // bf16 : fp16
-      constexpr uint32_t base = (1u << 4) | (ty << 7) | (ty << 10) | (8u << 24);
-      constexpr uint32_t id_g = base | (128u / 8 << 17);                             // C B^T and C S^T: both K-major, N = 128
-      constexpr uint32_t id_y = base | (1u << 16) | ((uint32_t)PW / 8 << 17);        // masked x X: X is N-major
-      constexpr uint32_t id_s = base | (1u << 16) | ((uint32_t)NS / 8 << 17);        // w X x B: B is N-major
-      const uint32_t s16a = smem_u32(s16);
-      auto full = [&](int c, int o) {
-        const int i = c * BPC + o;
-        wait_tc(&sh.full[i % kRing], (i / kRing) & 1, dead, p.err);
-      };
-      auto gain = [&](int c, int round) {  // two quarters of 32 tokens into S
-        const uint32_t b = smem_u32(box(c, oB));
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < NT; ++e)
-              mma_ts(tm + kColS, tm + kColX + 64 * q + 16 * e + 8 * k,
-                     smem_desc(b + (round * 64 + q * 32 + k * 16) * 128, kBox, 1024), id_s, true);
-      };
+  } else if (warp == 17) {
+    // ---- products for Y ----
+    if (lane == 0 && !SUMMARY) {
+      constexpr uint32_t id_g = kIdesc<T> | (128u / 8 << 17);                       // C B^T and C S^T: both K-major, N = 128
+      constexpr uint32_t id_y = kIdesc<T> | (1u << 16) | ((uint32_t)PW / 8 << 17);  // masked x X: X is N-major
+      const uint64_t sd = smem_desc(smem_u32(s16), 16, 1024);
       for (int c = 0; c < chunks; ++c) {
         const uint32_t ph = c & 1;
-        for (int o = 0; o < NB; ++o) full(c, oB + o);
-        if (!SUMMARY) {
-          for (int o = 0; o < NB; ++o) full(c, oC + o);
-          if (c > 0) wait_tc(&sh.y_done, ph ^ 1, dead, p.err);  // the masked form's columns are free again
-          fence_after();
-          const uint32_t ca = smem_u32(box(c, oC)), ba = smem_u32(box(c, oB));
-          if (!*dead) {
+        for (int o = 0; o < 2 * NB; ++o) full(c, oC + o);
+        if (c > 0) wait_tc(&sh.y_done, ph ^ 1, dead, p.err);  // the masked forms' columns are free again
+        fence_after();
+        const uint64_t cd = smem_desc(smem_u32(box(c, oC)), 16, 1024), bd = smem_desc(smem_u32(box(c, oB)), 16, 1024);
+        if (!*dead) {
 #pragma unroll
-            for (int k = 0; k < NS / 16; ++k) {
-              const uint32_t at = (k / 4) * kBox + (k % 4) * 32;
-              mma_ss(tm + kColG, smem_desc(ca + at, 16, 1024), smem_desc(ba + at, 16, 1024), id_g, k > 0);
-            }
+          for (int k = 0; k < NS / 16; ++k) {
+            const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
+            mma_ss(tm + kColG, cd + at, bd + at, id_g, k > 0);
           }
-          wait_tc(&sh.s_ready, ph, dead, p.err);
-          fence_after();
-          if (!*dead) {
-#pragma unroll
-            for (int k = 0; k < NS / 16; ++k) {
-              const uint32_t at = (k / 4) * kBox + (k % 4) * 32;
-              mma_ss(tm + kColY, smem_desc(ca + at, 16, 1024), smem_desc(s16a + at, 16, 1024), id_g, k > 0);
-            }
-            commit(&sh.gy_done);
-          }
-        } else {
-          wait_tc(&sh.s_ready, ph, dead, p.err);
         }
-        wait_tc(&sh.xw0, ph, dead, p.err);
+        if (c > 0) wait_tc(&sh.y_free, ph ^ 1, dead, p.err);
+        wait_tc(&sh.s_ready, ph, dead, p.err);
         fence_after();
         if (!*dead) {
-          gain(c, 0);
-          commit(&sh.xw0_done);
-        }
-        if (!SUMMARY) {
-          full(c, oX);
-          full(c, oX + 1);
-          wait_tc(&sh.masked, ph, dead, p.err);
-          fence_after();
-          if (!*dead) {
-            for (int h = 0; h < HT; ++h) {
-              const uint32_t xa = smem_u32(box(c, oX + h));
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_ts(tm + kColY + 64 * h, tm + kColG + 64 * h + 8 * k, smem_desc(xa + k * 2048, kBox, 1024), id_y, true);
-            }
-            commit(&sh.y_done);
+          for (int k = 0; k < NS / 16; ++k) {
+            const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
+            mma_ss(tm + kColY, cd + at, sd + at, id_g, k > 0);
           }
+          commit(&sh.gy_done);
         }
-        wait_tc(&sh.xw1, ph, dead, p.err);
+        full(c, oX);
+        full(c, oX + 1);
+        wait_tc(&sh.xw0, ph, dead, p.err);  // rows past the request's end are cleared
+        wait_tc(&sh.masked, ph, dead, p.err);
         fence_after();
         if (!*dead) {
-          gain(c, 1);
-          commit(&sh.s_done);
+          const uint64_t xd = smem_desc(smem_u32(box(c, oX)), kBox, 1024);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+              mma_ts(tm + kColY + 64 * h, tm + kColG + 16 * k + 8 * h, xd + ((h * kBox + k * 2048) >> 4), id_y, true);
+          commit(&sh.y_done);
         }
       }
     }
-  } else {
-    // ---- scaling warps ----
-    const int hr = HT == 2 ? wg : 0;                    // thread = row: its head
-    const bool hin = h0 + hr < hend;
-    const int hh = hin ? h0 + hr : h0;
-    const float A2 = p.A[hh] * kLog2e, bias = p.bias ? p.bias[hh] : 0.f, skip = p.D ? p.D[hh] : 0.f;
+  } else if (warp == 18) {
+    // ---- products for S ----
+    if (lane == 0) {
+      constexpr uint32_t id_s = kIdesc<T> | (1u << 16) | ((uint32_t)NS / 8 << 17);  // w X x B: B is N-major
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t ph = c & 1;
+        for (int o = 0; o < NB; ++o) full(c, oB + o);
+        wait_tc(&sh.s_ready, ph, dead, p.err);
+        const uint64_t bd = smem_desc(smem_u32(box(c, oB)), kBox, 1024);
+#pragma unroll 1
+        for (int round = 0; round < 2; ++round) {
+          wait_tc(round ? &sh.xw1 : &sh.xw0, ph, dead, p.err);
+          fence_after();
+          if (!*dead) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < NT; ++e)
+                  mma_ts(tm + kColS, tm + kColX + 64 * q + 16 * e + 8 * k, bd + (((round * 64 + q * 32 + k * 16) * 128) >> 4), id_s,
+                         true);
+            commit(round ? &sh.s_done : &sh.xw0_done);
+          }
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ---- masking warps: thread = row t; warpgroup wg prepares head wg ----
+    const int hh = HT == 2 && h0 + wg < hend ? h0 + wg : h0;
+    const float A2 = p.A[hh] * kLog2e, bias = p.bias ? p.bias[hh] : 0.f;
     const int trow = wq * 32 + lane;
-    const uint32_t lane_at = (uint32_t)(wq * 32) << 16;
     const long long dt_at = hh * p.sdt[1];
     auto load_dt = [&](int c) -> float {
       const int t = c * 128 + trow;
@@ -367,262 +376,235 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const long long at = (long long)(first + t) * p.sdt[0] + dt_at;
       return p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]);
     };
-    float l = 0.f, since = 0.f;       // log2 decay since the start of the 32 tokens, of the chunk
-    float decay = 0.f, scale = 1.f;   // of this column's head: log2 decay so far; w's scale in this chunk
-    // dt and the decays of chunk c
-    auto prepare = [&](int c, float raw_dt) {
-      float dt = raw_dt + bias;
-      if (p.softplus) dt = softplus_f(dt);
-      if (c * 128 + trow >= size) dt = 0.f;
-      const float a = dt * A2;
-      l = a;
-      float to_end = a;
+    float raw_dt = load_dt(0);
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = c & 1;
+      const int st = c & 1;
+      {  // dt and the decays of the chunk
+        float dt = raw_dt + bias;
+        if (p.softplus) dt = softplus_f(dt);
+        if (c * 128 + trow >= size) dt = 0.f;
+        float l = dt * A2, to_end = l;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float up = __shfl_up_sync(0xffffffffu, l, o), dn = __shfl_down_sync(0xffffffffu, to_end, o);
-        if (lane >= o) l += up;
-        if (lane + o < 32) to_end += dn;
-      }
-      if (lane == 31) sh.tot[wg][wq] = l;
-      // what follows this token, without the token itself
-      const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
-      to_end = lane < 31 ? nx : 0.f;
-      sync_scalers();
-      float before = 0.f, after = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float t = sh.tot[wg][k];
-        if (k < wq) before += t;
-        if (k > wq) after += t;
-      }
-      since = before + l;
-      const float w = dt * ex2(to_end + after);
-      sh.ldt[wg][trow] = make_float2(l, dt);
-      sh.colf[wg][trow] = dt * ex2(to_end);
-      sh.w[wg][trow] = w;
-      if (NT == 2) {
-        float m = fabsf(w);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) sh.top[wg][wq] = m;
-      }
-      sync_scalers();
-    };
-    auto total = [&]() { return (sh.tot[hs][0] + sh.tot[hs][1]) + (sh.tot[hs][2] + sh.tot[hs][3]); };
-    // power of two that brings this chunk's largest w to [1/2, 1)
-    auto w_scale = [&]() -> float {
-      if (NT != 2) return 1.f;
-      const float m = fmaxf(fmaxf(sh.top[hs][0], sh.top[hs][1]), fmaxf(sh.top[hs][2], sh.top[hs][3]));
-      const int e = (int)(__float_as_uint(m) >> 23);
-      return e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
-    };
-    // S (in v, true values): its 16-bit form for the next chunk's product, and its
-    // decayed, scaled form as the accumulator
-    auto hand_on = [&](float (&v)[NH]) {
-      const float t = total();
-      decay += t;
-      scale = w_scale();
-      const float keep = ex2(t) * scale;
-      if (!SUMMARY) {
-#pragma unroll
-        for (int q = 0; q < NH / 8; ++q) {
-          const int n = n0 + 8 * q;  // a 16-byte piece of the row
-          uint4 w4;
-          w4.x = pack2<T>(v[8 * q], v[8 * q + 1]);
-          w4.y = pack2<T>(v[8 * q + 2], v[8 * q + 3]);
-          w4.z = pack2<T>(v[8 * q + 4], v[8 * q + 5]);
-          w4.w = pack2<T>(v[8 * q + 6], v[8 * q + 7]);
-          *reinterpret_cast<uint4 *>(s16 + (n / 64) * kBox + swz(pc, (n % 64) * 2)) = w4;
+        for (int o = 1; o < 32; o <<= 1) {
+          const float up = __shfl_up_sync(0xffffffffu, l, o), dn = __shfl_down_sync(0xffffffffu, to_end, o);
+          if (lane >= o) l += up;
+          if (lane + o < 32) to_end += dn;
         }
-        fence_proxy_async();
+        // what follows this token, without the token itself
+        const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
+        const float cf = dt * ex2(lane < 31 ? nx : 0.f);
+        sh.ldt[st][wg][trow] = make_float2(l, dt);
+        sh.colf[st][wg][trow] = cf;
+        if (lane == 31) sh.tot[st][wg][wq] = l;
+        if (NT == 2) {
+          float m = fabsf(cf);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (lane == 0) sh.top[st][wg][wq] = m;
+        }
+        arrive_warp(&sh.prepared, lane);
       }
+      raw_dt = load_dt(c + 1);
+      if (SUMMARY) {
+        wait_tc(&sh.s_ready, ph, dead, p.err);  // chunk c - 1 no longer needs its stage, and chunk c's is taken up
+        continue;
+      }
+      wait_tc(&sh.prepared, ph, dead, p.err);  // all warps' rows of this chunk
+      wait_tc(&sh.gy_done, ph, dead, p.err);
+      fence_after();
+      if (tid == 0) release(c, oC, NB);
+      // The masked forms of 16 columns, one per head, in place of C B^T. Of the
+      // blocks of 32 a warpgroup takes 0 and 3, or 1 and 2: equal work below the
+      // diagonal.
+#pragma unroll 1
+      for (int i4 = 0; i4 < 4; ++i4) {
+        const int jb = i4 < 2 ? 2 * wg + i4 : 4 - 2 * wg + i4, j = jb >> 1;
+        const uint32_t at = tm + lane_at + kColG + 16 * jb;
+        uint32_t g[16];
+        if (j <= wq) tm_ld16(at, g);
+#pragma unroll 1
+        for (int h = 0; h < HT; ++h) {
+          uint32_t m[8];
+          if (j > wq) {
 #pragma unroll
-      for (int q = 0; q < NH / 32; ++q) {
-        uint32_t w[32];
+            for (int i = 0; i < 8; ++i) m[i] = 0;
+          } else {
+            float l = sh.ldt[st][h][trow].x;
+            if (j < wq) {
+              for (int k = j + 1; k < wq; ++k) l += sh.tot[st][h][k];
+              l = ex2(l);
+              const f2 rf = pk(l, l);
+              const float *colf = sh.colf[st][h] + 16 * jb;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[32 * q + i] * keep);
-        tm_st32(tm + lane_at + kColS + n0 + 32 * q, w);
+              for (int i = 0; i < 16; i += 4) {
+                const float4 cf = *reinterpret_cast<const float4 *>(colf + i);
+                const float2 a = upk(mul2(mul2(pk(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), rf), pk(cf.x, cf.y)));
+                const float2 b = upk(mul2(mul2(pk(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3])), rf), pk(cf.z, cf.w)));
+                m[i / 2] = pack2<T>(a.x, a.y);
+                m[i / 2 + 1] = pack2<T>(b.x, b.y);
+              }
+            } else {
+              const float2 *ldt = sh.ldt[st][h] + 16 * jb;
+              const int d = trow - 16 * jb;  // columns up to d are at or before the row
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float4 q = *reinterpret_cast<const float4 *>(ldt + i);  // (l, dt) of two tokens
+                const float a = __uint_as_float(g[i]) * (ex2(l - q.x) * q.y), b = __uint_as_float(g[i + 1]) * (ex2(l - q.z) * q.w);
+                m[i / 2] = pack2<T>(i <= d ? a : 0.f, i + 1 <= d ? b : 0.f);
+              }
+            }
+          }
+          tm_st8(at + 8 * h, m);
+        }
+      }
+      // Y = e^L (C S^T)
+      const int h = HT == 2 ? wg : 0;
+      float e = sh.ldt[st][h][trow].x;
+      for (int k = 0; k < wq; ++k) e += sh.tot[st][h][k];
+      e = ex2(e);
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t y[16];
+        const uint32_t at = tm + lane_at + kColY + 64 * wg + 16 * q;
+        tm_ld16(at, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * e);
+        tm_st16(at, y);
       }
       wait_st();
       fence_before();
-      arrive_warp(&sh.s_ready, lane);
-    };
-
-    float raw_dt = load_dt(0);
-    {
-      float v[NH];
-#pragma unroll
-      for (int i = 0; i < NH; ++i) v[i] = 0.f;
-      auto fold = [&](const float *src, float keep) {
-#pragma unroll
-        for (int n = 0; n < NH; n += 4)
-          if (n < nv) {
-            const float4 q = *reinterpret_cast<const float4 *>(src + n);
-            v[n] = fmaf(keep, v[n], q.x);
-            v[n + 1] = fmaf(keep, v[n + 1], q.y);
-            v[n + 2] = fmaf(keep, v[n + 2], q.z);
-            v[n + 3] = fmaf(keep, v[n + 3], q.w);
-          }
-      };
-      if (pin) {
-        if (index == 0) {
-          if (goes_on) fold(!SUMMARY && last > 0 ? entry(last) : cache, 0.f);
-        } else if (!SUMMARY) {
-          fold(entry(0), 0.f);
-          for (int i = 1; i < index; ++i) fold(entry(i), ex2(*decay_of(i)));
-        }
-      }
-      prepare(0, raw_dt);
-      hand_on(v);
+      arrive_warp(&sh.masked, lane);
     }
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t ph = c & 1;
-      const int valid = min(128, size - c * 128);
-      raw_dt = load_dt(c + 1);
-      auto full = [&](int o) {
-        const int i = c * BPC + o;
-        wait_tc(&sh.full[i % kRing], (i / kRing) & 1, dead, p.err);
-      };
-      full(oX);
-      full(oX + 1);
-      if (valid < 128) {  // rows of the next request, or of nothing: 0 x anything must be 0
-        for (int o = 0; o < NB; ++o) full(oB + o);
-        const int todo = (128 - valid) * 8;
-        for (int i = tid; i < todo * (2 + NB); i += 256) {
-          const int o = i / todo, k = i % todo;
-          unsigned char *b = o < 2 ? box(c, oX + o) : box(c, oB + o - 2);
-          *reinterpret_cast<uint4 *>(b + (valid + k / 8) * 128 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+    fence_before();
+  } else {
+    // ---- weighing warps: thread = column p, and for the output row t ----
+    const int hr = HT == 2 ? wg : 0;
+    const bool hin = h0 + hr < hend;
+    const int hh = hin ? h0 + hr : h0;
+    const float skip = p.D ? p.D[hh] : 0.f;
+    const int trow = wq * 32 + lane;
+    float decay = 0.f, scale = 1.f;  // of this column's head: log2 decay so far; w's scale in this chunk
+    float fade0 = 0.f, fade1 = 0.f;  // from the ends of the 32 tokens weighed first and second to the chunk's end, times scale
+#pragma unroll 1
+    for (int c = 0; c <= chunks; ++c) {
+      const uint32_t ph = c & 1, before = ph ^ 1;
+      const bool more = c < chunks;
+      const float unscale = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / scale, a power of two
+      float keep = 0.f;              // decay of this chunk, times its scale
+      if (more) {
+        wait_tc(&sh.prepared, ph, dead, p.err);
+        const float *t = sh.tot[ph][hs];
+        const float t3 = t[3], t2 = t3 + t[2], t1 = t2 + t[1], t0 = t1 + t[0];
+        decay += t0;
+        keep = ex2(t0);
+        fade0 = ex2(wg ? t2 : t1);
+        fade1 = wg ? 1.f : ex2(t3);
+        if (NT == 2) {  // the power of two that brings the chunk's largest w to [1/2, 1)
+          const float *top = sh.top[ph][hs];
+          const float m = fmaxf(fmaxf(top[0] * ex2(t1), top[1] * ex2(t2)), fmaxf(top[2] * ex2(t3), top[3]));
+          const int e = (int)(__float_as_uint(m) >> 23);
+          scale = e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
+          keep *= scale;
+          fade0 *= scale;
+          fade1 *= scale;
         }
-        fence_proxy_async();
-        sync_scalers();
       }
-      // w X of 32 tokens as the product's A operand: thread = column
-      auto weigh = [&](int round) {
-        const int s0 = round * 64 + wg * 32;
-        const unsigned char *col = box(c, oX + (pc >> 6)) + (pc & 7) * 2;
-        const int piece = (pc & 63) >> 3;
-        uint32_t t[NT][16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 w = *reinterpret_cast<const float4 *>(&sh.w[hs][s0 + i]);
-          if (NT == 2) { w.x *= scale; w.y *= scale; w.z *= scale; w.w *= scale; }
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int s = s0 + i + k;
-            x[k] = to_f<T>(*reinterpret_cast<const T *>(col + s * 128 + ((piece ^ (s & 7)) << 4)));
-          }
-          uint32_t a[NT], b[NT];
-          Terms<T>::split(make_float2(x[0] * w.x, x[1] * w.y), a);
-          Terms<T>::split(make_float2(x[2] * w.z, x[3] * w.w), b);
-#pragma unroll
-          for (int e = 0; e < NT; ++e) {
-            t[e][i / 2] = a[e];
-            t[e][i / 2 + 1] = b[e];
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < NT; ++e) tm_st16(tm + lane_at + kColX + 64 * wg + 16 * e, t[e]);
-        wait_st();
-        fence_before();
-        arrive_warp(round ? &sh.xw1 : &sh.xw0, lane);
-      };
-      weigh(0);
-
-      if (!SUMMARY) {
-        // the masked form of C B^T, and Y = e^L (C S^T): thread = row
-        wait_tc(&sh.gy_done, ph, dead, p.err);
+      // S after the chunk before (at first, the block's start): its 16-bit form for
+      // this chunk's product, and its decayed, scaled form as the accumulator
+      if (c > 0) {
+        wait_tc(&sh.s_done, before, dead, p.err);  // and all columns of X are read
+        if (!SUMMARY) wait_tc(&sh.gy_done, before, dead, p.err);
         fence_after();
-        const float2 *ldt = sh.ldt[wg];
-        const float *colf = sh.colf[wg];
-        auto masked_block = [&](int j, uint32_t (&m)[16]) {  // columns 32 j .. 32 j + 31
-          if (j > wq) {
+        if (tid == 256) release(c - 1, oB, SUMMARY ? NB + 2 : NB);
+      }
+#pragma unroll 1
+      for (int q = 0; q < NH / 16; ++q) {
+        float v[16];
+        const int n = 16 * q;
+        if (c > 0) {
+          uint32_t s[16];
+          tm_ld16(tm + lane_at + kColS + n0 + n, s);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m[i] = 0;
-            return;
-          }
-          uint32_t g[32];
-          tm_ld32(tm + lane_at + kColG + 32 * j, g);
-          if (j < wq) {
-            float e = l;
-            for (int k = j + 1; k < wq; ++k) e += sh.tot[wg][k];
-            const f2 rf = pk(ex2(e), ex2(e));
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 cf = *reinterpret_cast<const float4 *>(colf + 32 * j + i);
-              const float2 a = upk(mul2(mul2(pk(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), rf), pk(cf.x, cf.y)));
-              const float2 b = upk(mul2(mul2(pk(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3])), rf), pk(cf.z, cf.w)));
-              m[i / 2] = pack2<T>(a.x, a.y);
-              m[i / 2 + 1] = pack2<T>(b.x, b.y);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float4 q = *reinterpret_cast<const float4 *>(ldt + 32 * j + i);  // (l, dt) of two tokens
-              const float a = __uint_as_float(g[i]) * (ex2(l - q.x) * q.y), b = __uint_as_float(g[i + 1]) * (ex2(l - q.z) * q.w);
-              m[i / 2] = pack2<T>(i <= lane ? a : 0.f, i + 1 <= lane ? b : 0.f);
-            }
-          }
-        };
-        const float e = ex2(since);
-        auto scale_y = [&]() {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t y[32];
-            const uint32_t at = tm + lane_at + kColY + 64 * wg + 32 * q;
-            tm_ld32(at, y);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * e);
-            tm_st32(at, y);
-          }
-        };
-        if constexpr (HT == 2) {
-          uint32_t m[4][16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) masked_block(j, m[j]);
-          fence_before();
-          sync_scalers();  // all of C B^T is read before any of it is overlaid
-          fence_after();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tm_st16(tm + lane_at + kColG + 64 * wg + 16 * j, m[j]);
+          for (int i = 0; i < 16; ++i) v[i] = NT == 2 ? __uint_as_float(s[i]) * unscale : __uint_as_float(s[i]);
         } else {
-          const int j0 = wg, j1 = 3 - wg;  // blocks 0 and 3, or 1 and 2: equal work below the diagonal
-          uint32_t m[2][16];
-          masked_block(j0, m[0]);
-          masked_block(j1, m[1]);
-          fence_before();
-          sync_scalers();
-          fence_after();
-          tm_st16(tm + lane_at + kColG + 16 * j0, m[0]);
-          tm_st16(tm + lane_at + kColG + 16 * j1, m[1]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          auto fold = [&](const float *src, float k) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              if (n + i < nv) {
+                const float4 f = *reinterpret_cast<const float4 *>(src + n + i);
+                v[i] = fmaf(k, v[i], f.x);
+                v[i + 1] = fmaf(k, v[i + 1], f.y);
+                v[i + 2] = fmaf(k, v[i + 2], f.z);
+                v[i + 3] = fmaf(k, v[i + 3], f.w);
+              }
+          };
+          if (pin) {
+            if (index == 0) {
+              if (goes_on) fold(!SUMMARY && last > 0 ? entry(last) : cache, 0.f);
+            } else if (!SUMMARY) {
+#pragma unroll 1
+              for (int i = 0; i < index; ++i) fold(entry(i), ex2(*decay_of(i)));
+            }
+          }
         }
-        scale_y();
+        if (more) {
+          if (!SUMMARY) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) {
+              uint4 w4;  // a 16-byte piece of the row
+              w4.x = pack2<T>(v[i], v[i + 1]);
+              w4.y = pack2<T>(v[i + 2], v[i + 3]);
+              w4.z = pack2<T>(v[i + 4], v[i + 5]);
+              w4.w = pack2<T>(v[i + 6], v[i + 7]);
+              *reinterpret_cast<uint4 *>(s16 + ((n0 + n) / 64) * kBox + swz(pc, ((n0 + n + i) % 64) * 2)) = w4;
+            }
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * keep);
+          tm_st16(tm + lane_at + kColS + n0 + n, w);
+        } else if (pin && !*dead && (SUMMARY || (index == last && kept))) {
+          float *dst = (SUMMARY ? entry(index) : cache) + n;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            if (n + i < nv) *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      }
+      if (more) {
+        if (!SUMMARY) fence_proxy_async();
         wait_st();
         fence_before();
-        arrive_warp(&sh.masked, lane);
+        arrive_warp(&sh.s_ready, lane);
+      } else if (SUMMARY && pin && pp == 0 && wg == 0 && !*dead) {
+        *decay_of(index) = decay;
       }
 
-      wait_tc(&sh.xw0_done, ph, dead, p.err);
-      fence_after();
-      weigh(1);
-      sync_scalers();  // X is read by columns no more: its rows become the output's
-
-      if (!SUMMARY) {
+      if (!SUMMARY && c > 0) {
+        // the output of the chunk before, in place of X's rows
+        const int cb = c - 1, valid = min(128, size - cb * 128);
         if (GATE) {
-          full(oZ);
-          full(oZ + 1);
+          full(cb, oZ);
+          full(cb, oZ + 1);
         }
-        wait_tc(&sh.y_done, ph, dead, p.err);
+        wait_tc(&sh.y_done, before, dead, p.err);
         fence_after();
-        unsigned char *xr = box(c, oX + wg);
-        const unsigned char *zr = box(c, oZ + wg);
+        unsigned char *xr = box(cb, oX + wg);
+        const unsigned char *zr = box(cb, oZ + wg);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t y[16];
+          tm_ld16(tm + lane_at + kColY + 64 * wg + 16 * q, y);
+          if (q == 3) {
+            fence_before();
+            arrive_warp(&sh.y_free, lane);
+          }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t y[32];
-          tm_ld32(tm + lane_at + kColY + 64 * wg + 32 * q, y);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = swz(trow, 64 * q + 16 * k);
+          for (int k = 0; k < 2; ++k) {
+            const int at = swz(trow, 32 * q + 16 * k);
             const uint4 xq = *reinterpret_cast<const uint4 *>(xr + at);
             const uint32_t xw[4] = {xq.x, xq.y, xq.z, xq.w};
             uint4 zq = make_uint4(0, 0, 0, 0);
@@ -647,48 +629,77 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the warp's 32 rows leave as whole 128-byte lines
         if (hin && !*dead) {
           const int piece = lane & 7, col = (HT == 2 ? 0 : 64 * wg) + 8 * piece;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = wq * 32 + i * 4 + (lane >> 3);
-            if (t < valid && col < p.headdim)
-              *reinterpret_cast<uint4 *>(out + (long long)(first + c * 128 + t) * p.so[0] + hh * p.so[1] + col) =
-                  *reinterpret_cast<const uint4 *>(xr + swz(t, 16 * piece));
+          if (col < p.headdim) {
+#pragma unroll 4
+            for (int i = 0; i < 8; ++i) {
+              const int t = wq * 32 + i * 4 + (lane >> 3);
+              if (t < valid)
+                *reinterpret_cast<uint4 *>(out + (long long)(first + cb * 128 + t) * p.so[0] + hh * p.so[1] + col) =
+                    *reinterpret_cast<const uint4 *>(xr + swz(t, 16 * piece));
+            }
           }
         }
+        fence_proxy_async();  // before the next copies into these boxes
+        sync_weighers();
+        if (tid == 256) release(cb, oX, BPC - oX);
+      }
+      if (!more) break;
+
+      const int valid = min(128, size - c * 128);
+      full(c, oX);
+      full(c, oX + 1);
+      if (valid < 128) {  // rows of the next request, or of nothing: 0 x anything must be 0
+        for (int o = 0; o < NB; ++o) full(c, oB + o);
+        const int todo = (128 - valid) * 8;
+        for (int i = tid - 256; i < todo * (2 + NB); i += 256) {
+          const int o = i / todo, k = i % todo;
+          unsigned char *b = o < 2 ? box(c, oX + o) : box(c, oB + o - 2);
+          *reinterpret_cast<uint4 *>(b + (valid + k / 8) * 128 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        sync_weighers();
+      }
+      // w X as the product's A operand: thread = column, 32 tokens at a time
+      const unsigned char *col = box(c, oX + (pc >> 6)) + (pc & 7) * 2;
+      const int piece = (pc & 63) >> 3;
+#pragma unroll 1
+      for (int round = 0; round < 2; ++round) {
+        if (round) {
+          wait_tc(&sh.xw0_done, ph, dead, p.err);
+          fence_after();
+        }
+        const int s0 = round * 64 + wg * 32;
+        const float f = round ? fade1 : fade0;
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t t[NT][4];
+          const float4 wa = *reinterpret_cast<const float4 *>(&sh.colf[ph][hs][s0 + i]);
+          const float4 wb = *reinterpret_cast<const float4 *>(&sh.colf[ph][hs][s0 + i + 4]);
+          const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // rows s0 + i are multiples of 8: row k of a swizzle atom
+            x[k] = to_f<T>(*reinterpret_cast<const T *>(col + (s0 + i + k) * 128 + ((piece ^ k) << 4)));
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            uint32_t a[NT];
+            Terms<T>::split(make_float2(x[k] * (w[k] * f), x[k + 1] * (w[k + 1] * f)), a);
+#pragma unroll
+            for (int e = 0; e < NT; ++e) t[e][k / 2] = a[e];
+          }
+#pragma unroll
+          for (int e = 0; e < NT; ++e) tm_st4(tm + lane_at + kColX + 64 * wg + 16 * e + i / 2, t[e]);
+        }
+        wait_st();
         fence_before();
-        fence_proxy_async();  // before the next copy into these boxes
-      }
-      const bool more = c + 1 < chunks;
-      const float unscale = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / scale, a power of two
-      if (more) prepare(c + 1, raw_dt);
-      else sync_scalers();
-      wait_tc(&sh.s_done, ph, dead, p.err);
-      fence_after();
-      if (tid == 0)
-        for (int o = 0; o < BPC; ++o) mbar_arrive(&sh.empty[(c * BPC + o) % kRing]);
-      float v[NH];
-#pragma unroll
-      for (int q = 0; q < NH / 32; ++q) {
-        uint32_t s[32];
-        tm_ld32(tm + lane_at + kColS + n0 + 32 * q, s);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[32 * q + i] = NT == 2 ? __uint_as_float(s[i]) * unscale : __uint_as_float(s[i]);
-      }
-      if (more) {
-        hand_on(v);
-      } else if (pin && !*dead && (SUMMARY || (index == last && kept))) {
-        float *dst = SUMMARY ? entry(index) : cache;
-#pragma unroll
-        for (int n = 0; n < NH; n += 4)
-          if (n < nv) *reinterpret_cast<float4 *>(dst + n) = make_float4(v[n], v[n + 1], v[n + 2], v[n + 3]);
-        if (SUMMARY && pp == 0 && wg == 0) *decay_of(index) = decay;
+        arrive_warp(round ? &sh.xw1 : &sh.xw0, lane);
       }
     }
     fence_before();
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
   }

@@ -351,13 +351,29 @@ int ss_head_scan(const ss_head_scan_params *p, void *stream) {
 }
 
 int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int64_t headdim, int32_t dtype, int32_t sms) {
-  // (rows of 64 of a head) x (blocks) should give every multiprocessor work
   if (tokens < 1 || requests < 1 || heads < 1 || headdim < 1 || sms < 1) return 128;
-  const int64_t units = heads * ((headdim + 63) / 64);
-  (void)dtype;
-  int64_t want = std::max<int64_t>(1, (2 * sms + units - 1) / units);
-  int64_t block = (tokens + want - 1) / want;
-  block = (block + 127) / 128 * 128;
+  // Requests of the average length, cut into `cut` blocks each: the waves of CTAs
+  // times the chunks of 128 tokens in one, plus the summaries of all blocks but
+  // the last (about half of the work of a chunk) and the launch and folding that
+  // they bring (in chunks, as measured: 3 and 1/4 per block).
+  const bool tc = dtype != SS_F32 && headdim <= 128;
+  const int64_t tiles = tc ? (headdim <= 64 ? (heads + 1) / 2 : heads) : heads * ((headdim + 63) / 64);
+  const int64_t resident = tc ? sms : 4 * sms;
+  const int64_t chunks = (tokens / requests + 127) / 128;
+  int64_t best = 1;
+  double least = 0;
+  for (int64_t cut = 1; cut <= std::min<int64_t>(chunks, 64); ++cut) {
+    const int64_t len = (chunks + cut - 1) / cut;
+    const double waves = static_cast<double>((requests * tiles * cut + resident - 1) / resident);
+    const double cost = waves * len * (cut > 1 ? 1.5 : 1.0) + (cut > 1 ? 3.0 + 0.25 * cut : 0.0);
+    if (cut == 1 || cost < least) {
+      least = cost;
+      best = cut;
+    }
+  }
+  int64_t block = (chunks + best - 1) / best * 128;
+  // a batch whose requests need no cut may still hold one long request
+  if (best == 1) block = std::max<int64_t>(block, 2048);
   return std::min<int64_t>(block, 1 << 19);
 }
 
