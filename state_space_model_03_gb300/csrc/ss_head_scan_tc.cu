@@ -14,14 +14,16 @@
 //
 // One CTA carries 128 (head, p) columns, two heads of 64 or one of 128, through
 // one block of a request. C B^T and the operands C and B are shared by its heads.
-//   warps 0 - 7   mask: C B^T to its masked form, C S^T by e^L (thread = row t),
-//                 and the decays of the next chunk
-//   warps 8 - 15  weigh: X to w X, S to the next chunk's start (thread = column p),
-//                 then finish the output (thread = row t)
-//   warp 16       loads the chunks by TMA (boxes of 128 tokens x 64 values)
-//   warp 17       issues the products for Y, warp 18 those for S (tcgen05,
-//                 accumulators in tensor memory)
-// The masking warps run on chunk c+1 while the weighing warps finish chunk c.
+//   warps 0 - 7    mask: C B^T to its masked form, C S^T by e^L (thread = row t),
+//                  and the decays of the next chunk
+//   warps 8 - 15   weigh: S to the chunk's start, X to w X (thread = column p)
+//   warps 16 - 23  finish: Y to the output (thread = row t)
+//   warp 24        loads the chunks by TMA (boxes of 128 tokens x 64 values),
+//                  warp 27 stores the output the same way
+//   warp 25        issues the products for Y, warp 26 those for S (tcgen05,
+//                  accumulators in tensor memory)
+// The groups run on different chunks: while one chunk's output is finished, the
+// next is masked and weighed.
 // Tensor memory, 512 columns: C B^T, overlaid block by block by the masked forms
 // as the product's A operand (128); Y (128); S (128); w X as A operand (128).
 //
@@ -41,23 +43,28 @@ namespace {
 
 constexpr int kBox = 16384;      // 128 rows of 128 bytes
 constexpr int kRing = 10;        // boxes in flight; even, so that a pair is adjacent
-constexpr int kTcThreads = 608;  // 8 masking warps, 8 weighing warps, TMA warp, 2 MMA warps
+constexpr int kTcThreads = 896;  // 3 groups of 8 warps, then TMA loads, 2 x MMA, TMA stores
 constexpr uint32_t kColG = 0, kColY = 128, kColS = 256, kColX = 384;
 constexpr int32_t kErrTcWait = 16;
 
 struct TcMaps {
-  CUtensorMap x, B, C, z;
+  CUtensorMap x, B, C, z, out;
 };
 
 struct Shared {
   uint64_t full[kRing], empty[kRing];
   uint64_t prepared, xw0, xw0_done, masked, y_done, y_free, xw1, s_done, s_ready, gy_done;
+  // A group waits on these that does not hold up the one that arrives for a chunk
+  // or more: one barrier for each chunk that the latter can be ahead.
+  uint64_t x_read[2];    // weighing -> finishing (and products for Y): X's columns are read, its rows may be overwritten
+  uint64_t finished[4];  // finishing -> storing
   uint32_t tmem;
   int dead;
   // of chunk c in stage c % 2, by head of the tile
   float tot[2][2][4];                   // log2 decay of each 32 tokens
   float top[2][2][4];                   // largest |colf| of each 32 tokens (fp16)
-  alignas(16) float2 ldt[2][2][128];    // (log2 decay since the start of the 32, dt)
+  alignas(16) float nl[2][2][128];      // minus the log2 decay since the start of the 32
+  alignas(16) float dt[2][2][128];
   alignas(16) float colf[2][2][128];    // dt times the decay to the end of the 32
 };
 
@@ -128,6 +135,19 @@ __device__ __forceinline__ void tm_st4(uint32_t addr, const uint32_t (&v)[4]) {
                : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *tm, const void *src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+               : "memory");
+}
+
 // Barrier of the 8 weighing warps.
 __device__ __forceinline__ void sync_weighers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // One arrival per warp, after all its lanes.
@@ -136,25 +156,43 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 pku(uint32_t lo, uint32_t hi) { return pk(__uint_as_float(lo), __uint_as_float(hi)); }
+template <typename T>
+__device__ __forceinline__ f2 wide(uint32_t w) {  // two 16-bit values as a packed fp32 pair
+  const float2 v = unpack2<T>(w);
+  return pk(v.x, v.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t narrow(f2 v) {
+  const float2 f = upk(v);
+  return pack2<T>(f.x, f.y);
+}
+
 // Two fp32 values as 16-bit terms of decreasing size, packed: hi + mid (+ lo).
 template <typename T> struct Terms;
 template <> struct Terms<__nv_bfloat16> {
   static constexpr int N = 3;  // by truncation, 8 bits each
-  static __device__ __forceinline__ void split(float2 v, uint32_t (&t)[3]) {
+  static __device__ __forceinline__ void split(f2 v, uint32_t (&t)[3]) {
+    const f2 minus = pk(-1.f, -1.f);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      t[k] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
-      v.x -= __uint_as_float(__float_as_uint(v.x) & 0xffff0000u);
-      v.y -= __uint_as_float(__float_as_uint(v.y) & 0xffff0000u);
+      const float2 f = upk(v);
+      const uint32_t x = __float_as_uint(f.x), y = __float_as_uint(f.y);
+      t[k] = __byte_perm(x, y, 0x7632);
+      if (k < 2) v = fma2(pku(x & 0xffff0000u, y & 0xffff0000u), minus, v);
     }
   }
 };
 template <> struct Terms<__half> {
   static constexpr int N = 2;
-  static __device__ __forceinline__ void split(float2 v, uint32_t (&t)[2]) {
-    t[0] = pack2<__half>(v.x, v.y);
-    const float2 h = unpack2<__half>(t[0]);
-    t[1] = pack2<__half>(v.x - h.x, v.y - h.y);
+  static __device__ __forceinline__ void split(f2 v, uint32_t (&t)[2]) {
+    t[0] = narrow<__half>(v);
+    t[1] = narrow<__half>(fma2(wide<__half>(t[0]), pk(-1.f, -1.f), v));
   }
 };
 
@@ -238,10 +276,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&sh.y_done, 1);
     mbar_init(&sh.s_done, 1);
     mbar_init(&sh.gy_done, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.x_read[i], 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.finished[i], 8);
     sh.dead = 0;
     fence_barrier_init();
   }
-  if (warp == 17) {
+  if (warp == 25) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     fence_before();
@@ -261,7 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int k = 0; k < n; ++k) mbar_arrive(&sh.empty[(c * BPC + o + k) % kRing]);
   };
 
-  if (warp == 16) {
+  if (warp == 24) {
     // ---- TMA ----
     if (lane == 0) {
       int issued = 0;
@@ -291,19 +331,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (mbar_try_wait(&sh.full[i % kRing], parity)) break;
       }
     }
-  } else if (warp == 17) {
+  } else if (warp == 25) {
     // ---- products for Y ----
-    if (lane == 0 && !SUMMARY) {
+    if (!SUMMARY) {
       constexpr uint32_t id_g = kIdesc<T> | (128u / 8 << 17);                       // C B^T and C S^T: both K-major, N = 128
       constexpr uint32_t id_y = kIdesc<T> | (1u << 16) | ((uint32_t)PW / 8 << 17);  // masked x X: X is N-major
       const uint64_t sd = smem_desc(smem_u32(s16), 16, 1024);
+#pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const uint32_t ph = c & 1;
         for (int o = 0; o < 2 * NB; ++o) full(c, oC + o);
         if (c > 0) wait_tc(&sh.y_done, ph ^ 1, dead, p.err);  // the masked forms' columns are free again
         fence_after();
         const uint64_t cd = smem_desc(smem_u32(box(c, oC)), 16, 1024), bd = smem_desc(smem_u32(box(c, oB)), 16, 1024);
-        if (!*dead) {
+        __syncwarp();
+        if (elect() && !*dead) {
 #pragma unroll
           for (int k = 0; k < NS / 16; ++k) {
             const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
@@ -313,7 +355,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (c > 0) wait_tc(&sh.y_free, ph ^ 1, dead, p.err);
         wait_tc(&sh.s_ready, ph, dead, p.err);
         fence_after();
-        if (!*dead) {
+        __syncwarp();
+        if (elect() && !*dead) {
 #pragma unroll
           for (int k = 0; k < NS / 16; ++k) {
             const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
@@ -323,11 +366,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         full(c, oX);
         full(c, oX + 1);
-        wait_tc(&sh.xw0, ph, dead, p.err);  // rows past the request's end are cleared
+        if (size - c * 128 < 128) wait_tc(&sh.x_read[c & 1], (c >> 1) & 1, dead, p.err);  // rows past the request's end are cleared
         wait_tc(&sh.masked, ph, dead, p.err);
         fence_after();
-        if (!*dead) {
-          const uint64_t xd = smem_desc(smem_u32(box(c, oX)), kBox, 1024);
+        const uint64_t xd = smem_desc(smem_u32(box(c, oX)), kBox, 1024);
+        __syncwarp();
+        if (elect() && !*dead) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
 #pragma unroll
@@ -337,32 +381,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-  } else if (warp == 18) {
+  } else if (warp == 26) {
     // ---- products for S ----
-    if (lane == 0) {
-      constexpr uint32_t id_s = kIdesc<T> | (1u << 16) | ((uint32_t)NS / 8 << 17);  // w X x B: B is N-major
-      for (int c = 0; c < chunks; ++c) {
-        const uint32_t ph = c & 1;
-        for (int o = 0; o < NB; ++o) full(c, oB + o);
-        wait_tc(&sh.s_ready, ph, dead, p.err);
-        const uint64_t bd = smem_desc(smem_u32(box(c, oB)), kBox, 1024);
+    constexpr uint32_t id_s = kIdesc<T> | (1u << 16) | ((uint32_t)NS / 8 << 17);  // w X x B: B is N-major
 #pragma unroll 1
-        for (int round = 0; round < 2; ++round) {
-          wait_tc(round ? &sh.xw1 : &sh.xw0, ph, dead, p.err);
-          fence_after();
-          if (!*dead) {
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = c & 1;
+      for (int o = 0; o < NB; ++o) full(c, oB + o);
+      wait_tc(&sh.s_ready, ph, dead, p.err);
+#pragma unroll 1
+      for (int round = 0; round < 2; ++round) {
+        wait_tc(round ? &sh.xw1 : &sh.xw0, ph, dead, p.err);
+        fence_after();
+        const uint64_t bd = smem_desc(smem_u32(box(c, oB)) + round * 64 * 128, kBox, 1024);
+        __syncwarp();
+        if (elect() && !*dead) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int e = 0; e < NT; ++e)
-                  mma_ts(tm + kColS, tm + kColX + 64 * q + 16 * e + 8 * k, bd + (((round * 64 + q * 32 + k * 16) * 128) >> 4), id_s,
-                         true);
-            commit(round ? &sh.s_done : &sh.xw0_done);
-          }
+              for (int e = 0; e < NT; ++e)
+                mma_ts(tm + kColS, tm + kColX + 64 * q + 16 * e + 8 * k, bd + (((q * 32 + k * 16) * 128) >> 4), id_s, true);
+          commit(round ? &sh.s_done : &sh.xw0_done);
         }
       }
+    }
+  } else if (warp == 27) {
+    // ---- output: whole chunks leave by TMA, a request's last rows have left already ----
+    if (!SUMMARY && lane == 0) {
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        wait_tc(&sh.finished[c & 3], (c >> 2) & 1, dead, p.err);
+        if (size - c * 128 >= 128 && !*dead) {
+          for (int k = 0; k < 2; ++k)
+            if (HT == 1 || h0 + k < hend)
+              tma_store_3d(&maps.out, box(c, oX + k), HT == 2 ? 0 : 64 * k, HT == 2 ? h0 + k : h0, first + c * 128);
+          asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        release(c, oX, BPC - oX);
+      }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   } else if (warp < 8) {
     // ---- masking warps: thread = row t; warpgroup wg prepares head wg ----
@@ -395,7 +454,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // what follows this token, without the token itself
         const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
         const float cf = dt * ex2(lane < 31 ? nx : 0.f);
-        sh.ldt[st][wg][trow] = make_float2(l, dt);
+        sh.nl[st][wg][trow] = -l;
+        sh.dt[st][wg][trow] = dt;
         sh.colf[st][wg][trow] = cf;
         if (lane == 31) sh.tot[st][wg][wq] = l;
         if (NT == 2) {
@@ -424,14 +484,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t at = tm + lane_at + kColG + 16 * jb;
         uint32_t g[16];
         if (j <= wq) tm_ld16(at, g);
-#pragma unroll 1
+#pragma unroll
         for (int h = 0; h < HT; ++h) {
           uint32_t m[8];
           if (j > wq) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) m[i] = 0;
           } else {
-            float l = sh.ldt[st][h][trow].x;
+            float l = -sh.nl[st][h][trow];
             if (j < wq) {
               for (int k = j + 1; k < wq; ++k) l += sh.tot[st][h][k];
               l = ex2(l);
@@ -440,19 +500,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
                 const float4 cf = *reinterpret_cast<const float4 *>(colf + i);
-                const float2 a = upk(mul2(mul2(pk(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), rf), pk(cf.x, cf.y)));
-                const float2 b = upk(mul2(mul2(pk(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3])), rf), pk(cf.z, cf.w)));
-                m[i / 2] = pack2<T>(a.x, a.y);
-                m[i / 2 + 1] = pack2<T>(b.x, b.y);
+                m[i / 2] = narrow<T>(mul2(mul2(pku(g[i], g[i + 1]), rf), pk(cf.x, cf.y)));
+                m[i / 2 + 1] = narrow<T>(mul2(mul2(pku(g[i + 2], g[i + 3]), rf), pk(cf.z, cf.w)));
               }
             } else {
-              const float2 *ldt = sh.ldt[st][h] + 16 * jb;
+              const float *nl = sh.nl[st][h] + 16 * jb, *dt = sh.dt[st][h] + 16 * jb;
               const int d = trow - 16 * jb;  // columns up to d are at or before the row
+              const f2 l2 = pk(l, l);
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float4 q = *reinterpret_cast<const float4 *>(ldt + i);  // (l, dt) of two tokens
-                const float a = __uint_as_float(g[i]) * (ex2(l - q.x) * q.y), b = __uint_as_float(g[i + 1]) * (ex2(l - q.z) * q.w);
-                m[i / 2] = pack2<T>(i <= d ? a : 0.f, i + 1 <= d ? b : 0.f);
+              for (int i = 0; i < 16; i += 4) {
+                const float4 n4 = *reinterpret_cast<const float4 *>(nl + i), d4 = *reinterpret_cast<const float4 *>(dt + i);
+                const float2 a = upk(add2(l2, pk(n4.x, n4.y))), b = upk(add2(l2, pk(n4.z, n4.w)));
+                const float2 u = upk(mul2(mul2(pk(ex2(a.x), ex2(a.y)), pk(d4.x, d4.y)), pku(g[i], g[i + 1])));
+                const float2 v = upk(mul2(mul2(pk(ex2(b.x), ex2(b.y)), pk(d4.z, d4.w)), pku(g[i + 2], g[i + 3])));
+                m[i / 2] = pack2<T>(i <= d ? u.x : 0.f, i + 1 <= d ? u.y : 0.f);
+                m[i / 2 + 1] = pack2<T>(i + 2 <= d ? v.x : 0.f, i + 3 <= d ? v.y : 0.f);
               }
             }
           }
@@ -461,7 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       // Y = e^L (C S^T)
       const int h = HT == 2 ? wg : 0;
-      float e = sh.ldt[st][h][trow].x;
+      float e = -sh.nl[st][h][trow];
       for (int k = 0; k < wq; ++k) e += sh.tot[st][h][k];
       e = ex2(e);
 #pragma unroll 1
@@ -470,7 +532,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t at = tm + lane_at + kColY + 64 * wg + 16 * q;
         tm_ld16(at, y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * e);
+        for (int i = 0; i < 16; i += 2) {
+          const float2 v = upk(mul2(pku(y[i], y[i + 1]), pk(e, e)));
+          y[i] = __float_as_uint(v.x);
+          y[i + 1] = __float_as_uint(v.y);
+        }
         tm_st16(at, y);
       }
       wait_st();
@@ -478,13 +544,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       arrive_warp(&sh.masked, lane);
     }
     fence_before();
-  } else {
-    // ---- weighing warps: thread = column p, and for the output row t ----
-    const int hr = HT == 2 ? wg : 0;
-    const bool hin = h0 + hr < hend;
-    const int hh = hin ? h0 + hr : h0;
-    const float skip = p.D ? p.D[hh] : 0.f;
-    const int trow = wq * 32 + lane;
+  } else if (warp < 16) {
+    // ---- weighing warps: thread = column p ----
     float decay = 0.f, scale = 1.f;  // of this column's head: log2 decay so far; w's scale in this chunk
     float fade0 = 0.f, fade1 = 0.f;  // from the ends of the 32 tokens weighed first and second to the chunk's end, times scale
 #pragma unroll 1
@@ -565,7 +626,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * keep);
+          for (int i = 0; i < 16; i += 2) {
+            const float2 k = upk(mul2(pk(v[i], v[i + 1]), pk(keep, keep)));
+            w[i] = __float_as_uint(k.x);
+            w[i + 1] = __float_as_uint(k.y);
+          }
           tm_st16(tm + lane_at + kColS + n0 + n, w);
         } else if (pin && !*dead && (SUMMARY || (index == last && kept))) {
           float *dst = (SUMMARY ? entry(index) : cache) + n;
@@ -583,66 +648,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *decay_of(index) = decay;
       }
 
-      if (!SUMMARY && c > 0) {
-        // the output of the chunk before, in place of X's rows
-        const int cb = c - 1, valid = min(128, size - cb * 128);
-        if (GATE) {
-          full(cb, oZ);
-          full(cb, oZ + 1);
-        }
-        wait_tc(&sh.y_done, before, dead, p.err);
-        fence_after();
-        unsigned char *xr = box(cb, oX + wg);
-        const unsigned char *zr = box(cb, oZ + wg);
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t y[16];
-          tm_ld16(tm + lane_at + kColY + 64 * wg + 16 * q, y);
-          if (q == 3) {
-            fence_before();
-            arrive_warp(&sh.y_free, lane);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int at = swz(trow, 32 * q + 16 * k);
-            const uint4 xq = *reinterpret_cast<const uint4 *>(xr + at);
-            const uint32_t xw[4] = {xq.x, xq.y, xq.z, xq.w};
-            uint4 zq = make_uint4(0, 0, 0, 0);
-            if (GATE) zq = *reinterpret_cast<const uint4 *>(zr + at);
-            const uint32_t zw[4] = {zq.x, zq.y, zq.z, zq.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 xv = unpack2<T>(xw[i]);
-              float a = fmaf(skip, xv.x, __uint_as_float(y[8 * k + 2 * i])), b = fmaf(skip, xv.y, __uint_as_float(y[8 * k + 2 * i + 1]));
-              if (GATE) {
-                const float2 zv = unpack2<T>(zw[i]);
-                a *= silu_f(zv.x);
-                b *= silu_f(zv.y);
-              }
-              o[i] = pack2<T>(a, b);
-            }
-            *reinterpret_cast<uint4 *>(xr + at) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        }
-        __syncwarp();
-        // the warp's 32 rows leave as whole 128-byte lines
-        if (hin && !*dead) {
-          const int piece = lane & 7, col = (HT == 2 ? 0 : 64 * wg) + 8 * piece;
-          if (col < p.headdim) {
-#pragma unroll 4
-            for (int i = 0; i < 8; ++i) {
-              const int t = wq * 32 + i * 4 + (lane >> 3);
-              if (t < valid)
-                *reinterpret_cast<uint4 *>(out + (long long)(first + cb * 128 + t) * p.so[0] + hh * p.so[1] + col) =
-                    *reinterpret_cast<const uint4 *>(xr + swz(t, 16 * piece));
-            }
-          }
-        }
-        fence_proxy_async();  // before the next copies into these boxes
-        sync_weighers();
-        if (tid == 256) release(cb, oX, BPC - oX);
-      }
       if (!more) break;
 
       const int valid = min(128, size - c * 128);
@@ -675,17 +680,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint32_t t[NT][4];
           const float4 wa = *reinterpret_cast<const float4 *>(&sh.colf[ph][hs][s0 + i]);
           const float4 wb = *reinterpret_cast<const float4 *>(&sh.colf[ph][hs][s0 + i + 4]);
-          const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+          const f2 f2f = pk(f, f);
+          const f2 w[4] = {mul2(pk(wa.x, wa.y), f2f), mul2(pk(wa.z, wa.w), f2f), mul2(pk(wb.x, wb.y), f2f), mul2(pk(wb.z, wb.w), f2f)};
           float x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // rows s0 + i are multiples of 8: row k of a swizzle atom
             x[k] = to_f<T>(*reinterpret_cast<const T *>(col + (s0 + i + k) * 128 + ((piece ^ k) << 4)));
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) {
+          for (int k = 0; k < 4; ++k) {
             uint32_t a[NT];
-            Terms<T>::split(make_float2(x[k] * (w[k] * f), x[k + 1] * (w[k + 1] * f)), a);
+            Terms<T>::split(mul2(pk(x[2 * k], x[2 * k + 1]), w[k]), a);
 #pragma unroll
-            for (int e = 0; e < NT; ++e) t[e][k / 2] = a[e];
+            for (int e = 0; e < NT; ++e) t[e][k] = a[e];
           }
 #pragma unroll
           for (int e = 0; e < NT; ++e) tm_st4(tm + lane_at + kColX + 64 * wg + 16 * e + i / 2, t[e]);
@@ -694,12 +700,76 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_before();
         arrive_warp(round ? &sh.xw1 : &sh.xw0, lane);
       }
+      if (!SUMMARY) arrive_warp(&sh.x_read[ph], lane);
+    }
+    fence_before();
+  } else if (!SUMMARY) {
+    // ---- finishing warps: thread = row t ----
+    const int hr = HT == 2 ? wg : 0;
+    const bool hin = h0 + hr < hend;
+    const int hh = hin ? h0 + hr : h0;
+    const float skip = p.D ? p.D[hh] : 0.f;
+    const int trow = wq * 32 + lane;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      // the output, in place of X's rows
+      const int valid = min(128, size - c * 128);
+      full(c, oX + wg);
+      if (GATE) full(c, oZ + wg);
+      wait_tc(&sh.x_read[c & 1], (c >> 1) & 1, dead, p.err);
+      wait_tc(&sh.y_done, c & 1, dead, p.err);
+      fence_after();
+      unsigned char *xr = box(c, oX + wg);
+      const unsigned char *zr = box(c, oZ + wg);
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t y[16];
+        tm_ld16(tm + lane_at + kColY + 64 * wg + 16 * q, y);
+        if (q == 3) {
+          fence_before();
+          arrive_warp(&sh.y_free, lane);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int at = swz(trow, 32 * q + 16 * k);
+          const uint4 xq = *reinterpret_cast<const uint4 *>(xr + at);
+          const uint32_t xw[4] = {xq.x, xq.y, xq.z, xq.w};
+          uint4 zq = make_uint4(0, 0, 0, 0);
+          if (GATE) zq = *reinterpret_cast<const uint4 *>(zr + at);
+          const uint32_t zw[4] = {zq.x, zq.y, zq.z, zq.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f2 v = fma2(pk(skip, skip), wide<T>(xw[i]), pku(y[8 * k + 2 * i], y[8 * k + 2 * i + 1]));
+            if (GATE) {
+              const f2 zv = wide<T>(zw[i]);
+              const float2 e = upk(mul2(zv, pk(-kLog2e, -kLog2e)));
+              const float2 d = upk(add2(pk(ex2(e.x), ex2(e.y)), pk(1.f, 1.f)));
+              v = mul2(v, mul2(zv, pk(rcp(d.x), rcp(d.y))));
+            }
+            o[i] = narrow<T>(v);
+          }
+          *reinterpret_cast<uint4 *>(xr + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      if (valid < 128 && hin && !*dead) {  // the request's last rows, as 128-byte lines
+        __syncwarp();
+        const int piece = lane & 7, col = (HT == 2 ? 0 : 64 * wg) + 8 * piece;
+        if (col < p.headdim) {
+#pragma unroll 1
+          for (int t = wq * 32 + (lane >> 3); t < min(valid, wq * 32 + 32); t += 4)
+            *reinterpret_cast<uint4 *>(out + (long long)(first + c * 128 + t) * p.so[0] + hh * p.so[1] + col) =
+                *reinterpret_cast<const uint4 *>(xr + swz(t, 16 * piece));
+        }
+      }
+      fence_proxy_async();  // before the store, and the next copies into these boxes
+      arrive_warp(&sh.finished[c & 3], lane);
     }
     fence_before();
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 25) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
   }
@@ -773,7 +843,8 @@ cudaError_t launch_head_scan_tc(int dtype, const HeadScanParams &p, TensorMapEnc
   const int groups = p.heads / p.hpg;
   if (!map3(enc, &m.x, p.x, p.headdim, p.heads, p.t.tokens, p.sx) || !map3(enc, &m.B, p.B, p.dstate, groups, p.t.tokens, p.sB) ||
       !map3(enc, &m.C, p.C, p.dstate, groups, p.t.tokens, p.sC) ||
-      !map3(enc, &m.z, p.z ? p.z : p.x, p.headdim, p.heads, p.t.tokens, p.z ? p.sz : p.sx))
+      !map3(enc, &m.z, p.z ? p.z : p.x, p.headdim, p.heads, p.t.tokens, p.z ? p.sz : p.sx) ||
+      !map3(enc, &m.out, p.out, p.headdim, p.heads, p.t.tokens, p.so))
     return cudaErrorInvalidValue;
   return dtype == 1 ? by_size<__half>(p, m, s) : by_size<__nv_bfloat16>(p, m, s);
 }
