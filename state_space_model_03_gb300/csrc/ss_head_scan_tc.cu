@@ -14,10 +14,10 @@
 //
 // One CTA carries 128 (head, p) columns, two heads of 64 or one of 128, through
 // one block of a request. C B^T and the operands C and B are shared by its heads.
-//   warps 0 - 7    mask: C B^T to its masked form, C S^T by e^L (thread = row t),
-//                  and the decays of the next chunk
+//   warps 0 - 7    mask: C B^T to its masked form, C S^T by e^L (thread = row t)
 //   warps 8 - 15   weigh: S to the chunk's start, X to w X (thread = column p)
-//   warps 16 - 23  finish: Y to the output (thread = row t)
+//   warps 16 - 23  finish: Y to the output (thread = row t), and the decays of the
+//                  chunk after the next
 //   warp 24        loads the chunks by TMA (boxes of 128 tokens x 64 values),
 //                  warp 27 stores the output the same way
 //   warp 25        issues the products for Y, warp 26 those for S (tcgen05,
@@ -53,19 +53,20 @@ struct TcMaps {
 
 struct Shared {
   uint64_t full[kRing], empty[kRing];
-  uint64_t prepared, xw0, xw0_done, masked, y_done, y_free, xw1, s_done, s_ready, gy_done;
+  uint64_t xw0, xw0_done, masked, y_done, y_free, xw1, s_done, s_ready, gy_done;
   // A group waits on these that does not hold up the one that arrives for a chunk
   // or more: one barrier for each chunk that the latter can be ahead.
   uint64_t x_read[2];    // weighing -> finishing (and products for Y): X's columns are read, its rows may be overwritten
   uint64_t finished[4];  // finishing -> storing
+  uint64_t prepared[4];  // finishing -> masking and weighing: the chunk's decays
   uint32_t tmem;
   int dead;
-  // of chunk c in stage c % 2, by head of the tile
-  float tot[2][2][4];                   // log2 decay of each 32 tokens
-  float top[2][2][4];                   // largest |colf| of each 32 tokens (fp16)
-  alignas(16) float nl[2][2][128];      // minus the log2 decay since the start of the 32
-  alignas(16) float dt[2][2][128];
-  alignas(16) float colf[2][2][128];    // dt times the decay to the end of the 32
+  // of chunk c in stage c % 4, by head of the tile
+  float tot[4][2][4];                   // log2 decay of each 32 tokens
+  float top[4][2][4];                   // largest |colf| of each 32 tokens (fp16)
+  alignas(16) float nl[4][2][128];      // minus the log2 decay since the start of the 32
+  alignas(16) float dt[4][2][128];
+  alignas(16) float colf[4][2][128];    // dt times the decay to the end of the 32
 };
 
 // The code runs once per chunk in several roles at once, so its size counts (the
@@ -156,6 +157,14 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+template <typename T>
+__device__ __forceinline__ float lds_16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  T t;
+  memcpy(&t, &v, 2);
+  return to_f<T>(t);
+}
 __device__ __forceinline__ f2 add2(f2 a, f2 b) {
   f2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -266,7 +275,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
-    mbar_init(&sh.prepared, 8);
     mbar_init(&sh.xw0, 8);
     mbar_init(&sh.xw1, 8);
     mbar_init(&sh.masked, 8);
@@ -277,7 +285,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&sh.s_done, 1);
     mbar_init(&sh.gy_done, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.x_read[i], 8);
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.finished[i], 8);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.finished[i], 8);
+      mbar_init(&sh.prepared[i], 8);
+    }
     sh.dead = 0;
     fence_barrier_init();
   }
@@ -424,54 +435,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   } else if (warp < 8) {
-    // ---- masking warps: thread = row t; warpgroup wg prepares head wg ----
-    const int hh = HT == 2 && h0 + wg < hend ? h0 + wg : h0;
-    const float A2 = p.A[hh] * kLog2e, bias = p.bias ? p.bias[hh] : 0.f;
+    // ---- masking warps: thread = row t ----
     const int trow = wq * 32 + lane;
-    const long long dt_at = hh * p.sdt[1];
-    auto load_dt = [&](int c) -> float {
-      const int t = c * 128 + trow;
-      if (t >= size) return 0.f;
-      const long long at = (long long)(first + t) * p.sdt[0] + dt_at;
-      return p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]);
-    };
-    float raw_dt = load_dt(0);
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; c < (SUMMARY ? 0 : chunks); ++c) {
       const uint32_t ph = c & 1;
-      const int st = c & 1;
-      {  // dt and the decays of the chunk
-        float dt = raw_dt + bias;
-        if (p.softplus) dt = softplus_f(dt);
-        if (c * 128 + trow >= size) dt = 0.f;
-        float l = dt * A2, to_end = l;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float up = __shfl_up_sync(0xffffffffu, l, o), dn = __shfl_down_sync(0xffffffffu, to_end, o);
-          if (lane >= o) l += up;
-          if (lane + o < 32) to_end += dn;
-        }
-        // what follows this token, without the token itself
-        const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
-        const float cf = dt * ex2(lane < 31 ? nx : 0.f);
-        sh.nl[st][wg][trow] = -l;
-        sh.dt[st][wg][trow] = dt;
-        sh.colf[st][wg][trow] = cf;
-        if (lane == 31) sh.tot[st][wg][wq] = l;
-        if (NT == 2) {
-          float m = fabsf(cf);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (lane == 0) sh.top[st][wg][wq] = m;
-        }
-        arrive_warp(&sh.prepared, lane);
-      }
-      raw_dt = load_dt(c + 1);
-      if (SUMMARY) {
-        wait_tc(&sh.s_ready, ph, dead, p.err);  // chunk c - 1 no longer needs its stage, and chunk c's is taken up
-        continue;
-      }
-      wait_tc(&sh.prepared, ph, dead, p.err);  // all warps' rows of this chunk
+      const int st = c & 3;
+      wait_tc(&sh.prepared[st], (c >> 2) & 1, dead, p.err);
       wait_tc(&sh.gy_done, ph, dead, p.err);
       fence_after();
       if (tid == 0) release(c, oC, NB);
@@ -555,15 +525,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float unscale = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / scale, a power of two
       float keep = 0.f;              // decay of this chunk, times its scale
       if (more) {
-        wait_tc(&sh.prepared, ph, dead, p.err);
-        const float *t = sh.tot[ph][hs];
+        wait_tc(&sh.prepared[c & 3], (c >> 2) & 1, dead, p.err);
+        const float *t = sh.tot[c & 3][hs];
         const float t3 = t[3], t2 = t3 + t[2], t1 = t2 + t[1], t0 = t1 + t[0];
         decay += t0;
         keep = ex2(t0);
         fade0 = ex2(wg ? t2 : t1);
         fade1 = wg ? 1.f : ex2(t3);
         if (NT == 2) {  // the power of two that brings the chunk's largest w to [1/2, 1)
-          const float *top = sh.top[ph][hs];
+          const float *top = sh.top[c & 3][hs];
           const float m = fmaxf(fmaxf(top[0] * ex2(t1), top[1] * ex2(t2)), fmaxf(top[2] * ex2(t3), top[3]));
           const int e = (int)(__float_as_uint(m) >> 23);
           scale = e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
@@ -665,27 +635,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sync_weighers();
       }
       // w X as the product's A operand: thread = column, 32 tokens at a time
-      const unsigned char *col = box(c, oX + (pc >> 6)) + (pc & 7) * 2;
-      const int piece = (pc & 63) >> 3;
+      uint32_t col = smem_u32(box(c, oX + (pc >> 6))) + wg * 32 * 128 + (pc & 63) * 2;  // in row 0 of a swizzle atom
+      const float *cf = sh.colf[c & 3][hs] + wg * 32;
 #pragma unroll 1
       for (int round = 0; round < 2; ++round) {
         if (round) {
           wait_tc(&sh.xw0_done, ph, dead, p.err);
           fence_after();
         }
-        const int s0 = round * 64 + wg * 32;
         const float f = round ? fade1 : fade0;
 #pragma unroll 1
         for (int i = 0; i < 32; i += 8) {
           uint32_t t[NT][4];
-          const float4 wa = *reinterpret_cast<const float4 *>(&sh.colf[ph][hs][s0 + i]);
-          const float4 wb = *reinterpret_cast<const float4 *>(&sh.colf[ph][hs][s0 + i + 4]);
+          const float4 wa = *reinterpret_cast<const float4 *>(cf);
+          const float4 wb = *reinterpret_cast<const float4 *>(cf + 4);
           const f2 f2f = pk(f, f);
           const f2 w[4] = {mul2(pk(wa.x, wa.y), f2f), mul2(pk(wa.z, wa.w), f2f), mul2(pk(wb.x, wb.y), f2f), mul2(pk(wb.z, wb.w), f2f)};
           float x[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // rows s0 + i are multiples of 8: row k of a swizzle atom
-            x[k] = to_f<T>(*reinterpret_cast<const T *>(col + (s0 + i + k) * 128 + ((piece ^ k) << 4)));
+          for (int k = 0; k < 8; ++k) x[k] = lds_16<T>((col ^ (k << 4)) + k * 128);
+          col += 8 * 128;
+          cf += 8;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t a[NT];
@@ -699,19 +669,64 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wait_st();
         fence_before();
         arrive_warp(round ? &sh.xw1 : &sh.xw0, lane);
+        col += 32 * 128;
+        cf += 32;
       }
       if (!SUMMARY) arrive_warp(&sh.x_read[ph], lane);
     }
     fence_before();
-  } else if (!SUMMARY) {
-    // ---- finishing warps: thread = row t ----
+  } else if (warp < 24) {
+    // ---- finishing warps: thread = row t; warpgroup wg prepares head wg ----
     const int hr = HT == 2 ? wg : 0;
     const bool hin = h0 + hr < hend;
     const int hh = hin ? h0 + hr : h0;
-    const float skip = p.D ? p.D[hh] : 0.f;
+    const float skip = p.D ? p.D[hh] : 0.f, A2 = p.A[hh] * kLog2e, bias = p.bias ? p.bias[hh] : 0.f;
     const int trow = wq * 32 + lane;
+    auto load_dt = [&](int c) -> float {
+      const int t = c * 128 + trow;
+      if (t >= size) return 0.f;
+      const long long at = (long long)(first + t) * p.sdt[0] + hh * p.sdt[1];
+      return p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]);
+    };
+    // The decays are prepared two chunks ahead of the output.
+    constexpr int kAhead = SUMMARY ? 0 : 2;
+    float raw_dt = load_dt(0);
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
+    for (int cp = 0; cp < chunks + kAhead; ++cp) {
+      if (cp < chunks) {
+        const int st = cp & 3;
+        float dt = raw_dt + bias;
+        if (p.softplus) dt = softplus_f(dt);
+        if (cp * 128 + trow >= size) dt = 0.f;
+        float l = dt * A2, to_end = l;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float up = __shfl_up_sync(0xffffffffu, l, o), dn = __shfl_down_sync(0xffffffffu, to_end, o);
+          if (lane >= o) l += up;
+          if (lane + o < 32) to_end += dn;
+        }
+        // what follows this token, without the token itself
+        const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
+        const float cf = dt * ex2(lane < 31 ? nx : 0.f);
+        sh.nl[st][wg][trow] = -l;
+        sh.dt[st][wg][trow] = dt;
+        sh.colf[st][wg][trow] = cf;
+        if (lane == 31) sh.tot[st][wg][wq] = l;
+        if (NT == 2) {
+          float m = fabsf(cf);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (lane == 0) sh.top[st][wg][wq] = m;
+        }
+        arrive_warp(&sh.prepared[st], lane);
+        raw_dt = load_dt(cp + 1);
+      }
+      if (SUMMARY) {
+        wait_tc(&sh.s_ready, cp & 1, dead, p.err);  // the chunk's decays are taken up, its predecessor's no longer needed
+        continue;
+      }
+      const int c = cp - kAhead;
+      if (c < 0) continue;
       // the output, in place of X's rows
       const int valid = min(128, size - c * 128);
       full(c, oX + wg);
