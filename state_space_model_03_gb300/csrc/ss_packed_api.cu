@@ -353,28 +353,28 @@ int ss_head_scan(const ss_head_scan_params *p, void *stream) {
 int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int64_t headdim, int32_t dtype, int32_t sms) {
   if (tokens < 1 || requests < 1 || heads < 1 || headdim < 1 || sms < 1) return 128;
   // Requests of the average length, cut into `cut` blocks each: the waves of CTAs
-  // times the chunks of 128 tokens in one, plus the summaries of all blocks but
-  // the last (about half of the work of a chunk) and the launch and folding that
-  // they bring (in chunks, as measured: 3 and 1/4 per block).
+  // times the steps (of 128 tokens on the tensor cores, else of 16) in one, plus
+  // the summaries of all blocks but the last (about half of a step's work) and
+  // the launch and folding that they bring, in steps (5 us and 4 us, as measured).
   const bool tc = dtype != SS_F32 && headdim <= 128;
   const int64_t tiles = tc ? (headdim <= 64 ? (heads + 1) / 2 : heads) : heads * ((headdim + 63) / 64);
-  const int64_t resident = tc ? sms : 4 * sms;
-  const int64_t chunks = (tokens / requests + 127) / 128;
+  const int64_t resident = tc ? sms : 4 * sms, step = tc ? 128 : 16;
+  const int64_t steps = (tokens / requests + step - 1) / step;
   int64_t best = 1;
   double least = 0;
-  for (int64_t cut = 1; cut <= std::min<int64_t>(chunks, 64); ++cut) {
-    const int64_t len = (chunks + cut - 1) / cut;
+  for (int64_t cut = 1; cut <= std::min<int64_t>(std::max<int64_t>(steps, 1), 64); ++cut) {
+    const int64_t len = (steps + cut - 1) / cut;
     const double waves = static_cast<double>((requests * tiles * cut + resident - 1) / resident);
-    const double cost = waves * len * (cut > 1 ? 1.5 : 1.0) + (cut > 1 ? 3.0 + 0.25 * cut : 0.0);
+    const double cost = waves * len * (cut > 1 ? 1.5 : 1.0) + (cut > 1 ? 1.0 + 0.2 * cut : 0.0);
     if (cut == 1 || cost < least) {
       least = cost;
       best = cut;
     }
   }
-  int64_t block = (chunks + best - 1) / best * 128;
+  int64_t block = (steps + best - 1) / best * step;
   // a batch whose requests need no cut may still hold one long request
-  if (best == 1) block = std::max<int64_t>(block, 2048);
-  return std::min<int64_t>(block, 1 << 19);
+  if (best == 1) block = std::max<int64_t>(block, 4 * step);
+  return std::min<int64_t>(std::max<int64_t>(block, step), 1 << 19);
 }
 
 int ss_head_state_update_validate(const ss_head_state_update_params *p) { return validate(p); }
