@@ -14,16 +14,15 @@
 //
 // One CTA carries 128 (head, p) columns, two heads of 64 or one of 128, through
 // one block of a request. C B^T and the operands C and B are shared by its heads.
-//   warps 0 - 7    mask: C B^T to its masked form, C S^T by e^L (thread = row t)
-//   warps 8 - 15   weigh: S to the chunk's start, X to w X (thread = column p)
-//   warps 16 - 23  finish: Y to the output (thread = row t), and the decays of the
-//                  chunk after the next
+//   warps 0 - 15   mask C B^T and scale C S^T by e^L, then finish the output
+//                  (thread = row t, a warp one quarter of the columns); some also
+//                  prepare the decays of the chunk after the next
+//   warps 16 - 23  weigh: S to the chunk's start, X to w X (thread = column p)
 //   warp 24        loads the chunks by TMA (boxes of 128 tokens x 64 values),
 //                  warp 27 stores the output the same way
 //   warp 25        issues the products for Y, warp 26 those for S (tcgen05,
 //                  accumulators in tensor memory)
-// The groups run on different chunks: while one chunk's output is finished, the
-// next is masked and weighed.
+// Both groups run side by side: what is between chunks is only S.
 // Tensor memory, 512 columns: C B^T, overlaid block by block by the masked forms
 // as the product's A operand (128); Y (128); S (128); w X as A operand (128).
 //
@@ -42,8 +41,8 @@ namespace ssk {
 namespace {
 
 constexpr int kBox = 16384;      // 128 rows of 128 bytes
-constexpr int kRing = 10;        // boxes in flight; even, so that a pair is adjacent
-constexpr int kTcThreads = 896;  // 3 groups of 8 warps, then TMA loads, 2 x MMA, TMA stores
+constexpr int kBoxes = 10;       // X twice, B (then z) twice, C once, two boxes each
+constexpr int kTcThreads = 896;  // 16 row warps, 8 column warps, TMA loads, 2 x MMA, TMA stores
 constexpr uint32_t kColG = 0, kColY = 128, kColS = 256, kColX = 384;
 constexpr int32_t kErrTcWait = 16;
 
@@ -52,13 +51,15 @@ struct TcMaps {
 };
 
 struct Shared {
-  uint64_t full[kRing], empty[kRing];
-  uint64_t xw0, xw0_done, masked, y_done, y_free, xw1, s_done, s_ready, gy_done;
-  // A group waits on these that does not hold up the one that arrives for a chunk
-  // or more: one barrier for each chunk that the latter can be ahead.
-  uint64_t x_read[2];    // weighing -> finishing (and products for Y): X's columns are read, its rows may be overwritten
-  uint64_t finished[4];  // finishing -> storing
-  uint64_t prepared[4];  // finishing -> masking and weighing: the chunk's decays
+  uint64_t full_x[2], full_b[2], full_c, full_z[2];  // loaded
+  uint64_t empty_x[2], empty_b[2], empty_c;          // may be loaded again
+  uint64_t masked, y_done, y_free, s_ready, gy_done;
+  uint64_t weighed[2], gained[2];  // by buffer of w X: written; taken in by S
+  // Who waits on these does not hold up who arrives for a chunk or more: one
+  // barrier for each chunk that the latter can be ahead.
+  uint64_t x_read[2];    // columns -> rows (and products for Y): X's columns are read, its rows may be overwritten
+  uint64_t finished[4];  // rows -> storing
+  uint64_t prepared[4];  // rows -> rows and columns: the chunk's decays
   uint32_t tmem;
   int dead;
   // of chunk c in stage c % 4, by head of the tile
@@ -109,15 +110,26 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 16 columns of the warp's 32 lanes (thread = lane); the load is complete on return.
-__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&v)[16]) {
+// 16 columns of the warp's 32 lanes (thread = lane). The values of tm_ld16_async
+// are there after tm_wait on the same registers.
+__device__ __forceinline__ void tm_ld16_async(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
         "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tm_wait(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&v)[16]) {
+  tm_ld16_async(addr, v);
+  tm_wait(v);
 }
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -149,7 +161,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *tm, const void *
                : "memory");
 }
 
-// Barrier of the 8 weighing warps.
+// Barrier of the 8 column warps.
 __device__ __forceinline__ void sync_weighers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // One arrival per warp, after all its lanes.
 __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
@@ -214,16 +226,12 @@ template <typename T, int PW, int NS, bool SUMMARY, bool GATE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     ss_head_scan_tc_kernel(const __grid_constant__ HeadScanParams p, const __grid_constant__ TcMaps maps) {
   constexpr int HT = 128 / PW;
-  constexpr int NB = NS / 64;                           // boxes of B (and of C)
-  constexpr int oC = 0, oB = SUMMARY ? 0 : NB, oX = oB + NB, oZ = oX + 2;
-  constexpr int BPC = GATE ? oZ + 2 : oZ;               // ring places per chunk
+  constexpr int NB = NS / 64;  // boxes of B (and of C)
   constexpr int NT = Terms<T>::N;
   constexpr int NH = NS / 2;                            // states per thread of a column
-  // a product reads two boxes as one operand: such pairs start on an even place
-  static_assert(SUMMARY ? NB == 1 || BPC % 2 == 0 : BPC % 2 == 0 && oX % 2 == 0, "pairs of boxes are adjacent");
   extern __shared__ unsigned char raw[];
   unsigned char *ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  unsigned char *s16 = ring + kRing * kBox;             // S in 16 bits: [NB][128 p][64 n], swizzled
+  unsigned char *s16 = ring + kBoxes * kBox;            // S in 16 bits: [NB][128 p][64 n], swizzled
   Shared &sh = *reinterpret_cast<Shared *>(s16 + NB * kBox);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // thread = column: its head, row of the state and half of the states
   const int wg = (warp >> 2) & 1, wq = warp & 3;
   const int pc = wq * 32 + lane, hs = HT == 2 ? pc >> 6 : 0, pp = HT == 2 ? pc & 63 : pc;
-  const bool pin = warp >= 8 && warp < 16 && h0 + hs < hend && pp < p.headdim;
+  const bool pin = warp >= 16 && warp < 24 && h0 + hs < hend && pp < p.headdim;
   const int n0 = wg * NH, nv = min(max(p.dstate - n0, 0), NH);  // a multiple of 8
   const long long pn = (long long)p.headdim * p.dstate;
   float *cache = kept ? p.state + slot * p.ss[0] + (h0 + hs) * p.ss[1] + (long long)pp * p.dstate + n0 : nullptr;
@@ -271,23 +279,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.full_x[i], 1);
+      mbar_init(&sh.full_b[i], 1);
+      mbar_init(&sh.full_z[i], 1);
+      mbar_init(&sh.empty_x[i], 1);
+      mbar_init(&sh.empty_b[i], SUMMARY ? 1 : 2);  // both kinds of products read B
     }
-    mbar_init(&sh.xw0, 8);
-    mbar_init(&sh.xw1, 8);
-    mbar_init(&sh.masked, 8);
+    mbar_init(&sh.full_c, 1);
+    mbar_init(&sh.empty_c, 1);
+    mbar_init(&sh.masked, 16);
     mbar_init(&sh.s_ready, 8);
-    mbar_init(&sh.y_free, 8);
-    mbar_init(&sh.xw0_done, 1);
+    mbar_init(&sh.y_free, 16);
     mbar_init(&sh.y_done, 1);
-    mbar_init(&sh.s_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.weighed[i], 8);
+      mbar_init(&sh.gained[i], 1);
+    }
     mbar_init(&sh.gy_done, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.x_read[i], 8);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.finished[i], 8);
-      mbar_init(&sh.prepared[i], 8);
+      mbar_init(&sh.finished[i], 16);
+      mbar_init(&sh.prepared[i], 4 * HT);
     }
     sh.dead = 0;
     fence_barrier_init();
@@ -303,44 +316,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t lane_at = (uint32_t)(wq * 32) << 16;
   volatile int *dead = &sh.dead;
   const int chunks = (size + 127) / 128;
-  auto box = [&](int c, int o) { return ring + ((c * BPC + o) % kRing) * kBox; };
-  auto full = [&](int c, int o) {
-    const int i = c * BPC + o;
-    wait_tc(&sh.full[i % kRing], (i / kRing) & 1, dead, p.err);
-  };
-  auto release = [&](int c, int o, int n) {
-    for (int k = 0; k < n; ++k) mbar_arrive(&sh.empty[(c * BPC + o + k) % kRing]);
-  };
+  auto xbox = [&](int c, int k) { return ring + (2 * (c & 1) + k) * kBox; };
+  auto bbox = [&](int c, int k) { return ring + (4 + 2 * (c & 1) + k) * kBox; };  // later in the chunk z's
+  unsigned char *const cbox = ring + 8 * kBox;
+  auto full = [&](uint64_t *bars, int c) { wait_tc(&bars[c & 1], (c >> 1) & 1, dead, p.err); };
 
   if (warp == 24) {
     // ---- TMA ----
     if (lane == 0) {
-      int issued = 0;
+      // C has one place: the next chunk's takes it once this chunk's products with
+      // it are done. z takes the place of its chunk's B.
+      int nx = 0, nb = 0, nc = 0, nz = 0;  // loads under way or done
+      auto load_z = [&](int c) {
+        if (!wait_tc(&sh.empty_b[c & 1], (c >> 1) & 1, dead, p.err)) return;
+        mbar_arrive_expect_tx(&sh.full_z[c & 1], 2 * kBox);
+        for (int k = 0; k < 2; ++k)
+          tma_load_3d(bbox(c, k), &maps.z, &sh.full_z[c & 1], HT == 2 ? 0 : 64 * k, HT == 2 ? h0 + k : h0, first + c * 128);
+        ++nz;
+      };
       for (int c = 0; c < chunks && !*dead; ++c) {
-        const int t = first + c * 128;
-        for (int o = 0; o < BPC; ++o) {
-          const int i = c * BPC + o, place = i % kRing, use = i / kRing;
-          if (use > 0 && !wait_tc(&sh.empty[place], (use - 1) & 1, dead, p.err)) break;
-          unsigned char *dst = ring + place * kBox;
-          mbar_arrive_expect_tx(&sh.full[place], kBox);
-          issued = i + 1;
-          if (o >= oX) {
-            const int k = (o - oX) & 1;
-            const CUtensorMap *m = o >= oZ ? &maps.z : &maps.x;
-            tma_load_3d(dst, m, &sh.full[place], HT == 2 ? 0 : 64 * k, HT == 2 ? h0 + k : h0, t);
-          } else if (o >= oB) {
-            tma_load_3d(dst, &maps.B, &sh.full[place], 64 * (o - oB), grp, t);
-          } else {
-            tma_load_3d(dst, &maps.C, &sh.full[place], 64 * (o - oC), grp, t);
-          }
-        }
+        const int t = first + c * 128, before = ((c >> 1) - 1) & 1;
+        if (c >= 2 && !wait_tc(&sh.empty_x[c & 1], before, dead, p.err)) break;
+        mbar_arrive_expect_tx(&sh.full_x[c & 1], 2 * kBox);
+        for (int k = 0; k < 2; ++k)
+          tma_load_3d(xbox(c, k), &maps.x, &sh.full_x[c & 1], HT == 2 ? 0 : 64 * k, HT == 2 ? h0 + k : h0, t);
+        ++nx;
+        if (!GATE && c >= 2 && !wait_tc(&sh.empty_b[c & 1], before, dead, p.err)) break;
+        mbar_arrive_expect_tx(&sh.full_b[c & 1], NB * kBox);
+        for (int k = 0; k < NB; ++k) tma_load_3d(bbox(c, k), &maps.B, &sh.full_b[c & 1], 64 * k, grp, t);
+        ++nb;
+        if (SUMMARY) continue;
+        if (c >= 1 && !wait_tc(&sh.empty_c, (c - 1) & 1, dead, p.err)) break;
+        mbar_arrive_expect_tx(&sh.full_c, NB * kBox);
+        for (int k = 0; k < NB; ++k) tma_load_3d(cbox + k * kBox, &maps.C, &sh.full_c, 64 * k, grp, t);
+        ++nc;
+        if (GATE && c >= 1) load_z(c - 1);
       }
+      if (GATE && !*dead) load_z(chunks - 1);
       // nothing of this block's copies is left in flight, whatever became of the rest
-      for (int i = max(0, issued - kRing); i < issued; ++i) {
-        const uint32_t parity = (i / kRing) & 1;
+      auto landed = [&](uint64_t *bar, uint32_t parity) {
         for (uint32_t k = 0; k < kMaxWaitIters; ++k)
-          if (mbar_try_wait(&sh.full[i % kRing], parity)) break;
-      }
+          if (mbar_try_wait(bar, parity)) return;
+      };
+      for (int i = max(0, nx - 2); i < nx; ++i) landed(&sh.full_x[i & 1], (i >> 1) & 1);
+      for (int i = max(0, nb - 2); i < nb; ++i) landed(&sh.full_b[i & 1], (i >> 1) & 1);
+      for (int i = max(0, nz - 2); i < nz; ++i) landed(&sh.full_z[i & 1], (i >> 1) & 1);
+      if (nc > 0) landed(&sh.full_c, (nc - 1) & 1);
     }
   } else if (warp == 25) {
     // ---- products for Y ----
@@ -351,10 +372,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const uint32_t ph = c & 1;
-        for (int o = 0; o < 2 * NB; ++o) full(c, oC + o);
+        full(sh.full_b, c);
+        wait_tc(&sh.full_c, ph, dead, p.err);
         if (c > 0) wait_tc(&sh.y_done, ph ^ 1, dead, p.err);  // the masked forms' columns are free again
         fence_after();
-        const uint64_t cd = smem_desc(smem_u32(box(c, oC)), 16, 1024), bd = smem_desc(smem_u32(box(c, oB)), 16, 1024);
+        const uint64_t cd = smem_desc(smem_u32(cbox), 16, 1024), bd = smem_desc(smem_u32(bbox(c, 0)), 16, 1024);
         __syncwarp();
         if (elect() && !*dead) {
 #pragma unroll
@@ -375,12 +397,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           commit(&sh.gy_done);
         }
-        full(c, oX);
-        full(c, oX + 1);
+        full(sh.full_x, c);
         if (size - c * 128 < 128) wait_tc(&sh.x_read[c & 1], (c >> 1) & 1, dead, p.err);  // rows past the request's end are cleared
         wait_tc(&sh.masked, ph, dead, p.err);
         fence_after();
-        const uint64_t xd = smem_desc(smem_u32(box(c, oX)), kBox, 1024);
+        const uint64_t xd = smem_desc(smem_u32(xbox(c, 0)), kBox, 1024);
         __syncwarp();
         if (elect() && !*dead) {
 #pragma unroll
@@ -398,23 +419,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const uint32_t ph = c & 1;
-      for (int o = 0; o < NB; ++o) full(c, oB + o);
+      full(sh.full_b, c);
       wait_tc(&sh.s_ready, ph, dead, p.err);
+      const uint64_t bd = smem_desc(smem_u32(bbox(c, 0)), kBox, 1024);
 #pragma unroll 1
-      for (int round = 0; round < 2; ++round) {
-        wait_tc(round ? &sh.xw1 : &sh.xw0, ph, dead, p.err);
+      for (int q = 0; q < 4; ++q) {  // 32 tokens
+        wait_tc(&sh.weighed[q & 1], (q >> 1) & 1, dead, p.err);  // a buffer's second use in the chunk
         fence_after();
-        const uint64_t bd = smem_desc(smem_u32(box(c, oB)) + round * 64 * 128, kBox, 1024);
         __syncwarp();
         if (elect() && !*dead) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int e = 0; e < NT; ++e)
-                mma_ts(tm + kColS, tm + kColX + 64 * q + 16 * e + 8 * k, bd + (((q * 32 + k * 16) * 128) >> 4), id_s, true);
-          commit(round ? &sh.s_done : &sh.xw0_done);
+            for (int e = 0; e < NT; ++e)
+              mma_ts(tm + kColS, tm + kColX + 64 * (q & 1) + 16 * e + 8 * k, bd + (((q * 32 + k * 16) * 128) >> 4), id_s, true);
+          commit(&sh.gained[q & 1]);
+          if (q == 3) commit(&sh.empty_b[c & 1]);
         }
       }
     }
@@ -427,40 +447,228 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (size - c * 128 >= 128 && !*dead) {
           for (int k = 0; k < 2; ++k)
             if (HT == 1 || h0 + k < hend)
-              tma_store_3d(&maps.out, box(c, oX + k), HT == 2 ? 0 : 64 * k, HT == 2 ? h0 + k : h0, first + c * 128);
+              tma_store_3d(&maps.out, xbox(c, k), HT == 2 ? 0 : 64 * k, HT == 2 ? h0 + k : h0, first + c * 128);
           asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
-        release(c, oX, BPC - oX);
+        mbar_arrive(&sh.empty_x[c & 1]);  // and z's place
       }
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
-  } else if (warp < 8) {
-    // ---- masking warps: thread = row t ----
+  } else if (warp >= 16) {
+    // ---- column warps: thread = column p ----
+    float decay = 0.f, scale = 1.f;  // of this column's head: log2 decay so far; w's scale in this chunk
+    float fade0 = 0.f, fade1 = 0.f, fade2 = 0.f;  // from the ends of the first 32 tokens, ... to the chunk's end, times scale
+#pragma unroll 1
+    for (int c = 0; c <= chunks; ++c) {
+      const uint32_t ph = c & 1, before = ph ^ 1;
+      const bool more = c < chunks;
+      const float unscale = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / scale, a power of two
+      uint32_t col = 0;              // this column of X, in row 0 of a swizzle atom
+      const float *cf = nullptr;
+      float keep = 0.f;              // decay of this chunk, times its scale
+      if (more) {
+        wait_tc(&sh.prepared[c & 3], (c >> 2) & 1, dead, p.err);
+        const float *t = sh.tot[c & 3][hs];
+        const float t3 = t[3], t2 = t3 + t[2], t1 = t2 + t[1], t0 = t1 + t[0];
+        decay += t0;
+        keep = ex2(t0);
+        fade0 = ex2(t1);
+        fade1 = ex2(t2);
+        fade2 = ex2(t3);
+        if (NT == 2) {  // the power of two that brings the chunk's largest w to [1/2, 1)
+          const float *top = sh.top[c & 3][hs];
+          const float m = fmaxf(fmaxf(top[0] * fade0, top[1] * fade1), fmaxf(top[2] * fade2, top[3]));
+          const int e = (int)(__float_as_uint(m) >> 23);
+          scale = e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
+          keep *= scale;
+          fade0 *= scale;
+          fade1 *= scale;
+          fade2 *= scale;
+        }
+        const int valid = min(128, size - c * 128);
+        full(sh.full_x, c);
+        if (valid < 128) {  // rows of the next request, or of nothing: 0 x anything must be 0
+          full(sh.full_b, c);
+          const int todo = (128 - valid) * 8;
+          for (int i = tid - 512; i < todo * (2 + NB); i += 256) {
+            const int o = i / todo, k = i % todo;
+            unsigned char *b = o < 2 ? xbox(c, o) : bbox(c, o - 2);
+            *reinterpret_cast<uint4 *>(b + (valid + k / 8) * 128 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          sync_weighers();
+        }
+        col = smem_u32(xbox(c, pc >> 6)) + wg * 16 * 128 + (pc & 63) * 2;
+        cf = sh.colf[c & 3][hs] + wg * 16;
+      }
+      // Four times 32 tokens of w X, in two buffers: the products take in one while
+      // the other is written. The first is weighed before S is handed on, which has
+      // to wait for the products of the chunk before.
+#pragma unroll 1
+      for (int q = more ? 0 : 1; q < 4; ++q) {
+        if (q == 1) {
+          // S after the chunk before (at first, the block's start): its 16-bit form for
+          // this chunk's product, and its decayed, scaled form as the accumulator
+          if (c > 0) {
+            wait_tc(&sh.gained[1], 1, dead, p.err);  // the chunk's last; and all its columns of X are read
+            if (!SUMMARY) wait_tc(&sh.gy_done, before, dead, p.err);
+            fence_after();
+            if (SUMMARY && tid == 512) mbar_arrive(&sh.empty_x[(c - 1) & 1]);
+          }
+#pragma unroll 1
+          for (int n = 0; n < NH; n += 16) {
+            float v[16];
+            if (c > 0) {
+              uint32_t s[16];
+              tm_ld16(tm + lane_at + kColS + n0 + n, s);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = NT == 2 ? __uint_as_float(s[i]) * unscale : __uint_as_float(s[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = 0.f;
+              auto fold = [&](const float *src, float k) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                  if (n + i < nv) {
+                    const float4 f = *reinterpret_cast<const float4 *>(src + n + i);
+                    v[i] = fmaf(k, v[i], f.x);
+                    v[i + 1] = fmaf(k, v[i + 1], f.y);
+                    v[i + 2] = fmaf(k, v[i + 2], f.z);
+                    v[i + 3] = fmaf(k, v[i + 3], f.w);
+                  }
+              };
+              if (pin) {
+                if (index == 0) {
+                  if (goes_on) fold(!SUMMARY && last > 0 ? entry(last) : cache, 0.f);
+                } else if (!SUMMARY) {
+#pragma unroll 1
+                  for (int i = 0; i < index; ++i) fold(entry(i), ex2(*decay_of(i)));
+                }
+              }
+            }
+            if (more) {
+              if (!SUMMARY) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 8) {
+                  uint4 w4;  // a 16-byte piece of the row
+                  w4.x = pack2<T>(v[i], v[i + 1]);
+                  w4.y = pack2<T>(v[i + 2], v[i + 3]);
+                  w4.z = pack2<T>(v[i + 4], v[i + 5]);
+                  w4.w = pack2<T>(v[i + 6], v[i + 7]);
+                  *reinterpret_cast<uint4 *>(s16 + ((n0 + n) / 64) * kBox + swz(pc, ((n0 + n + i) % 64) * 2)) = w4;
+                }
+              }
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float2 k = upk(mul2(pk(v[i], v[i + 1]), pk(keep, keep)));
+                w[i] = __float_as_uint(k.x);
+                w[i + 1] = __float_as_uint(k.y);
+              }
+              tm_st16(tm + lane_at + kColS + n0 + n, w);
+            } else if (pin && !*dead && (SUMMARY || (index == last && kept))) {
+              float *dst = (SUMMARY ? entry(index) : cache) + n;
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                if (n + i < nv) *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+          if (more) {
+            if (!SUMMARY) fence_proxy_async();
+            wait_st();
+            fence_before();
+            arrive_warp(&sh.s_ready, lane);
+          } else if (SUMMARY && pin && pp == 0 && wg == 0 && !*dead) {
+            *decay_of(index) = decay;
+          }
+          if (!more) break;
+        }
+        // w X as the product's A operand: thread = column, a warpgroup half of the tokens
+        const int use = 2 * c + (q >> 1);
+        if (use > 0) {
+          wait_tc(&sh.gained[q & 1], (use - 1) & 1, dead, p.err);
+          fence_after();
+        }
+        const float f = q == 0 ? fade0 : q == 1 ? fade1 : q == 2 ? fade2 : scale;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          uint32_t t[NT][4];
+          const float4 wa = *reinterpret_cast<const float4 *>(cf);
+          const float4 wb = *reinterpret_cast<const float4 *>(cf + 4);
+          const f2 f2f = pk(f, f);
+          const f2 w[4] = {mul2(pk(wa.x, wa.y), f2f), mul2(pk(wa.z, wa.w), f2f), mul2(pk(wb.x, wb.y), f2f), mul2(pk(wb.z, wb.w), f2f)};
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = lds_16<T>((col ^ (k << 4)) + k * 128);
+          col += 8 * 128;
+          cf += 8;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t a[NT];
+            Terms<T>::split(mul2(pk(x[2 * k], x[2 * k + 1]), w[k]), a);
+#pragma unroll
+            for (int e = 0; e < NT; ++e) t[e][k] = a[e];
+          }
+#pragma unroll
+          for (int e = 0; e < NT; ++e) tm_st4(tm + lane_at + kColX + 64 * (q & 1) + 16 * e + 8 * wg + 4 * i, t[e]);
+        }
+        col += 16 * 128;
+        cf += 16;
+        wait_st();
+        fence_before();
+        arrive_warp(&sh.weighed[q & 1], lane);
+      }
+      if (!SUMMARY && more) arrive_warp(&sh.x_read[ph], lane);
+    }
+    fence_before();
+  } else {
+    // ---- row warps: thread = row t; rg: a quarter of the columns, or a head to prepare ----
+    const int rg = warp >> 2;
+    const bool prepares = rg < HT;
+    const int hp = h0 + rg < hend && prepares ? h0 + rg : h0;   // the head to prepare
+    const int ho = HT == 2 ? rg >> 1 : 0;                       // the head of the columns in the tile
+    const bool hin = h0 + ho < hend;
+    const float A2 = p.A[hp] * kLog2e, bias = p.bias ? p.bias[hp] : 0.f, skip = p.D ? p.D[hin ? h0 + ho : h0] : 0.f;
     const int trow = wq * 32 + lane;
+    auto load_dt = [&](int c) -> float {
+      const int t = c * 128 + trow;
+      if (!prepares || t >= size) return 0.f;
+      const long long at = (long long)(first + t) * p.sdt[0] + hp * p.sdt[1];
+      return p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]);
+    };
+    // The decays of chunk cp are prepared between masking and finishing chunk cp - 2.
+    constexpr int kAhead = SUMMARY ? 0 : 2;
+    float raw_dt = load_dt(0);
 #pragma unroll 1
-    for (int c = 0; c < (SUMMARY ? 0 : chunks); ++c) {
-      const uint32_t ph = c & 1;
-      const int st = c & 3;
-      wait_tc(&sh.prepared[st], (c >> 2) & 1, dead, p.err);
-      wait_tc(&sh.gy_done, ph, dead, p.err);
-      fence_after();
-      if (tid == 0) release(c, oC, NB);
-      // The masked forms of 16 columns, one per head, in place of C B^T. Of the
-      // blocks of 32 a warpgroup takes 0 and 3, or 1 and 2: equal work below the
-      // diagonal.
+    for (int cp = 0; cp < chunks + kAhead; ++cp) {
+      const int c = cp - kAhead;
+      if (!SUMMARY && c >= 0) {
+        const int st = c & 3;
+        wait_tc(&sh.prepared[st], (c >> 2) & 1, dead, p.err);
+        wait_tc(&sh.gy_done, c & 1, dead, p.err);
+        fence_after();
+        if (tid == 0) {
+          mbar_arrive(&sh.empty_c);
+          mbar_arrive(&sh.empty_b[c & 1]);
+        }
+        // The masked forms of 16 columns, one per head, in place of C B^T. Of the
+        // eight pieces a warp takes rg and 7 - rg: near enough equal work below
+        // the diagonal.
 #pragma unroll 1
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const int jb = i4 < 2 ? 2 * wg + i4 : 4 - 2 * wg + i4, j = jb >> 1;
-        const uint32_t at = tm + lane_at + kColG + 16 * jb;
-        uint32_t g[16];
-        if (j <= wq) tm_ld16(at, g);
-#pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          uint32_t m[8];
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const int jb = i2 ? 7 - rg : rg, j = jb >> 1;
+          const uint32_t at = tm + lane_at + kColG + 16 * jb;
           if (j > wq) {
+            const uint32_t m[8] = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = 0;
-          } else {
+            for (int h = 0; h < HT; ++h) tm_st8(at + 8 * h, m);
+            continue;
+          }
+          uint32_t g[16];
+          tm_ld16(at, g);
+#pragma unroll
+          for (int h = 0; h < HT; ++h) {
+            uint32_t m[8];
             float l = -sh.nl[st][h][trow];
             if (j < wq) {
               for (int k = j + 1; k < wq; ++k) l += sh.tot[st][h][k];
@@ -487,213 +695,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 m[i / 2 + 1] = pack2<T>(i + 2 <= d ? v.x : 0.f, i + 3 <= d ? v.y : 0.f);
               }
             }
+            tm_st8(at + 8 * h, m);
           }
-          tm_st8(at + 8 * h, m);
         }
-      }
-      // Y = e^L (C S^T)
-      const int h = HT == 2 ? wg : 0;
-      float e = -sh.nl[st][h][trow];
-      for (int k = 0; k < wq; ++k) e += sh.tot[st][h][k];
-      e = ex2(e);
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t y[16];
-        const uint32_t at = tm + lane_at + kColY + 64 * wg + 16 * q;
-        tm_ld16(at, y);
+        // Y = e^L (C S^T), 32 columns
+        {
+          float e = -sh.nl[st][ho][trow];
+          for (int k = 0; k < wq; ++k) e += sh.tot[st][ho][k];
+          e = ex2(e);
+          const uint32_t at = tm + lane_at + kColY + 32 * rg;
+          uint32_t y[2][16];
+          tm_ld16_async(at, y[0]);
+          tm_ld16_async(at + 16, y[1]);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float2 v = upk(mul2(pku(y[i], y[i + 1]), pk(e, e)));
-          y[i] = __float_as_uint(v.x);
-          y[i + 1] = __float_as_uint(v.y);
-        }
-        tm_st16(at, y);
-      }
-      wait_st();
-      fence_before();
-      arrive_warp(&sh.masked, lane);
-    }
-    fence_before();
-  } else if (warp < 16) {
-    // ---- weighing warps: thread = column p ----
-    float decay = 0.f, scale = 1.f;  // of this column's head: log2 decay so far; w's scale in this chunk
-    float fade0 = 0.f, fade1 = 0.f;  // from the ends of the 32 tokens weighed first and second to the chunk's end, times scale
-#pragma unroll 1
-    for (int c = 0; c <= chunks; ++c) {
-      const uint32_t ph = c & 1, before = ph ^ 1;
-      const bool more = c < chunks;
-      const float unscale = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 1 / scale, a power of two
-      float keep = 0.f;              // decay of this chunk, times its scale
-      if (more) {
-        wait_tc(&sh.prepared[c & 3], (c >> 2) & 1, dead, p.err);
-        const float *t = sh.tot[c & 3][hs];
-        const float t3 = t[3], t2 = t3 + t[2], t1 = t2 + t[1], t0 = t1 + t[0];
-        decay += t0;
-        keep = ex2(t0);
-        fade0 = ex2(wg ? t2 : t1);
-        fade1 = wg ? 1.f : ex2(t3);
-        if (NT == 2) {  // the power of two that brings the chunk's largest w to [1/2, 1)
-          const float *top = sh.top[c & 3][hs];
-          const float m = fmaxf(fmaxf(top[0] * ex2(t1), top[1] * ex2(t2)), fmaxf(top[2] * ex2(t3), top[3]));
-          const int e = (int)(__float_as_uint(m) >> 23);
-          scale = e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
-          keep *= scale;
-          fade0 *= scale;
-          fade1 *= scale;
-        }
-      }
-      // S after the chunk before (at first, the block's start): its 16-bit form for
-      // this chunk's product, and its decayed, scaled form as the accumulator
-      if (c > 0) {
-        wait_tc(&sh.s_done, before, dead, p.err);  // and all columns of X are read
-        if (!SUMMARY) wait_tc(&sh.gy_done, before, dead, p.err);
-        fence_after();
-        if (tid == 256) release(c - 1, oB, SUMMARY ? NB + 2 : NB);
-      }
-#pragma unroll 1
-      for (int q = 0; q < NH / 16; ++q) {
-        float v[16];
-        const int n = 16 * q;
-        if (c > 0) {
-          uint32_t s[16];
-          tm_ld16(tm + lane_at + kColS + n0 + n, s);
+          for (int q = 0; q < 2; ++q) {
+            tm_wait(y[q]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = NT == 2 ? __uint_as_float(s[i]) * unscale : __uint_as_float(s[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.f;
-          auto fold = [&](const float *src, float k) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              if (n + i < nv) {
-                const float4 f = *reinterpret_cast<const float4 *>(src + n + i);
-                v[i] = fmaf(k, v[i], f.x);
-                v[i + 1] = fmaf(k, v[i + 1], f.y);
-                v[i + 2] = fmaf(k, v[i + 2], f.z);
-                v[i + 3] = fmaf(k, v[i + 3], f.w);
-              }
-          };
-          if (pin) {
-            if (index == 0) {
-              if (goes_on) fold(!SUMMARY && last > 0 ? entry(last) : cache, 0.f);
-            } else if (!SUMMARY) {
-#pragma unroll 1
-              for (int i = 0; i < index; ++i) fold(entry(i), ex2(*decay_of(i)));
+            for (int i = 0; i < 16; i += 2) {
+              const float2 v = upk(mul2(pku(y[q][i], y[q][i + 1]), pk(e, e)));
+              y[q][i] = __float_as_uint(v.x);
+              y[q][i + 1] = __float_as_uint(v.y);
             }
+            tm_st16(at + 16 * q, y[q]);
           }
-        }
-        if (more) {
-          if (!SUMMARY) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8) {
-              uint4 w4;  // a 16-byte piece of the row
-              w4.x = pack2<T>(v[i], v[i + 1]);
-              w4.y = pack2<T>(v[i + 2], v[i + 3]);
-              w4.z = pack2<T>(v[i + 4], v[i + 5]);
-              w4.w = pack2<T>(v[i + 6], v[i + 7]);
-              *reinterpret_cast<uint4 *>(s16 + ((n0 + n) / 64) * kBox + swz(pc, ((n0 + n + i) % 64) * 2)) = w4;
-            }
-          }
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float2 k = upk(mul2(pk(v[i], v[i + 1]), pk(keep, keep)));
-            w[i] = __float_as_uint(k.x);
-            w[i + 1] = __float_as_uint(k.y);
-          }
-          tm_st16(tm + lane_at + kColS + n0 + n, w);
-        } else if (pin && !*dead && (SUMMARY || (index == last && kept))) {
-          float *dst = (SUMMARY ? entry(index) : cache) + n;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            if (n + i < nv) *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
-      }
-      if (more) {
-        if (!SUMMARY) fence_proxy_async();
-        wait_st();
-        fence_before();
-        arrive_warp(&sh.s_ready, lane);
-      } else if (SUMMARY && pin && pp == 0 && wg == 0 && !*dead) {
-        *decay_of(index) = decay;
-      }
-
-      if (!more) break;
-
-      const int valid = min(128, size - c * 128);
-      full(c, oX);
-      full(c, oX + 1);
-      if (valid < 128) {  // rows of the next request, or of nothing: 0 x anything must be 0
-        for (int o = 0; o < NB; ++o) full(c, oB + o);
-        const int todo = (128 - valid) * 8;
-        for (int i = tid - 256; i < todo * (2 + NB); i += 256) {
-          const int o = i / todo, k = i % todo;
-          unsigned char *b = o < 2 ? box(c, oX + o) : box(c, oB + o - 2);
-          *reinterpret_cast<uint4 *>(b + (valid + k / 8) * 128 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        sync_weighers();
-      }
-      // w X as the product's A operand: thread = column, 32 tokens at a time
-      uint32_t col = smem_u32(box(c, oX + (pc >> 6))) + wg * 32 * 128 + (pc & 63) * 2;  // in row 0 of a swizzle atom
-      const float *cf = sh.colf[c & 3][hs] + wg * 32;
-#pragma unroll 1
-      for (int round = 0; round < 2; ++round) {
-        if (round) {
-          wait_tc(&sh.xw0_done, ph, dead, p.err);
-          fence_after();
-        }
-        const float f = round ? fade1 : fade0;
-#pragma unroll 1
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t t[NT][4];
-          const float4 wa = *reinterpret_cast<const float4 *>(cf);
-          const float4 wb = *reinterpret_cast<const float4 *>(cf + 4);
-          const f2 f2f = pk(f, f);
-          const f2 w[4] = {mul2(pk(wa.x, wa.y), f2f), mul2(pk(wa.z, wa.w), f2f), mul2(pk(wb.x, wb.y), f2f), mul2(pk(wb.z, wb.w), f2f)};
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = lds_16<T>((col ^ (k << 4)) + k * 128);
-          col += 8 * 128;
-          cf += 8;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t a[NT];
-            Terms<T>::split(mul2(pk(x[2 * k], x[2 * k + 1]), w[k]), a);
-#pragma unroll
-            for (int e = 0; e < NT; ++e) t[e][k] = a[e];
-          }
-#pragma unroll
-          for (int e = 0; e < NT; ++e) tm_st4(tm + lane_at + kColX + 64 * wg + 16 * e + i / 2, t[e]);
         }
         wait_st();
         fence_before();
-        arrive_warp(round ? &sh.xw1 : &sh.xw0, lane);
-        col += 32 * 128;
-        cf += 32;
+        arrive_warp(&sh.masked, lane);
       }
-      if (!SUMMARY) arrive_warp(&sh.x_read[ph], lane);
-    }
-    fence_before();
-  } else if (warp < 24) {
-    // ---- finishing warps: thread = row t; warpgroup wg prepares head wg ----
-    const int hr = HT == 2 ? wg : 0;
-    const bool hin = h0 + hr < hend;
-    const int hh = hin ? h0 + hr : h0;
-    const float skip = p.D ? p.D[hh] : 0.f, A2 = p.A[hh] * kLog2e, bias = p.bias ? p.bias[hh] : 0.f;
-    const int trow = wq * 32 + lane;
-    auto load_dt = [&](int c) -> float {
-      const int t = c * 128 + trow;
-      if (t >= size) return 0.f;
-      const long long at = (long long)(first + t) * p.sdt[0] + hh * p.sdt[1];
-      return p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]);
-    };
-    // The decays are prepared two chunks ahead of the output.
-    constexpr int kAhead = SUMMARY ? 0 : 2;
-    float raw_dt = load_dt(0);
-#pragma unroll 1
-    for (int cp = 0; cp < chunks + kAhead; ++cp) {
-      if (cp < chunks) {
+      if (cp < chunks && prepares) {
         const int st = cp & 3;
         float dt = raw_dt + bias;
         if (p.softplus) dt = softplus_f(dt);
@@ -708,15 +738,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // what follows this token, without the token itself
         const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
         const float cf = dt * ex2(lane < 31 ? nx : 0.f);
-        sh.nl[st][wg][trow] = -l;
-        sh.dt[st][wg][trow] = dt;
-        sh.colf[st][wg][trow] = cf;
-        if (lane == 31) sh.tot[st][wg][wq] = l;
+        sh.nl[st][rg][trow] = -l;
+        sh.dt[st][rg][trow] = dt;
+        sh.colf[st][rg][trow] = cf;
+        if (lane == 31) sh.tot[st][rg][wq] = l;
         if (NT == 2) {
           float m = fabsf(cf);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (lane == 0) sh.top[st][wg][wq] = m;
+          if (lane == 0) sh.top[st][rg][wq] = m;
         }
         arrive_warp(&sh.prepared[st], lane);
         raw_dt = load_dt(cp + 1);
@@ -725,55 +755,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wait_tc(&sh.s_ready, cp & 1, dead, p.err);  // the chunk's decays are taken up, its predecessor's no longer needed
         continue;
       }
-      const int c = cp - kAhead;
       if (c < 0) continue;
-      // the output, in place of X's rows
+      // the output, 32 columns, in place of X's rows
       const int valid = min(128, size - c * 128);
-      full(c, oX + wg);
-      if (GATE) full(c, oZ + wg);
+      full(sh.full_x, c);
       wait_tc(&sh.x_read[c & 1], (c >> 1) & 1, dead, p.err);
       wait_tc(&sh.y_done, c & 1, dead, p.err);
+      if (GATE) full(sh.full_z, c);
       fence_after();
-      unsigned char *xr = box(c, oX + wg);
-      const unsigned char *zr = box(c, oZ + wg);
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t y[16];
-        tm_ld16(tm + lane_at + kColY + 64 * wg + 16 * q, y);
-        if (q == 3) {
-          fence_before();
-          arrive_warp(&sh.y_free, lane);
-        }
+      unsigned char *xr = xbox(c, rg >> 1);
+      const unsigned char *zr = bbox(c, rg >> 1);
+      uint32_t y[2][16];
+      tm_ld16_async(tm + lane_at + kColY + 32 * rg, y[0]);
+      tm_ld16_async(tm + lane_at + kColY + 32 * rg + 16, y[1]);
+      tm_wait(y[0]);
+      tm_wait(y[1]);
+      fence_before();
+      arrive_warp(&sh.y_free, lane);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int at = swz(trow, 32 * q + 16 * k);
-          const uint4 xq = *reinterpret_cast<const uint4 *>(xr + at);
-          const uint32_t xw[4] = {xq.x, xq.y, xq.z, xq.w};
-          uint4 zq = make_uint4(0, 0, 0, 0);
-          if (GATE) zq = *reinterpret_cast<const uint4 *>(zr + at);
-          const uint32_t zw[4] = {zq.x, zq.y, zq.z, zq.w};
-          uint32_t o[4];
+      for (int k = 0; k < 4; ++k) {
+        const int at = swz(trow, 64 * (rg & 1) + 16 * k);
+        const uint4 xq = *reinterpret_cast<const uint4 *>(xr + at);
+        const uint32_t xw[4] = {xq.x, xq.y, xq.z, xq.w};
+        uint4 zq = make_uint4(0, 0, 0, 0);
+        if (GATE) zq = *reinterpret_cast<const uint4 *>(zr + at);
+        const uint32_t zw[4] = {zq.x, zq.y, zq.z, zq.w};
+        uint32_t o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f2 v = fma2(pk(skip, skip), wide<T>(xw[i]), pku(y[8 * k + 2 * i], y[8 * k + 2 * i + 1]));
-            if (GATE) {
-              const f2 zv = wide<T>(zw[i]);
-              const float2 e = upk(mul2(zv, pk(-kLog2e, -kLog2e)));
-              const float2 d = upk(add2(pk(ex2(e.x), ex2(e.y)), pk(1.f, 1.f)));
-              v = mul2(v, mul2(zv, pk(rcp(d.x), rcp(d.y))));
-            }
-            o[i] = narrow<T>(v);
+        for (int i = 0; i < 4; ++i) {
+          f2 v = fma2(pk(skip, skip), wide<T>(xw[i]), pku(y[k / 2][8 * (k % 2) + 2 * i], y[k / 2][8 * (k % 2) + 2 * i + 1]));
+          if (GATE) {
+            const f2 zv = wide<T>(zw[i]);
+            const float2 e = upk(mul2(zv, pk(-kLog2e, -kLog2e)));
+            const float2 d = upk(add2(pk(ex2(e.x), ex2(e.y)), pk(1.f, 1.f)));
+            v = mul2(v, mul2(zv, pk(rcp(d.x), rcp(d.y))));
           }
-          *reinterpret_cast<uint4 *>(xr + at) = make_uint4(o[0], o[1], o[2], o[3]);
+          o[i] = narrow<T>(v);
         }
+        *reinterpret_cast<uint4 *>(xr + at) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      if (valid < 128 && hin && !*dead) {  // the request's last rows, as 128-byte lines
+      if (valid < 128 && hin && !*dead) {  // the request's last rows, as 64-byte pieces
         __syncwarp();
-        const int piece = lane & 7, col = (HT == 2 ? 0 : 64 * wg) + 8 * piece;
+        const int piece = 4 * (rg & 1) + (lane & 3), col = (HT == 2 ? 0 : 64 * (rg >> 1)) + 8 * piece;
         if (col < p.headdim) {
 #pragma unroll 1
-          for (int t = wq * 32 + (lane >> 3); t < min(valid, wq * 32 + 32); t += 4)
-            *reinterpret_cast<uint4 *>(out + (long long)(first + c * 128 + t) * p.so[0] + hh * p.so[1] + col) =
+          for (int t = wq * 32 + (lane >> 2); t < min(valid, wq * 32 + 32); t += 8)
+            *reinterpret_cast<uint4 *>(out + (long long)(first + c * 128 + t) * p.so[0] + (h0 + ho) * p.so[1] + col) =
                 *reinterpret_cast<const uint4 *>(xr + swz(t, 16 * piece));
         }
       }
@@ -792,7 +819,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 template <typename T, int PW, int NS, bool GATE>
 cudaError_t go(const HeadScanParams &p, const TcMaps &maps, cudaStream_t s) {
-  constexpr int smem = kRing * kBox + NS / 64 * kBox + (int)sizeof(Shared) + 1024;
+  constexpr int smem = kBoxes * kBox + NS / 64 * kBox + (int)sizeof(Shared) + 1024;
   const int ht = 128 / PW;
   const long long tiles = (long long)(p.heads / p.hpg) * ((p.hpg + ht - 1) / ht);
   const long long ctas = tiles * (p.t.max_blocks + 1);
