@@ -624,8 +624,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else {
     // ---- row warps: thread = row t; rg: a quarter of the columns, or a head to prepare ----
     const int rg = warp >> 2;
-    const bool prepares = rg < HT;
-    const int hp = h0 + rg < hend && prepares ? h0 + rg : h0;   // the head to prepare
+    // The last rows have most columns to mask, and their diagonal ones fall to the
+    // first two quarters: the other two prepare.
+    const int tp = rg - 2;                                      // the tile's head to prepare
+    const bool prepares = tp >= 0 && tp < HT;
+    const int hp = prepares && h0 + tp < hend ? h0 + tp : h0;
     const int ho = HT == 2 ? rg >> 1 : 0;                       // the head of the columns in the tile
     const bool hin = h0 + ho < hend;
     const float A2 = p.A[hp] * kLog2e, bias = p.bias ? p.bias[hp] : 0.f, skip = p.D ? p.D[hin ? h0 + ho : h0] : 0.f;
@@ -738,15 +741,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // what follows this token, without the token itself
         const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
         const float cf = dt * ex2(lane < 31 ? nx : 0.f);
-        sh.nl[st][rg][trow] = -l;
-        sh.dt[st][rg][trow] = dt;
-        sh.colf[st][rg][trow] = cf;
-        if (lane == 31) sh.tot[st][rg][wq] = l;
+        sh.nl[st][tp][trow] = -l;
+        sh.dt[st][tp][trow] = dt;
+        sh.colf[st][tp][trow] = cf;
+        if (lane == 31) sh.tot[st][tp][wq] = l;
         if (NT == 2) {
           float m = fabsf(cf);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (lane == 0) sh.top[st][rg][wq] = m;
+          if (lane == 0) sh.top[st][tp][wq] = m;
         }
         arrive_warp(&sh.prepared[st], lane);
         raw_dt = load_dt(cp + 1);
@@ -786,9 +789,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           f2 v = fma2(pk(skip, skip), wide<T>(xw[i]), pku(y[k / 2][8 * (k % 2) + 2 * i], y[k / 2][8 * (k % 2) + 2 * i + 1]));
           if (GATE) {
             const f2 zv = wide<T>(zw[i]);
-            const float2 e = upk(mul2(zv, pk(-kLog2e, -kLog2e)));
-            const float2 d = upk(add2(pk(ex2(e.x), ex2(e.y)), pk(1.f, 1.f)));
-            v = mul2(v, mul2(zv, pk(rcp(d.x), rcp(d.y))));
+            if constexpr (NT == 3) {  // silu(z) = z/2 + z/2 tanh(z/2): one MUFU operation, 2^-11, well inside bf16's rounding
+              const f2 hz = mul2(zv, pk(0.5f, 0.5f));
+              const float2 h = upk(hz);
+              v = mul2(v, fma2(hz, pk(tanh_approx(h.x), tanh_approx(h.y)), hz));
+            } else {
+              const float2 e = upk(mul2(zv, pk(-kLog2e, -kLog2e)));
+              const float2 d = upk(add2(pk(ex2(e.x), ex2(e.y)), pk(1.f, 1.f)));
+              v = mul2(v, mul2(zv, pk(rcp(d.x), rcp(d.y))));
+            }
           }
           o[i] = narrow<T>(v);
         }
