@@ -13,6 +13,8 @@
 #include "ss_fwd_kernel.cuh"
 #include "ss_packed.h"
 
+#include <type_traits>
+
 namespace ssk {
 namespace {
 
@@ -137,7 +139,7 @@ __device__ __forceinline__ void load_taps(const float *weight, const float *bias
 }
 
 // One output of V channels from their window and the new input, which the window takes in.
-template <int V, int W>
+template <typename T, int V, int W>
 __device__ __forceinline__ void advance(const float (&w)[W][V], const float (&b)[V], float (&win)[W - 1][V], const float (&v)[V],
                                         int act, float (&y)[V]) {
   constexpr int H = W - 1;
@@ -147,24 +149,26 @@ __device__ __forceinline__ void advance(const float (&w)[W][V], const float (&b)
 #pragma unroll
     for (int k = 0; k < H; ++k) acc = fmaf(w[k][i], win[k][i], acc);
     acc = fmaf(w[H][i], v[i], acc);
-    y[i] = act ? silu_f(acc) : acc;
+    // bf16 takes the form with one MUFU operation (2^-11), well inside its rounding
+    y[i] = !act ? acc : std::is_same<T, __nv_bfloat16>::value ? silu_fast(acc) : silu_f(acc);
 #pragma unroll
     for (int k = 0; k + 1 < H; ++k) win[k][i] = win[k + 1][i];
     win[H - 1][i] = v[i];
   }
 }
 
-// TOK tokens per thread, loaded STEP at a time. What is particular about a
+// `run` tokens per thread, loaded STEP at a time. What is particular about a
 // request's start stands once, outside the loop over its tokens: inside it, it
 // is repeated for every unrolled token and the loop no longer fits the
 // instruction cache (125 us instead of 33 at 16384 x 1792 bf16).
-template <typename T, int V, int W, int TOK, int STEP>
-__global__ void __launch_bounds__(kConvCta, 4) ss_packed_conv1d_kernel(const __grid_constant__ PackedConvParams p) {
+template <typename T, int V, int W, int STEP>
+__global__ void __launch_bounds__(kConvCta, 4) ss_packed_conv1d_kernel(const __grid_constant__ PackedConvParams p, const int run) {
   constexpr int H = W - 1;
-  const int c = (blockIdx.y * kConvCta + threadIdx.x) * V;
-  if (c >= p.dim) return;
-  const int t0 = blockIdx.x * TOK;
-  int t1 = min(t0 + TOK, p.t.tokens);
+  // a warp is 32 channel pieces wide, so that few lanes pass the last channel
+  const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * V;
+  const int t0 = (blockIdx.x * (kConvCta / 32) + (threadIdx.x >> 5)) * run;
+  if (c >= p.dim || t0 >= p.t.tokens) return;
+  int t1 = min(t0 + run, p.t.tokens);
   const T *x = static_cast<const T *>(p.x) + c;
   T *out = static_cast<T *>(p.out) + c;
   float w[W][V], b[V], win[H][V];
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kConvCta, 4) ss_packed_conv1d_kernel(const __g
       for (int s = 0; s < STEP; ++s) {
         float v[V], y[V];
         in[s].widen(v);
-        advance<V, W>(w, b, win, v, p.act, y);
+        advance<T, V, W>(w, b, win, v, p.act, y);
         store_v<T, V>(op + s * p.so, y);
       }
       xp += STEP * p.sx;
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kConvCta, 4) ss_packed_conv1d_kernel(const __g
     for (; t < to; ++t) {
       float v[V], y[V];
       load_v<T, V>(xp, v);
-      advance<V, W>(w, b, win, v, p.act, y);
+      advance<T, V, W>(w, b, win, v, p.act, y);
       store_v<T, V>(op, y);
       xp += p.sx;
       op += p.so;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kConvCta, 4) ss_packed_conv1d_kernel(const __g
   }
   const float zero[V] = {};
 #pragma unroll 1
-  for (t = max(t0, live); t < min(t0 + TOK, p.t.tokens); ++t) store_v<T, V>(out + (long long)t * p.so, zero);
+  for (t = max(t0, live); t < min(t0 + run, p.t.tokens); ++t) store_v<T, V>(out + (long long)t * p.so, zero);
 }
 
 // ROWS requests per thread, one after another on the same taps; the loads of all
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kConvCta) ss_packed_conv1d_update_kernel(const
     if (slot[i] >= 0 && slot[i] < p.slots) {
       float v[V];
       in[i].widen(v);
-      advance<V, W>(w, b, win[i], v, p.act, y);
+      advance<T, V, W>(w, b, win[i], v, p.act, y);
       store_window<T, V, H>(static_cast<T *>(p.state) + slot[i] * p.ss + (long long)c * H, win[i]);
     }
     store_v<T, V>(out, y);
@@ -298,9 +302,16 @@ __global__ void __launch_bounds__(kConvCta) ss_packed_conv1d_update_kernel(const
 
 template <typename T, int V, int W>
 void go(const PackedConvParams &p, cudaStream_t s) {
-  constexpr int TOK = 32, STEP = V == 1 ? 16 : 8;
-  const dim3 grid((p.t.tokens + TOK - 1) / TOK, (p.dim + kConvCta * V - 1) / (kConvCta * V));
-  ss_packed_conv1d_kernel<T, V, W, TOK, STEP><<<grid, kConvCta, 0, s>>>(p);
+  // Runs that fill the SMs once: 4 CTAs of the 16-byte form fit one SM (128
+  // registers a thread), 10 of the other. Longer ones leave SMs idle, shorter ones
+  // a part of a second wave (31.5 us against 26 at 16384 x 1792 bf16, runs of 32
+  // against 56).
+  constexpr int STEP = V == 1 ? 16 : 8, resident = V == 1 ? 10 : 4;
+  const int cols = (p.dim + 32 * V - 1) / (32 * V), warps = 152 * resident * (kConvCta / 32);
+  const long long want = ((long long)p.t.tokens * cols + warps - 1) / warps;
+  const int run = (int)(want < 16 ? 16 : want > 128 ? 128 : (want + STEP - 1) / STEP * STEP);
+  const int per = run * (kConvCta / 32);
+  ss_packed_conv1d_kernel<T, V, W, STEP><<<dim3((p.t.tokens + per - 1) / per, cols), kConvCta, 0, s>>>(p, run);
 }
 template <typename T, int V, int W>
 void go(const PackedConvUpdateParams &p, cudaStream_t s) {
