@@ -380,3 +380,73 @@ def test_nothing_is_done_for_no_tokens():
     assert ssm.head_scan_fn(**q, tables=tables, state=st).shape == (0, 2, 64)
     assert torch.equal(st, before)
     assert tables.counts.tolist() == [0, 0, 0, 0]
+
+
+def test_example_serves_in_pieces():
+    import examples.packed_serving as example
+    # convolution, scan and projections each round to bf16 (2^-9) on either side, in other places
+    assert example.main() < 2e-2
+
+
+# ---- refusals ----
+
+def _step_args(n=2):
+    p, t, st = _scan_problem([1] * n, 2, 1, 64, 64, torch.bfloat16)
+    return p, t, st
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(dt=lambda p: p["dt"].to(torch.float16)), TypeError),
+    (dict(B=lambda p: p["B"].float()), TypeError),
+    (dict(C=lambda p: p["C"][:, :, :8]), TypeError),
+    (dict(z=lambda p: p["z"][:1]), TypeError),
+    (dict(A=lambda p: p["A"].double()), TypeError),
+    (dict(D=lambda p: p["D"][:1]), TypeError),
+    (dict(x=lambda p: p["x"].clone().requires_grad_()), NotImplementedError),
+    (dict(x=lambda p: p["x"].cpu()), RuntimeError),
+    (dict(A=lambda p: p["A"].cpu()), ValueError),
+])
+def test_scan_refuses(change, error):
+    p, t, st = _step_args()
+    q = p | {k: f(p) for k, f in change.items()}
+    with pytest.raises(error):
+        ssm.head_state_update(st, **q)
+    tables = ssm.request_tables(_i32([2]), 2)
+    with pytest.raises(error):
+        ssm.head_scan_fn(**q, tables=tables)
+
+
+def test_operators_refuse_what_does_not_belong_together():
+    p, t, st = _step_args(3)
+    tables = ssm.request_tables(_i32([2]), 2)
+    with pytest.raises(ValueError):
+        ssm.head_scan_fn(**p, tables=tables)           # tables of another batch
+    with pytest.raises(ValueError):
+        ssm.head_state_update(st.transpose(2, 3).contiguous().transpose(2, 3), **p)
+    with pytest.raises(TypeError):
+        ssm.head_state_update(st.bfloat16(), **p)
+    with pytest.raises(TypeError):
+        ssm.head_state_update(st, slots=_i32([0, 1]), **p)
+    with pytest.raises(api.SSError) as e:
+        ssm.head_state_update(st[:2], **p)             # three rows, two slots, no map
+    assert e.value.status == 2
+    with pytest.raises(api.SSError) as e:              # 257 states
+        q, _, st2 = _scan_problem([1], 1, 1, 8, 257, torch.float32)
+        ssm.head_state_update(st2, **q)
+    assert e.value.status == 7
+    c, ct = _conv_problem([3], 16, 4, torch.float32)
+    with pytest.raises(NotImplementedError):
+        ssm.packed_conv1d_update(c["x"], c["conv_state"], c["weight"], activation="gelu")
+    with pytest.raises(TypeError):
+        ssm.packed_conv1d_update(c["x"], c["conv_state"][:, :, :2], c["weight"])
+    with pytest.raises(api.SSError) as e:
+        ssm.packed_conv1d_update(c["x"], torch.zeros(3, 16, 4, device="cuda"), torch.zeros(16, 5, device="cuda"))
+    assert e.value.status == 7
+    with pytest.raises(ValueError):
+        ssm.request_tables(_i32([1]), 1, free_slots=_i32([0]))
+    with pytest.raises(TypeError):
+        ssm.request_tables(torch.ones(2, device="cuda"), 2)
+    with pytest.raises(ValueError):
+        ssm.request_tables(_i32([1]), 1, block=0)
+    with pytest.raises(RuntimeError):
+        ssm.request_tables(torch.ones(2, dtype=torch.int32), 2)
