@@ -41,6 +41,8 @@ extern "C" {
  *   blocks[i]          {request, first token, tokens, index in the request} of
  *                      the i-th run of at most `block` tokens of one request;
  *                      {-1, 0, 0, 0} past the last
+ *   carried[i]         the i-th row of blocks that is not its request's last
+ *                      (tokens / block of them at most); -1 past the last
  *   slot_map[r]        slots[r] where it is >= 0, else free_slots[k] for the
  *                      k-th such request in order, else (free_slots used up or
  *                      NULL) -1; with slots NULL, r itself
@@ -60,7 +62,7 @@ typedef struct ss_request_tables_params {
   int32_t abi_version, reserved0;
   int64_t requests, tokens, block, max_blocks, free;
   const int32_t *lengths, *context, *slots, *free_slots;
-  int32_t *offsets, *token_request, *token_position, *blocks, *slot_map, *counts;
+  int32_t *offsets, *token_request, *token_position, *blocks, *carried, *slot_map, *counts;
 } ss_request_tables_params;
 
 int ss_request_tables_validate(const ss_request_tables_params *p);
@@ -70,7 +72,7 @@ int ss_request_tables(const ss_request_tables_params *p, void *stream);
  * and the context it was given, or NULL). */
 typedef struct ss_packed_tables {
   int64_t requests, tokens, block, max_blocks;
-  const int32_t *offsets, *token_request, *blocks, *slot_map, *counts, *context;
+  const int32_t *offsets, *token_request, *blocks, *carried, *slot_map, *counts, *context;
 } ss_packed_tables;
 
 /*

@@ -25,7 +25,7 @@ def softplus(v):
 
 
 def request_tables(lengths, tokens, context=None, slots=None, free_slots=None, block=512):
-    """dict of offsets, token_request, token_position, blocks, slots, counts."""
+    """dict of offsets, token_request, token_position, blocks, slots, carried, counts."""
     lengths, context, slots, free = _ints(lengths), _ints(context), _ints(slots), _ints(free_slots) or []
     errors, offsets, taken, got = 0, [0], 0, []
     req, pos, blocks = [-1] * tokens, [0] * tokens, []
@@ -46,9 +46,11 @@ def request_tables(lengths, tokens, context=None, slots=None, free_slots=None, b
             else:
                 slot, errors = -1, errors | 4
         got.append(slot)
+    carried = [i for i, b in enumerate(blocks) if b[1] + b[2] < offsets[b[0] + 1]]
     rows = blocks + [[-1, 0, 0, 0]] * (tokens // block + min(len(lengths), tokens) - len(blocks))
     return {"offsets": np.array(offsets), "token_request": np.array(req, dtype=int), "token_position": np.array(pos, dtype=int),
             "blocks": np.array(rows, dtype=int).reshape(-1, 4), "slots": np.array(got),
+            "carried": np.array(carried + [-1] * (tokens // block - len(carried)), dtype=int),
             "counts": np.array([offsets[-1], len(blocks), taken, errors])}
 
 

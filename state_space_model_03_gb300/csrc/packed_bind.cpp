@@ -150,7 +150,7 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // request_tables(lengths, num_tokens, context, slots, free_slots, block) ->
-// (offsets, token_request, token_position, blocks, slots, counts, plan, max_blocks)
+// (offsets, token_request, token_position, blocks, slots, counts, plan, max_blocks, context, carried)
 PyObject *request_tables(PyObject *, PyObject *const *a, Py_ssize_t given) {
   return guarded(given, 6, [&]() -> PyObject * {
     const at::Tensor &len = need(a[0], "lengths");
@@ -167,7 +167,7 @@ PyObject *request_tables(PyObject *, PyObject *const *a, Py_ssize_t given) {
     auto table = [&](int64_t k) { return at::empty({k}, len.options()); };
     // one allocation each: the tables outlive one another
     at::Tensor off = table(n + 1), req = table(tokens), pos = table(tokens), blk = at::empty({most, 4}, len.options()), slt = table(n),
-               cnt = table(4);
+               cnt = table(4), car = table(tokens / block);
     ss_request_tables_params p{};
     p.abi_version = SS_ABI_VERSION;
     p.requests = n;
@@ -183,11 +183,12 @@ PyObject *request_tables(PyObject *, PyObject *const *a, Py_ssize_t given) {
     p.token_request = req.data_ptr<int32_t>();
     p.token_position = pos.data_ptr<int32_t>();
     p.blocks = blk.data_ptr<int32_t>();
+    p.carried = car.data_ptr<int32_t>();
     p.slot_map = slt.data_ptr<int32_t>();
     p.counts = cnt.data_ptr<int32_t>();
     check(g_tables(&p, stream_of(len)));
-    Plan plan{{n, tokens, block, most, p.offsets, p.token_request, p.blocks, p.slot_map, p.counts, p.context}, len.get_device()};
-    PyObject *r = PyTuple_New(9);
+    Plan plan{{n, tokens, block, most, p.offsets, p.token_request, p.blocks, p.carried, p.slot_map, p.counts, p.context}, len.get_device()};
+    PyObject *r = PyTuple_New(10);
     if (!r) throw python_error();
     at::Tensor *ts[6] = {&off, &req, &pos, &blk, &slt, &cnt};
     for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(*ts[i])));
@@ -199,6 +200,7 @@ PyObject *request_tables(PyObject *, PyObject *const *a, Py_ssize_t given) {
       Py_INCREF(Py_None);
       PyTuple_SET_ITEM(r, 8, Py_None);
     }
+    PyTuple_SET_ITEM(r, 9, THPVariable_Wrap(std::move(car)));
     return r;
   });
 }

@@ -8,8 +8,8 @@
 // shared memory. It is bound by the fp32 operations, three for every state value
 // and token. When requests may have several blocks, a first launch brings every
 // block but the last from zero (the first one from the request's start) to its
-// end; the second folds the ends of the earlier blocks, each with the decay
-// since, into its start.
+// end, a second one carries these ends on from block to block, and the third
+// starts every block where the one before it ends.
 #include "ss_fwd_kernel.cuh"
 #include "ss_packed.h"
 
@@ -33,14 +33,14 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
   const int prow = min(kRows, p.headdim - p0);
   const int g = h / p.hpg;
   T *out = static_cast<T *>(p.out) + h * p.so[1] + p0;
-  if ((int)blockIdx.x == p.t.max_blocks) {  // past the last token: zeros
-    if (!SUMMARY) {
-      for (int t = p.t.counts[0]; t < p.t.tokens; ++t)
-        for (int i = tid; i < prow; i += kScanThreads) out[t * p.so[0] + i] = from_f<T>(0.f);
-    }
+  if (!SUMMARY && (int)blockIdx.x == p.t.max_blocks) {  // past the last token: zeros
+    for (int t = p.t.counts[0]; t < p.t.tokens; ++t)
+      for (int i = tid; i < prow; i += kScanThreads) out[t * p.so[0] + i] = from_f<T>(0.f);
     return;
   }
-  const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blockIdx.x];
+  const int blk = SUMMARY ? p.t.carried[blockIdx.x] : blockIdx.x;
+  if (blk < 0) return;
+  const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blk];
   const int r = row.x, first = row.y, size = row.z, index = row.w;
   if (r < 0) return;
   const int len = p.t.offsets[r + 1] - p.t.offsets[r];
@@ -51,10 +51,9 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
   float *cache = kept ? p.state + slot0 * p.ss[0] + h * p.ss[1] + (long long)p0 * p.dstate : nullptr;
   const long long pn = (long long)p.headdim * p.dstate;
   auto entry = [&](int i) {  // summary of the request's block i
-    return p.ws_state + ((long long)(blockIdx.x - index + i) * p.heads + h) * pn + (long long)p0 * p.dstate;
+    return p.ws_state + ((long long)(blk - index + i) * p.heads + h) * pn + (long long)p0 * p.dstate;
   };
-  auto decay_of = [&](int i) { return p.ws_decay + (long long)(blockIdx.x - index + i) * p.heads + h; };
-  if (SUMMARY && last == 0) return;
+  auto decay_of = [&](int i) { return p.ws_decay + (long long)(blk - index + i) * p.heads + h; };
 
   float s[kRowsPerLane][NPL];
   auto each = [&](auto f) {  // f(row, state, register) over the lane's values
@@ -75,23 +74,13 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
     each([&](bool in, long long at, float &v) { if (in) dst[at] = v; });
   };
   if (SUMMARY) {
-    if (index == last) {  // keeps the start, which the cache loses when the last block ends
-      if (goes_on) {
-        load(cache);
-        store(entry(last));
-      }
-      return;
-    }
     load(index == 0 && goes_on ? cache : nullptr);
+    // the last block's entry keeps the start, which the cache loses when that block ends
+    if (index == 0 && goes_on) store(entry(last));
   } else if (index == 0) {
     load(goes_on ? (last > 0 ? entry(last) : cache) : nullptr);
   } else {
-    load(entry(0));
-    for (int i = 1; i < index; ++i) {
-      const float keep = ex2(*decay_of(i) * kLog2e);
-      const float *e = entry(i);
-      each([&](bool in, long long at, float &v) { v = in ? fmaf(keep, v, e[at]) : 0.f; });
-    }
+    load(entry(index - 1));
   }
 
   const float A = p.A[h], bias = p.bias ? p.bias[h] : 0.f, skip = p.D ? p.D[h] : 0.f;
@@ -118,11 +107,11 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
       float dt = bias + (p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]));
       if (p.softplus) dt = softplus_f(dt);
       dts[tid] = dt;
-      keeps[tid] = dt * A;
+      keeps[tid] = dt * A * kLog2e;
     }
     __syncthreads();
     for (int t = 0; t < n_tok; ++t) {
-      const float dt = dts[t], keep = ex2(keeps[t] * kLog2e);
+      const float dt = dts[t], keep = ex2(keeps[t]);
       float b[NPL], c[NPL], y[kRowsPerLane], in[kRowsPerLane];
       decay += keeps[t];
 #pragma unroll
@@ -172,10 +161,54 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
   }
 }
 
+// One thread: 4 values of one head's state, along a request's blocks. The loads
+// do not wait for one another, only the sums do.
+__global__ void __launch_bounds__(256) ss_head_scan_carry_kernel(const __grid_constant__ HeadScanParams p, int pieces) {
+  const int blk = p.t.carried[blockIdx.x / (p.heads * pieces)], rest = blockIdx.x % (p.heads * pieces), h = rest / pieces;
+  if (blk < 0) return;
+  const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blk];
+  if (row.w != 0) return;
+  const int last = (p.t.offsets[row.x + 1] - p.t.offsets[row.x] - 1) / p.t.block;
+  const int pn = p.headdim * p.dstate, n = ((rest % pieces) * 256 + threadIdx.x) * 4;
+  if (last < 2 || n >= pn) return;
+  const long long step = (long long)p.heads * pn;
+  float *e = p.ws_state + ((long long)blk * p.heads + h) * pn + n;
+  const float *decay = p.ws_decay + (long long)blk * p.heads + h;
+  const bool vec = pn % 4 == 0;
+  float v[4] = {};
+  auto get = [&](const float *src, float (&f)[4]) {
+    if (vec) {
+      const float4 q = *reinterpret_cast<const float4 *>(src);
+      f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+    } else {
+      for (int k = 0; k < 4; ++k) f[k] = n + k < pn ? src[k] : 0.f;
+    }
+  };
+  get(e, v);
+#pragma unroll 4
+  for (int i = 1; i < last; ++i) {
+    e += step;
+    float f[4];
+    get(e, f);
+    const float keep = ex2(decay[(long long)i * p.heads]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = fmaf(keep, v[k], f[k]);
+    if (vec) {
+      *reinterpret_cast<float4 *>(e) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      for (int k = 0; k < 4; ++k)
+        if (n + k < pn) e[k] = v[k];
+    }
+  }
+}
+
 template <typename T, int NPL>
 void go(const HeadScanParams &p, cudaStream_t s) {
   const dim3 grid(p.t.max_blocks + 1, p.heads * ((p.headdim + kRows - 1) / kRows));
-  if (p.split) ss_head_scan_kernel<T, NPL, true><<<grid, kScanThreads, 0, s>>>(p);
+  if (p.split) {
+    ss_head_scan_kernel<T, NPL, true><<<dim3(p.t.tokens / p.t.block, grid.y), kScanThreads, 0, s>>>(p);
+    launch_head_scan_carry(p, s);
+  }
   ss_head_scan_kernel<T, NPL, false><<<grid, kScanThreads, 0, s>>>(p);
 }
 template <typename T>
@@ -188,6 +221,14 @@ void by_states(const HeadScanParams &p, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_head_scan_carry(const HeadScanParams &p, cudaStream_t s) {
+  const int pieces = (p.headdim * p.dstate + 1023) / 1024;
+  const long long ctas = (long long)(p.t.tokens / p.t.block) * p.heads * pieces;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  ss_head_scan_carry_kernel<<<(unsigned)ctas, 256, 0, s>>>(p, pieces);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s) {
   if (dtype == 0) by_states<float>(p, s);

@@ -221,8 +221,300 @@ template <> struct Terms<__half> {
 template <typename T>
 constexpr uint32_t kIdesc = (1u << 4) | ((Terms<T>::N == 3 ? 1u : 0u) << 7) | ((Terms<T>::N == 3 ? 1u : 0u) << 10) | (8u << 24);
 
+// What a CTA works on: HT heads of a group through one block of a request.
+struct Place {
+  int h0, hend, grp, blk;             // first head, end of the group's heads, group, row of the block table
+  int r, first, size, index, last;    // request (-1: none), the block's tokens, its index and that of the request's last block
+  long long slot;
+  bool kept, goes_on;                 // the request has a slot, and starts from it
+};
+template <int HT, bool CARRIED>  // CARRIED: over the rows of t.carried
+__device__ __forceinline__ Place place_of(const HeadScanParams &p) {
+  Place w;
+  const int tpg = (p.hpg + HT - 1) / HT, tiles = p.heads / p.hpg * tpg, tile = blockIdx.x % tiles;
+  w.blk = blockIdx.x / tiles;
+  w.grp = tile / tpg;
+  w.h0 = w.grp * p.hpg + (tile % tpg) * HT;
+  w.hend = (w.grp + 1) * p.hpg;
+  w.r = -1;
+  if (CARRIED) {
+    w.blk = p.t.carried[w.blk];
+    if (w.blk < 0) return w;
+  } else if (w.blk == p.t.max_blocks) {
+    return w;
+  }
+  const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[w.blk];
+  w.r = row.x;
+  w.first = row.y;
+  w.size = row.z;
+  w.index = row.w;
+  if (w.r < 0) return w;
+  w.last = (p.t.offsets[w.r + 1] - p.t.offsets[w.r] - 1) / p.t.block;
+  w.slot = p.state ? p.t.slot_map[w.r] : -1;
+  w.kept = w.slot >= 0 && w.slot < p.slots;
+  w.goes_on = w.kept && p.t.context && p.t.context[w.r] > 0;
+  return w;
+}
+// Row pp of head h of a request's kept state, and of its block i's summary.
+__device__ __forceinline__ float *cache_row(const HeadScanParams &p, const Place &w, int h, int pp) {
+  return p.state + w.slot * p.ss[0] + h * p.ss[1] + (long long)pp * p.dstate;
+}
+__device__ __forceinline__ long long entry_of(const HeadScanParams &p, const Place &w, int h, int i) {
+  return (long long)(w.blk - w.index + i) * p.heads + h;
+}
+__device__ __forceinline__ float *entry_row(const HeadScanParams &p, const Place &w, int h, int pp, int i) {
+  return p.ws_state + (entry_of(p, w, h, i) * p.headdim + pp) * p.dstate;
+}
+
+// ---- summaries of a block: the state it ends in ----
+//
+// Its own gain, with S_0 = 0 but in a request's first block:
+// S_end = e^(L_end) S_0 + (w X)^T B over the whole block, w_s = e^(L_end - L_s) dt_s:
+// from its last chunk to its first, so that the decay to the block's end is known
+// when a chunk is weighed, and S is one sum that no chunk has to scale.
+//   warps 0 - 15   weigh (thread = column p, a warpgroup 32 of the chunk's tokens)
+//   warps 16 - 23  prepare w (thread = token, a warpgroup per head)
+//   warp 24 loads by TMA, warp 25 issues the products
+// w X has two buffers of 128 tokens x 3 terms in tensor memory; X and B have
+// three places. Bound by the weighing warps' instructions.
+constexpr int kSumThreads = 832, kSumStages = 3;
+
+struct SumShared {
+  uint64_t full[kSumStages], empty[kSumStages], prepared[2], taken[2], weighed[2], gained[2];
+  uint32_t tmem;
+  int dead;
+  float part[2][2][4], top[2][4];
+  float total[2], scale[2];      // by head: log2 decay of the block; scale of w
+  alignas(16) float w[2][2][128];
+};
+
+template <typename T, int PW, int NS>
+__global__ void __launch_bounds__(kSumThreads, 1)
+    ss_head_scan_sum_tc_kernel(const __grid_constant__ HeadScanParams p, const __grid_constant__ TcMaps maps) {
+  constexpr int HT = 128 / PW, NB = NS / 64, NT = Terms<T>::N, NQ = NS / 4;
+  constexpr uint32_t kColSum = 0, kColW = 128;
+  extern __shared__ unsigned char raw[];
+  unsigned char *ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  SumShared &sh = *reinterpret_cast<SumShared *>(ring + kSumStages * (2 + NB) * kBox);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wq = warp & 3, wg = (warp >> 2) & 3;
+  const Place at = place_of<HT, true>(p);
+  if (at.r < 0) return;
+  const int pc = wq * 32 + lane, hs = HT == 2 ? pc >> 6 : 0, pp = HT == 2 ? pc & 63 : pc, h = at.h0 + hs;
+  const bool pin = warp < 16 && h < at.hend && pp < p.headdim;
+  const int n0 = wg * NQ, nv = min(max(p.dstate - n0, 0), NQ);  // this thread's states of its column
+  if (tid == 0) {
+    for (int i = 0; i < kSumStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 17);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.prepared[i], 4 * HT);
+      mbar_init(&sh.taken[i], 16);
+      mbar_init(&sh.weighed[i], 16);
+      mbar_init(&sh.gained[i], 1);
+    }
+    sh.dead = 0;
+    fence_barrier_init();
+  }
+  if (warp == 25) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = sh.tmem, lane_at = (uint32_t)(wq * 32) << 16;
+  volatile int *dead = &sh.dead;
+  const int chunks = (at.size + 127) / 128;  // i-th from the end: chunk chunks - 1 - i
+  auto xbox = [&](int i, int k) { return ring + ((i % kSumStages) * (2 + NB) + k) * kBox; };
+  auto bbox = [&](int i, int k) { return xbox(i, 2 + k); };
+
+  if (warp == 24) {
+    // ---- TMA ----
+    if (lane == 0) {
+      int n = 0;
+      for (int i = 0; i < chunks && !*dead; ++i, ++n) {
+        const int s = i % kSumStages, t = at.first + (chunks - 1 - i) * 128;
+        if (i >= kSumStages && !wait_tc(&sh.empty[s], (i / kSumStages - 1) & 1, dead, p.err)) break;
+        mbar_arrive_expect_tx(&sh.full[s], (2 + NB) * kBox);
+        for (int k = 0; k < 2; ++k)
+          tma_load_3d(xbox(i, k), &maps.x, &sh.full[s], HT == 2 ? 0 : 64 * k, HT == 2 ? at.h0 + k : at.h0, t);
+        for (int k = 0; k < NB; ++k) tma_load_3d(bbox(i, k), &maps.B, &sh.full[s], 64 * k, at.grp, t);
+      }
+      // nothing of this block's copies is left in flight, whatever became of the rest
+      for (int i = max(0, n - kSumStages); i < n; ++i)
+        for (uint32_t k = 0; k < kMaxWaitIters; ++k)
+          if (mbar_try_wait(&sh.full[i % kSumStages], (i / kSumStages) & 1)) break;
+    }
+  } else if (warp == 25) {
+    // ---- products ----
+    constexpr uint32_t id_s = kIdesc<T> | (1u << 16) | ((uint32_t)NS / 8 << 17);  // w X x B: B is N-major
+#pragma unroll 1
+    for (int i = 0; i < chunks; ++i) {
+      wait_tc(&sh.full[i % kSumStages], (i / kSumStages) & 1, dead, p.err);
+      wait_tc(&sh.weighed[i & 1], (i >> 1) & 1, dead, p.err);
+      fence_after();
+      const uint64_t bd = smem_desc(smem_u32(bbox(i, 0)), kBox, 1024);
+      __syncwarp();
+      if (elect() && !*dead) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < NT; ++e)
+            mma_ts(tm + kColSum, tm + kColW + 192 * (i & 1) + 64 * e + 8 * k, bd + ((k * 2048) >> 4), id_s, i > 0 || k > 0 || e > 0);
+        commit(&sh.gained[i & 1]);
+        commit(&sh.empty[i % kSumStages]);
+      }
+    }
+  } else if (warp >= 16) {
+    // ---- w: thread = token, warpgroup = head ----
+    const int tp = wg, trow = pc;
+    if (tp < HT) {
+      const int hp = at.h0 + tp < at.hend ? at.h0 + tp : at.h0;
+      const float A2 = p.A[hp] * kLog2e, bias = p.bias ? p.bias[hp] : 0.f;
+      auto load_dt = [&](int i) -> float {
+        const int t = (chunks - 1 - i) * 128 + trow;
+        if (i >= chunks || t >= at.size) return 0.f;
+        const long long k = (long long)(at.first + t) * p.sdt[0] + hp * p.sdt[1];
+        return p.dt_f32 ? static_cast<const float *>(p.dt)[k] : to_f<T>(static_cast<const T *>(p.dt)[k]);
+      };
+      float later = 0.f, scale = 1.f, raw_dt = load_dt(0);  // later: log2 decay of the chunks after this one
+#pragma unroll 1
+      for (int i = 0; i < chunks; ++i) {
+        float dt = raw_dt + bias;
+        if (p.softplus) dt = softplus_f(dt);
+        if ((chunks - 1 - i) * 128 + trow >= at.size) dt = 0.f;
+        raw_dt = load_dt(i + 1);
+        float to_end = dt * A2;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float dn = __shfl_down_sync(0xffffffffu, to_end, o);
+          if (lane + o < 32) to_end += dn;
+        }
+        if (lane == 0) sh.part[i & 1][tp][wq] = to_end;
+        const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
+        asm volatile("bar.sync %0, 128;" ::"r"(2 + tp) : "memory");
+        float after = later, total = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float t = sh.part[i & 1][tp][k];
+          if (k > wq) after += t;
+          total += t;
+        }
+        later += total;
+        float w = dt * ex2(after + (lane < 31 ? nx : 0.f));
+        if (NT == 2 && i == 0) {
+          // a power of two that brings the last chunk's largest w to [1/32, 1/16): the
+          // smaller term of w X does not underflow, and w may be 2^15 times as large
+          // in an earlier chunk
+          float m = fabsf(w);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (lane == 0) sh.top[tp][wq] = m;
+          asm volatile("bar.sync %0, 128;" ::"r"(2 + tp) : "memory");
+          m = fmaxf(fmaxf(sh.top[tp][0], sh.top[tp][1]), fmaxf(sh.top[tp][2], sh.top[tp][3]));
+          const int e = (int)(__float_as_uint(m) >> 23);
+          scale = e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(249 - e) << 23);
+        }
+        if (i >= 2) wait_tc(&sh.taken[i & 1], ((i >> 1) - 1) & 1, dead, p.err);
+        sh.w[i & 1][tp][trow] = w * scale;
+        if (trow == 0) {
+          sh.total[tp] = later;
+          sh.scale[tp] = scale;
+        }
+        arrive_warp(&sh.prepared[i & 1], lane);
+      }
+    }
+  } else {
+    // ---- w X: thread = column, warpgroup = 32 tokens ----
+    const int valid = at.size - (chunks - 1) * 128;  // of the first chunk in this order
+#pragma unroll 1
+    for (int i = 0; i < chunks; ++i) {
+      wait_tc(&sh.full[i % kSumStages], (i / kSumStages) & 1, dead, p.err);
+      if (i == 0 && valid < 128) {  // rows of the next request, or of nothing: 0 x anything must be 0
+        const int todo = (128 - valid) * 8;
+        for (int k = tid; k < todo * (2 + NB); k += 512)
+          *reinterpret_cast<uint4 *>(xbox(0, k / todo) + (valid + k % todo / 8) * 128 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+      }
+      wait_tc(&sh.prepared[i & 1], (i >> 1) & 1, dead, p.err);
+      if (i >= 2) {
+        wait_tc(&sh.gained[i & 1], ((i >> 1) - 1) & 1, dead, p.err);
+        fence_after();
+      }
+      uint32_t col = smem_u32(xbox(i, pc >> 6)) + wg * 32 * 128 + (pc & 63) * 2;  // in row 0 of a swizzle atom
+      const float *wf = sh.w[i & 1][hs] + wg * 32;
+      uint32_t to = tm + lane_at + kColW + 192 * (i & 1) + 16 * wg;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        uint32_t t[NT][4];
+        const float4 wa = *reinterpret_cast<const float4 *>(wf), wb = *reinterpret_cast<const float4 *>(wf + 4);
+        const f2 w[4] = {pk(wa.x, wa.y), pk(wa.z, wa.w), pk(wb.x, wb.y), pk(wb.z, wb.w)};
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = lds_16<T>((col ^ (k << 4)) + k * 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t a[NT];
+          Terms<T>::split(mul2(pk(x[2 * k], x[2 * k + 1]), w[k]), a);
+#pragma unroll
+          for (int e = 0; e < NT; ++e) t[e][k] = a[e];
+        }
+#pragma unroll
+        for (int e = 0; e < NT; ++e) tm_st4(to + 64 * e, t[e]);
+        col += 8 * 128;
+        wf += 8;
+        to += 4;
+      }
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.weighed[i & 1]);
+        mbar_arrive(&sh.taken[i & 1]);
+        mbar_arrive(&sh.empty[i % kSumStages]);
+      }
+    }
+    wait_tc(&sh.gained[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, dead, p.err);
+    fence_after();
+    const float keep = ex2(sh.total[hs]);
+    const float unscale = __uint_as_float((254u << 23) - __float_as_uint(sh.scale[hs]));  // a power of two
+#pragma unroll 1
+    for (int n = 0; n < NQ; n += 16) {
+      uint32_t v[16];
+      tm_ld16(tm + lane_at + kColSum + n0 + n, v);
+      if (!pin || *dead) continue;
+      const float *start = at.index == 0 && at.goes_on ? cache_row(p, at, h, pp) + n0 : nullptr;
+      float *dst = entry_row(p, at, h, pp, at.index) + n0;
+#pragma unroll
+      for (int k = 0; k < 16; k += 4)
+        if (n + k < nv) {
+          float4 f = make_float4(__uint_as_float(v[k]) * unscale, __uint_as_float(v[k + 1]) * unscale,
+                                 __uint_as_float(v[k + 2]) * unscale, __uint_as_float(v[k + 3]) * unscale);
+          if (start) {
+            // the last block's entry keeps the start, which the cache loses when that block ends
+            const float4 q = *reinterpret_cast<const float4 *>(start + n + k);
+            *reinterpret_cast<float4 *>(entry_row(p, at, h, pp, at.last) + n0 + n + k) = q;
+            f = make_float4(fmaf(keep, q.x, f.x), fmaf(keep, q.y, f.y), fmaf(keep, q.z, f.z), fmaf(keep, q.w, f.w));
+          }
+          *reinterpret_cast<float4 *>(dst + n + k) = f;
+        }
+    }
+    if (pin && pp == 0 && wg == 0 && !*dead) p.ws_decay[entry_of(p, at, h, at.index)] = sh.total[hs];
+    fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 25) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+  }
+}
+
+// ---- the scan of a block ----
 // PW: columns of a head in the tile (64: two heads, 128: one). NS: padded dstate.
-template <typename T, int PW, int NS, bool SUMMARY, bool GATE>
+template <typename T, int PW, int NS, bool GATE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     ss_head_scan_tc_kernel(const __grid_constant__ HeadScanParams p, const __grid_constant__ TcMaps maps) {
   constexpr int HT = 128 / PW;
@@ -235,56 +527,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   Shared &sh = *reinterpret_cast<Shared *>(s16 + NB * kBox);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tpg = (p.hpg + HT - 1) / HT;                // tiles per group
-  const int tiles = p.heads / p.hpg * tpg;
-  const int tile = blockIdx.x % tiles, blk = blockIdx.x / tiles;
-  const int grp = tile / tpg, h0 = grp * p.hpg + (tile % tpg) * HT;
-  const int hend = (grp + 1) * p.hpg;                   // heads of the group end here
+  const Place at = place_of<HT, false>(p);
+  const int h0 = at.h0, hend = at.hend, first = at.first, size = at.size, index = at.index;
   T *out = static_cast<T *>(p.out);
-  if (blk == p.t.max_blocks) {                          // past the last token: zeros
-    if (!SUMMARY) {
-      const int cols = min(HT, hend - h0) * p.headdim;
-      for (int t = p.t.counts[0] + warp; t < p.t.tokens; t += kTcThreads / 32)
-        for (int i = lane; i < cols; i += 32)
-          out[t * p.so[0] + (h0 + i / p.headdim) * p.so[1] + i % p.headdim] = from_f<T>(0.f);
-    }
+  if (at.blk == p.t.max_blocks) {                       // past the last token: zeros
+    const int cols = min(HT, hend - h0) * p.headdim;
+    for (int t = p.t.counts[0] + warp; t < p.t.tokens; t += kTcThreads / 32)
+      for (int i = lane; i < cols; i += 32)
+        out[t * p.so[0] + (h0 + i / p.headdim) * p.so[1] + i % p.headdim] = from_f<T>(0.f);
     return;
   }
-  const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blk];
-  const int r = row.x, first = row.y, size = row.z, index = row.w;
-  if (r < 0) return;
-  const int len = p.t.offsets[r + 1] - p.t.offsets[r];
-  const int last = (len - 1) / p.t.block;
-  if (SUMMARY && last == 0) return;
-  const int slot = p.state ? p.t.slot_map[r] : -1;
-  const bool kept = slot >= 0 && slot < p.slots;
-  const bool goes_on = kept && p.t.context && p.t.context[r] > 0;
+  if (at.r < 0) return;
 
   // thread = column: its head, row of the state and half of the states
   const int wg = (warp >> 2) & 1, wq = warp & 3;
   const int pc = wq * 32 + lane, hs = HT == 2 ? pc >> 6 : 0, pp = HT == 2 ? pc & 63 : pc;
   const bool pin = warp >= 16 && warp < 24 && h0 + hs < hend && pp < p.headdim;
   const int n0 = wg * NH, nv = min(max(p.dstate - n0, 0), NH);  // a multiple of 8
-  const long long pn = (long long)p.headdim * p.dstate;
-  float *cache = kept ? p.state + slot * p.ss[0] + (h0 + hs) * p.ss[1] + (long long)pp * p.dstate + n0 : nullptr;
-  auto entry = [&](int i) {
-    return p.ws_state + ((long long)(blk - index + i) * p.heads + h0 + hs) * pn + (long long)pp * p.dstate + n0;
-  };
-  auto decay_of = [&](int i) { return p.ws_decay + (long long)(blk - index + i) * p.heads + h0 + hs; };
-
-  if (SUMMARY && index == last) {  // keeps the start, which the cache loses when the last block ends
-    if (goes_on && pin)
-      for (int n = 0; n < nv; n += 4) *reinterpret_cast<float4 *>(entry(last) + n) = *reinterpret_cast<const float4 *>(cache + n);
-    return;
-  }
-
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.full_x[i], 1);
       mbar_init(&sh.full_b[i], 1);
       mbar_init(&sh.full_z[i], 1);
       mbar_init(&sh.empty_x[i], 1);
-      mbar_init(&sh.empty_b[i], SUMMARY ? 1 : 2);  // both kinds of products read B
+      mbar_init(&sh.empty_b[i], 2);  // both kinds of products read B
     }
     mbar_init(&sh.full_c, 1);
     mbar_init(&sh.empty_c, 1);
@@ -343,12 +609,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ++nx;
         if (!GATE && c >= 2 && !wait_tc(&sh.empty_b[c & 1], before, dead, p.err)) break;
         mbar_arrive_expect_tx(&sh.full_b[c & 1], NB * kBox);
-        for (int k = 0; k < NB; ++k) tma_load_3d(bbox(c, k), &maps.B, &sh.full_b[c & 1], 64 * k, grp, t);
+        for (int k = 0; k < NB; ++k) tma_load_3d(bbox(c, k), &maps.B, &sh.full_b[c & 1], 64 * k, at.grp, t);
         ++nb;
-        if (SUMMARY) continue;
         if (c >= 1 && !wait_tc(&sh.empty_c, (c - 1) & 1, dead, p.err)) break;
         mbar_arrive_expect_tx(&sh.full_c, NB * kBox);
-        for (int k = 0; k < NB; ++k) tma_load_3d(cbox + k * kBox, &maps.C, &sh.full_c, 64 * k, grp, t);
+        for (int k = 0; k < NB; ++k) tma_load_3d(cbox + k * kBox, &maps.C, &sh.full_c, 64 * k, at.grp, t);
         ++nc;
         if (GATE && c >= 1) load_z(c - 1);
       }
@@ -365,52 +630,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 25) {
     // ---- products for Y ----
-    if (!SUMMARY) {
-      constexpr uint32_t id_g = kIdesc<T> | (128u / 8 << 17);                       // C B^T and C S^T: both K-major, N = 128
-      constexpr uint32_t id_y = kIdesc<T> | (1u << 16) | ((uint32_t)PW / 8 << 17);  // masked x X: X is N-major
-      const uint64_t sd = smem_desc(smem_u32(s16), 16, 1024);
+    constexpr uint32_t id_g = kIdesc<T> | (128u / 8 << 17);                       // C B^T and C S^T: both K-major, N = 128
+    constexpr uint32_t id_y = kIdesc<T> | (1u << 16) | ((uint32_t)PW / 8 << 17);  // masked x X: X is N-major
+    const uint64_t sd = smem_desc(smem_u32(s16), 16, 1024);
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const uint32_t ph = c & 1;
-        full(sh.full_b, c);
-        wait_tc(&sh.full_c, ph, dead, p.err);
-        if (c > 0) wait_tc(&sh.y_done, ph ^ 1, dead, p.err);  // the masked forms' columns are free again
-        fence_after();
-        const uint64_t cd = smem_desc(smem_u32(cbox), 16, 1024), bd = smem_desc(smem_u32(bbox(c, 0)), 16, 1024);
-        __syncwarp();
-        if (elect() && !*dead) {
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t ph = c & 1;
+      full(sh.full_b, c);
+      wait_tc(&sh.full_c, ph, dead, p.err);
+      if (c > 0) wait_tc(&sh.y_done, ph ^ 1, dead, p.err);  // the masked forms' columns are free again
+      fence_after();
+      const uint64_t cd = smem_desc(smem_u32(cbox), 16, 1024), bd = smem_desc(smem_u32(bbox(c, 0)), 16, 1024);
+      __syncwarp();
+      if (elect() && !*dead) {
 #pragma unroll
-          for (int k = 0; k < NS / 16; ++k) {
-            const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
-            mma_ss(tm + kColG, cd + at, bd + at, id_g, k > 0);
-          }
+        for (int k = 0; k < NS / 16; ++k) {
+          const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
+          mma_ss(tm + kColG, cd + at, bd + at, id_g, k > 0);
         }
-        if (c > 0) wait_tc(&sh.y_free, ph ^ 1, dead, p.err);
-        wait_tc(&sh.s_ready, ph, dead, p.err);
-        fence_after();
-        __syncwarp();
-        if (elect() && !*dead) {
+      }
+      if (c > 0) wait_tc(&sh.y_free, ph ^ 1, dead, p.err);
+      wait_tc(&sh.s_ready, ph, dead, p.err);
+      fence_after();
+      __syncwarp();
+      if (elect() && !*dead) {
 #pragma unroll
-          for (int k = 0; k < NS / 16; ++k) {
-            const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
-            mma_ss(tm + kColY, cd + at, sd + at, id_g, k > 0);
-          }
-          commit(&sh.gy_done);
+        for (int k = 0; k < NS / 16; ++k) {
+          const uint32_t at = ((k / 4) * kBox + (k % 4) * 32) >> 4;
+          mma_ss(tm + kColY, cd + at, sd + at, id_g, k > 0);
         }
-        full(sh.full_x, c);
-        if (size - c * 128 < 128) wait_tc(&sh.x_read[c & 1], (c >> 1) & 1, dead, p.err);  // rows past the request's end are cleared
-        wait_tc(&sh.masked, ph, dead, p.err);
-        fence_after();
-        const uint64_t xd = smem_desc(smem_u32(xbox(c, 0)), kBox, 1024);
-        __syncwarp();
-        if (elect() && !*dead) {
+        commit(&sh.gy_done);
+      }
+      full(sh.full_x, c);
+      if (size - c * 128 < 128) wait_tc(&sh.x_read[c & 1], (c >> 1) & 1, dead, p.err);  // rows past the request's end are cleared
+      wait_tc(&sh.masked, ph, dead, p.err);
+      fence_after();
+      const uint64_t xd = smem_desc(smem_u32(xbox(c, 0)), kBox, 1024);
+      __syncwarp();
+      if (elect() && !*dead) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int h = 0; h < HT; ++h)
-              mma_ts(tm + kColY + 64 * h, tm + kColG + 16 * k + 8 * h, xd + ((h * kBox + k * 2048) >> 4), id_y, true);
-          commit(&sh.y_done);
-        }
+          for (int h = 0; h < HT; ++h)
+            mma_ts(tm + kColY + 64 * h, tm + kColG + 16 * k + 8 * h, xd + ((h * kBox + k * 2048) >> 4), id_y, true);
+        commit(&sh.y_done);
       }
     }
   } else if (warp == 26) {
@@ -440,7 +703,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 27) {
     // ---- output: whole chunks leave by TMA, a request's last rows have left already ----
-    if (!SUMMARY && lane == 0) {
+    if (lane == 0) {
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         wait_tc(&sh.finished[c & 3], (c >> 2) & 1, dead, p.err);
@@ -456,7 +719,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp >= 16) {
     // ---- column warps: thread = column p ----
-    float decay = 0.f, scale = 1.f;  // of this column's head: log2 decay so far; w's scale in this chunk
+    float scale = 1.f;  // of w in this chunk
     float fade0 = 0.f, fade1 = 0.f, fade2 = 0.f;  // from the ends of the first 32 tokens, ... to the chunk's end, times scale
 #pragma unroll 1
     for (int c = 0; c <= chunks; ++c) {
@@ -470,7 +733,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wait_tc(&sh.prepared[c & 3], (c >> 2) & 1, dead, p.err);
         const float *t = sh.tot[c & 3][hs];
         const float t3 = t[3], t2 = t3 + t[2], t1 = t2 + t[1], t0 = t1 + t[0];
-        decay += t0;
         keep = ex2(t0);
         fade0 = ex2(t1);
         fade1 = ex2(t2);
@@ -511,9 +773,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // this chunk's product, and its decayed, scaled form as the accumulator
           if (c > 0) {
             wait_tc(&sh.gained[1], 1, dead, p.err);  // the chunk's last; and all its columns of X are read
-            if (!SUMMARY) wait_tc(&sh.gy_done, before, dead, p.err);
+            wait_tc(&sh.gy_done, before, dead, p.err);
             fence_after();
-            if (SUMMARY && tid == 512) mbar_arrive(&sh.empty_x[(c - 1) & 1]);
           }
 #pragma unroll 1
           for (int n = 0; n < NH; n += 16) {
@@ -526,37 +787,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = 0.f;
-              auto fold = [&](const float *src, float k) {
+              auto start = [&](const float *src) {
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
                   if (n + i < nv) {
                     const float4 f = *reinterpret_cast<const float4 *>(src + n + i);
-                    v[i] = fmaf(k, v[i], f.x);
-                    v[i + 1] = fmaf(k, v[i + 1], f.y);
-                    v[i + 2] = fmaf(k, v[i + 2], f.z);
-                    v[i + 3] = fmaf(k, v[i + 3], f.w);
+                    v[i] = f.x;
+                    v[i + 1] = f.y;
+                    v[i + 2] = f.z;
+                    v[i + 3] = f.w;
                   }
               };
               if (pin) {
                 if (index == 0) {
-                  if (goes_on) fold(!SUMMARY && last > 0 ? entry(last) : cache, 0.f);
-                } else if (!SUMMARY) {
-#pragma unroll 1
-                  for (int i = 0; i < index; ++i) fold(entry(i), ex2(*decay_of(i)));
+                  if (at.goes_on) start((at.last > 0 ? entry_row(p, at, h0 + hs, pp, at.last) : cache_row(p, at, h0 + hs, pp)) + n0);
+                } else {
+                  start(entry_row(p, at, h0 + hs, pp, index - 1) + n0);
                 }
               }
             }
             if (more) {
-              if (!SUMMARY) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 8) {
-                  uint4 w4;  // a 16-byte piece of the row
-                  w4.x = pack2<T>(v[i], v[i + 1]);
-                  w4.y = pack2<T>(v[i + 2], v[i + 3]);
-                  w4.z = pack2<T>(v[i + 4], v[i + 5]);
-                  w4.w = pack2<T>(v[i + 6], v[i + 7]);
-                  *reinterpret_cast<uint4 *>(s16 + ((n0 + n) / 64) * kBox + swz(pc, ((n0 + n + i) % 64) * 2)) = w4;
-                }
+              for (int i = 0; i < 16; i += 8) {
+                uint4 w4;  // a 16-byte piece of the row
+                w4.x = pack2<T>(v[i], v[i + 1]);
+                w4.y = pack2<T>(v[i + 2], v[i + 3]);
+                w4.z = pack2<T>(v[i + 4], v[i + 5]);
+                w4.w = pack2<T>(v[i + 6], v[i + 7]);
+                *reinterpret_cast<uint4 *>(s16 + ((n0 + n) / 64) * kBox + swz(pc, ((n0 + n + i) % 64) * 2)) = w4;
               }
               uint32_t w[16];
 #pragma unroll
@@ -566,22 +824,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 w[i + 1] = __float_as_uint(k.y);
               }
               tm_st16(tm + lane_at + kColS + n0 + n, w);
-            } else if (pin && !*dead && (SUMMARY || (index == last && kept))) {
-              float *dst = (SUMMARY ? entry(index) : cache) + n;
+            } else if (pin && !*dead && index == at.last && at.kept) {
+              float *dst = cache_row(p, at, h0 + hs, pp) + n0 + n;
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
                 if (n + i < nv) *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
           }
-          if (more) {
-            if (!SUMMARY) fence_proxy_async();
-            wait_st();
-            fence_before();
-            arrive_warp(&sh.s_ready, lane);
-          } else if (SUMMARY && pin && pp == 0 && wg == 0 && !*dead) {
-            *decay_of(index) = decay;
-          }
           if (!more) break;
+          fence_proxy_async();
+          wait_st();
+          fence_before();
+          arrive_warp(&sh.s_ready, lane);
         }
         // w X as the product's A operand: thread = column, a warpgroup half of the tokens
         const int use = 2 * c + (q >> 1);
@@ -618,7 +872,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_before();
         arrive_warp(&sh.weighed[q & 1], lane);
       }
-      if (!SUMMARY && more) arrive_warp(&sh.x_read[ph], lane);
+      if (more) arrive_warp(&sh.x_read[ph], lane);
     }
     fence_before();
   } else {
@@ -640,12 +894,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       return p.dt_f32 ? static_cast<const float *>(p.dt)[at] : to_f<T>(static_cast<const T *>(p.dt)[at]);
     };
     // The decays of chunk cp are prepared between masking and finishing chunk cp - 2.
-    constexpr int kAhead = SUMMARY ? 0 : 2;
+    constexpr int kAhead = 2;
     float raw_dt = load_dt(0);
 #pragma unroll 1
     for (int cp = 0; cp < chunks + kAhead; ++cp) {
       const int c = cp - kAhead;
-      if (!SUMMARY && c >= 0) {
+      if (c >= 0) {
         const int st = c & 3;
         wait_tc(&sh.prepared[st], (c >> 2) & 1, dead, p.err);
         wait_tc(&sh.gy_done, c & 1, dead, p.err);
@@ -660,15 +914,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
         for (int i2 = 0; i2 < 2; ++i2) {
           const int jb = i2 ? 7 - rg : rg, j = jb >> 1;
-          const uint32_t at = tm + lane_at + kColG + 16 * jb;
+          const uint32_t tg = tm + lane_at + kColG + 16 * jb;
           if (j > wq) {
             const uint32_t m[8] = {};
 #pragma unroll
-            for (int h = 0; h < HT; ++h) tm_st8(at + 8 * h, m);
+            for (int h = 0; h < HT; ++h) tm_st8(tg + 8 * h, m);
             continue;
           }
           uint32_t g[16];
-          tm_ld16(at, g);
+          tm_ld16(tg, g);
 #pragma unroll
           for (int h = 0; h < HT; ++h) {
             uint32_t m[8];
@@ -698,7 +952,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 m[i / 2 + 1] = pack2<T>(i + 2 <= d ? v.x : 0.f, i + 3 <= d ? v.y : 0.f);
               }
             }
-            tm_st8(at + 8 * h, m);
+            tm_st8(tg + 8 * h, m);
           }
         }
         // Y = e^L (C S^T), 32 columns
@@ -706,10 +960,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float e = -sh.nl[st][ho][trow];
           for (int k = 0; k < wq; ++k) e += sh.tot[st][ho][k];
           e = ex2(e);
-          const uint32_t at = tm + lane_at + kColY + 32 * rg;
+          const uint32_t ty = tm + lane_at + kColY + 32 * rg;
           uint32_t y[2][16];
-          tm_ld16_async(at, y[0]);
-          tm_ld16_async(at + 16, y[1]);
+          tm_ld16_async(ty, y[0]);
+          tm_ld16_async(ty + 16, y[1]);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             tm_wait(y[q]);
@@ -719,7 +973,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               y[q][i] = __float_as_uint(v.x);
               y[q][i + 1] = __float_as_uint(v.y);
             }
-            tm_st16(at + 16 * q, y[q]);
+            tm_st16(ty + 16 * q, y[q]);
           }
         }
         wait_st();
@@ -754,10 +1008,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         arrive_warp(&sh.prepared[st], lane);
         raw_dt = load_dt(cp + 1);
       }
-      if (SUMMARY) {
-        wait_tc(&sh.s_ready, cp & 1, dead, p.err);  // the chunk's decays are taken up, its predecessor's no longer needed
-        continue;
-      }
       if (c < 0) continue;
       // the output, 32 columns, in place of X's rows
       const int valid = min(128, size - c * 128);
@@ -777,11 +1027,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       arrive_warp(&sh.y_free, lane);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int at = swz(trow, 64 * (rg & 1) + 16 * k);
-        const uint4 xq = *reinterpret_cast<const uint4 *>(xr + at);
+        const int off = swz(trow, 64 * (rg & 1) + 16 * k);
+        const uint4 xq = *reinterpret_cast<const uint4 *>(xr + off);
         const uint32_t xw[4] = {xq.x, xq.y, xq.z, xq.w};
         uint4 zq = make_uint4(0, 0, 0, 0);
-        if (GATE) zq = *reinterpret_cast<const uint4 *>(zr + at);
+        if (GATE) zq = *reinterpret_cast<const uint4 *>(zr + off);
         const uint32_t zw[4] = {zq.x, zq.y, zq.z, zq.w};
         uint32_t o[4];
 #pragma unroll
@@ -801,7 +1051,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           o[i] = narrow<T>(v);
         }
-        *reinterpret_cast<uint4 *>(xr + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(xr + off) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (valid < 128 && hin && !*dead) {  // the request's last rows, as 64-byte pieces
         __syncwarp();
@@ -829,23 +1079,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 template <typename T, int PW, int NS, bool GATE>
 cudaError_t go(const HeadScanParams &p, const TcMaps &maps, cudaStream_t s) {
   constexpr int smem = kBoxes * kBox + NS / 64 * kBox + (int)sizeof(Shared) + 1024;
+  constexpr int sum_smem = kSumStages * (2 + NS / 64) * kBox + (int)sizeof(SumShared) + 1024;
   const int ht = 128 / PW;
   const long long tiles = (long long)(p.heads / p.hpg) * ((p.hpg + ht - 1) / ht);
   const long long ctas = tiles * (p.t.max_blocks + 1);
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  auto sum = ss_head_scan_tc_kernel<T, PW, NS, true, false>;
-  auto fwd = ss_head_scan_tc_kernel<T, PW, NS, false, GATE>;
+  auto sum = ss_head_scan_sum_tc_kernel<T, PW, NS>;
+  auto fwd = ss_head_scan_tc_kernel<T, PW, NS, GATE>;
   static bool set[64] = {};  // the attribute is per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !set[dev]) {
-    e = cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, sum_smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev] = true;
   }
-  if (p.split) sum<<<(unsigned)ctas, kTcThreads, smem, s>>>(p, maps);
+  if (p.split) {
+    sum<<<(unsigned)(tiles * (p.t.tokens / p.t.block)), kSumThreads, sum_smem, s>>>(p, maps);
+    e = launch_head_scan_carry(p, s);
+    if (e != cudaSuccess) return e;
+  }
   fwd<<<(unsigned)ctas, kTcThreads, smem, s>>>(p, maps);
   return cudaGetLastError();
 }

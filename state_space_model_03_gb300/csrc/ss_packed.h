@@ -11,13 +11,13 @@ int32_t *packed_error_word();
 struct TablesParams {
   int requests, tokens, block, max_blocks, free;
   const int32_t *lengths, *context, *slots, *free_slots;
-  int32_t *offsets, *token_request, *token_position, *blocks, *slot_map, *counts;
+  int32_t *offsets, *token_request, *token_position, *blocks, *carried, *slot_map, *counts;
 };
 cudaError_t launch_request_tables(const TablesParams &p, cudaStream_t s);
 
 struct Tables {
   int requests, tokens, block, max_blocks;
-  const int32_t *offsets, *token_request, *blocks, *slot_map, *counts, *context;
+  const int32_t *offsets, *token_request, *blocks, *carried, *slot_map, *counts, *context;
 };
 
 struct PackedConvParams {
@@ -64,15 +64,19 @@ struct HeadScanParams {
   float *state;
   void *out;
   long long sx[2], sdt[2], sB[2], sC[2], sz[2], so[2], ss[2];
-  // Summaries (split): per block of the table and head, the state it ends in
-  // from zero (the request's first block: from its start state), headdim x
-  // dstate, and the logarithm of its whole decay. The entry of a request's last
-  // block, whose end nothing continues, keeps the request's start state.
+  // Summaries (split): per block of the table and head, the state it ends in,
+  // headdim x dstate, and log2 of its whole decay. The first launch leaves a
+  // block's own gain (the request's first block: from its start state), the second
+  // adds what earlier blocks left, the third starts each block from the entry
+  // before its own. The entry of a request's last block, whose end nothing
+  // continues, keeps the request's start state. The first two run over the rows
+  // of t.carried, tokens / block of them at most.
   float *ws_state, *ws_decay;
   int32_t *err;
   Tables t;
 };
 cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s);
+cudaError_t launch_head_scan_carry(const HeadScanParams &p, cudaStream_t s);  // the second launch
 
 // The same on the tensor cores, for 16-bit operands that TMA can describe.
 typedef void *TensorMapEncode;  // the driver's cuTensorMapEncodeTiled

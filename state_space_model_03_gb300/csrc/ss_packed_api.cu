@@ -81,17 +81,19 @@ int validate(const ss_request_tables_params *p) {
   if (p->free > kMaxTokens) return SS_ERR_UNSUPPORTED;
   if (!p->lengths || !p->offsets || !p->slot_map || !p->counts) return SS_ERR_NULL;
   if (p->tokens > 0 && (!p->token_request || !p->token_position || !p->blocks)) return SS_ERR_NULL;
+  if (p->tokens >= p->block && !p->carried) return SS_ERR_NULL;
   for (const void *q : {(const void *)p->lengths, (const void *)p->context, (const void *)p->slots, (const void *)p->free_slots})
     if (q && !aligned(q, 4)) return SS_ERR_ALIGN;
   for (const void *q : {(const void *)p->offsets, (const void *)p->token_request, (const void *)p->token_position,
-                        (const void *)p->blocks, (const void *)p->slot_map, (const void *)p->counts})
+                        (const void *)p->blocks, (const void *)p->carried, (const void *)p->slot_map, (const void *)p->counts})
     if (!aligned(q, 16)) return SS_ERR_ALIGN;
   const Range ins[4] = {span(p->lengths, 4, {p->requests}, {1}), span(p->context, 4, {p->requests}, {1}),
                         span(p->slots, 4, {p->requests}, {1}), span(p->free_slots, 4, {p->free}, {1})};
-  const Range outs[6] = {span(p->offsets, 4, {p->requests + 1}, {1}), span(p->token_request, 4, {p->tokens}, {1}),
+  const Range outs[7] = {span(p->offsets, 4, {p->requests + 1}, {1}), span(p->token_request, 4, {p->tokens}, {1}),
                          span(p->token_position, 4, {p->tokens}, {1}), span(p->blocks, 4, {4 * p->max_blocks}, {1}),
-                         span(p->slot_map, 4, {p->requests}, {1}), span(p->counts, 4, {4}, {1})};
-  for (int i = 0; i < 6; ++i) {
+                         span(p->slot_map, 4, {p->requests}, {1}), span(p->counts, 4, {4}, {1}),
+                         span(p->carried, 4, {p->tokens / p->block}, {1})};
+  for (int i = 0; i < 7; ++i) {
     for (const Range &in : ins)
       if (overlap(outs[i], in)) return SS_ERR_ALIAS;
     for (int k = 0; k < i; ++k)
@@ -106,7 +108,8 @@ int validate(const ss_packed_tables &t) {
   if (st != SS_OK) return st;
   if (t.tokens == 0) return SS_OK;
   if (!t.offsets || !t.token_request || !t.blocks || !t.slot_map || !t.counts) return SS_ERR_NULL;
-  for (const void *q : {(const void *)t.offsets, (const void *)t.token_request, (const void *)t.blocks,
+  if (t.tokens >= t.block && !t.carried) return SS_ERR_NULL;
+  for (const void *q : {(const void *)t.offsets, (const void *)t.token_request, (const void *)t.blocks, (const void *)t.carried,
                         (const void *)t.slot_map, (const void *)t.counts})
     if (!aligned(q, 16)) return SS_ERR_ALIGN;
   if (t.context && !aligned(t.context, 4)) return SS_ERR_ALIGN;
@@ -114,7 +117,7 @@ int validate(const ss_packed_tables &t) {
 }
 ssk::Tables tables_of(const ss_packed_tables &t) {
   return {(int)t.requests, (int)t.tokens, (int)t.block, (int)t.max_blocks, t.offsets, t.token_request, t.blocks,
-          t.slot_map, t.counts, t.context};
+          t.carried, t.slot_map, t.counts, t.context};
 }
 
 // ---- packed convolution ----
@@ -273,7 +276,7 @@ int ss_request_tables(const ss_request_tables_params *p, void *stream) {
   if (launch_fault()) return SS_ERR_CUDA;
   const ssk::TablesParams k = {(int)p->requests, (int)p->tokens, (int)p->block, (int)p->max_blocks, (int)p->free,
                                p->lengths, p->context, p->slots, p->free_slots, p->offsets, p->token_request,
-                               p->token_position, p->blocks, p->slot_map, p->counts};
+                               p->token_position, p->blocks, p->carried, p->slot_map, p->counts};
   return launched(ssk::launch_request_tables(k, static_cast<cudaStream_t>(stream)));
 }
 
@@ -352,10 +355,10 @@ int ss_head_scan(const ss_head_scan_params *p, void *stream) {
 
 int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int64_t headdim, int32_t dtype, int32_t sms) {
   if (tokens < 1 || requests < 1 || heads < 1 || headdim < 1 || sms < 1) return 128;
-  // Requests of the average length, cut into `cut` blocks each: the waves of CTAs
-  // times the steps (of 128 tokens on the tensor cores, else of 16) in one, plus
-  // the summaries of all blocks but the last (about half of a step's work) and
-  // the launch and folding that they bring, in steps (5 us and 4 us, as measured).
+  // Requests of the average length, cut into `cut` blocks each: the waves of CTAs,
+  // each of so many steps (of 128 tokens on the tensor cores, else of 16), the
+  // summaries of all blocks but the last (a third of a step's work) and two more
+  // launches.
   const bool tc = dtype != SS_F32 && headdim <= 128;
   const int64_t tiles = tc ? (headdim <= 64 ? (heads + 1) / 2 : heads) : heads * ((headdim + 63) / 64);
   const int64_t resident = tc ? sms : 4 * sms, step = tc ? 128 : 16;
@@ -365,15 +368,16 @@ int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int6
   for (int64_t cut = 1; cut <= std::min<int64_t>(std::max<int64_t>(steps, 1), 64); ++cut) {
     const int64_t len = (steps + cut - 1) / cut;
     const double waves = static_cast<double>((requests * tiles * cut + resident - 1) / resident);
-    const double cost = waves * len * (cut > 1 ? 1.5 : 1.0) + (cut > 1 ? 1.0 + 0.2 * cut : 0.0);
+    const double cost = cut > 1 ? waves * (len * 1.34 + 0.5) + 1.5 : waves * len;
     if (cut == 1 || cost < least) {
       least = cost;
       best = cut;
     }
   }
   int64_t block = (steps + best - 1) / best * step;
-  // a batch whose requests need no cut may still hold one long request
-  if (best == 1) block = std::max<int64_t>(block, 4 * step);
+  // A batch whose requests need no cut may still hold one long request. A small
+  // one is better off without the second launch.
+  if (best == 1) block = std::max(block, tc && tokens <= 8 * step ? (tokens + step - 1) / step * step : 4 * step);
   return std::min<int64_t>(std::max<int64_t>(block, step), 1 << 19);
 }
 

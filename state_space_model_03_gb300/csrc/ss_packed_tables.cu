@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kThreads) ss_request_tables_kernel(const __gri
   extern __shared__ int sm_tab[];
   int *off = sm_tab;                    // requests + 1
   int *bst = sm_tab + p.requests + 1;   // requests + 1: first block of each request
+  int *nst = bst + p.requests + 1;      // requests + 1: requests before it that have tokens
   __shared__ long long sums[kThreads / 32];
   const int tid = threadIdx.x;
   const int per = (p.requests + kThreads - 1) / kThreads;
@@ -72,26 +73,29 @@ __global__ void __launch_bounds__(kThreads) ss_request_tables_kernel(const __gri
   if (tid == 0) off[p.requests] = (int)min(total, (long long)p.tokens);
   int errors = total > p.tokens ? 1 : 0;
   __syncthreads();
-  // first block of each request (low half), requests that need a slot (high half)
+  // first block of each request (low half), requests before it that need a slot
+  // (upper 16 bits) and that have tokens (16 bits below)
   mine = 0;
   for (int r = r0; r < r1; ++r) {
     const int n = off[r + 1] - off[r];
     mine += (n + p.block - 1) / p.block;
-    if (p.slots && p.slots[r] < 0) mine += 1ll << 32;
+    if (n > 0) mine += 1ll << 32;
+    if (p.slots && p.slots[r] < 0) mine += 1ll << 48;
   }
   run = block_exclusive(mine, sums, total);
-  const int nblocks = (int)(total & 0xffffffff), wanted = (int)(total >> 32);
+  const int nblocks = (int)(total & 0xffffffff), wanted = (int)(total >> 48);
   for (int r = r0; r < r1; ++r) {
     bst[r] = (int)(run & 0xffffffff);
-    run += (off[r + 1] - off[r] + p.block - 1) / p.block;
+    nst[r] = (int)((run >> 32) & 0xffff);
+    run += (off[r + 1] - off[r] + p.block - 1) / p.block + (off[r + 1] > off[r] ? 1ll << 32 : 0ll);
     if (blockIdx.x == 0) {
       int slot = r;
       if (p.slots) {
         slot = p.slots[r];
         if (slot < 0) {
-          const int k = (int)(run >> 32);
+          const int k = (int)(run >> 48);
           slot = p.free_slots && k < p.free ? p.free_slots[k] : -1;
-          run += 1ll << 32;
+          run += 1ll << 48;
         }
       }
       p.slot_map[r] = slot;
@@ -119,7 +123,11 @@ __global__ void __launch_bounds__(kThreads) ss_request_tables_kernel(const __gri
       row = make_int4(r, first, min(off[r + 1] - first, p.block), k);
     }
     reinterpret_cast<int4 *>(p.blocks)[i] = row;
+    // each request before this one has one last block, which is not listed
+    if (row.x >= 0 && row.y + row.z < off[row.x + 1]) p.carried[i - nst[row.x]] = i;
   }
+  const int carried = nblocks - (int)((total >> 32) & 0xffff);
+  for (int i = carried + blockIdx.x * kThreads + tid; i < p.tokens / p.block; i += step) p.carried[i] = -1;
 
   // four tokens a thread: one bisection, then on along the offsets
   for (long long t0 = ((long long)blockIdx.x * kThreads + tid) * 4; t0 < p.tokens; t0 += (long long)step * 4) {
@@ -162,7 +170,7 @@ cudaError_t launch_request_tables(const TablesParams &p, cudaStream_t s) {
   // at most one CTA per SM, so that the sums are repeated no more often than that
   const long long want = ((long long)p.tokens + kTokensPerCta - 1) / kTokensPerCta;
   const int grid = (int)(want < 1 ? 1 : want > 152 ? 152 : want);
-  const int smem = 2 * (p.requests + 1) * (int)sizeof(int);
+  const int smem = 3 * (p.requests + 1) * (int)sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute((const void *)&ss_request_tables_kernel,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -56,10 +56,11 @@ class RequestTables:
     """Tables of one packed batch (int32, on the GPU), as ``request_tables``
     makes them: ``offsets`` (requests + 1), ``token_request`` and
     ``token_position`` (tokens), ``blocks`` (max_blocks, 4), ``slots``
-    (requests) and ``counts`` (4: tokens, blocks, slots taken, errors)."""
+    (requests), ``counts`` (4: tokens, blocks, slots taken, errors) and
+    ``carried`` (rows of blocks that another block of their request follows)."""
 
     __slots__ = ("tokens", "block", "max_blocks", "offsets", "token_request", "token_position", "blocks", "slots",
-                 "counts", "context", "_plan")
+                 "counts", "context", "carried", "_plan")
 
     def check(self):
         """Raise if the lengths did not fit the batch (reads counts: synchronises)."""
@@ -88,7 +89,7 @@ def request_tables(lengths, num_tokens, context=None, slots=None, free_slots=Non
     t = RequestTables()
     t.tokens, t.block = num_tokens, block
     (t.offsets, t.token_request, t.token_position, t.blocks, t.slots, t.counts, t._plan, t.max_blocks,
-     t.context) = _bind().request_tables(lengths, num_tokens, context, slots, free_slots, block)
+     t.context, t.carried) = _bind().request_tables(lengths, num_tokens, context, slots, free_slots, block)
     return t
 
 

@@ -104,4 +104,5 @@ def test_tables_by_hand():
     assert t["token_position"].tolist() == [7, 8, 9, 0, 1, 2, 3, 4, 0, 0]
     assert t["blocks"].tolist() == [[0, 0, 2, 0], [0, 2, 1, 1], [2, 3, 2, 0], [2, 5, 2, 1], [2, 7, 1, 2]] + [[-1, 0, 0, 0]] * 3
     assert t["slots"].tolist() == [4, 9, 8]
+    assert t["carried"].tolist() == [0, 2, 3, -1, -1]
     assert t["counts"].tolist() == [8, 5, 2, 0]

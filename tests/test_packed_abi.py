@@ -47,6 +47,7 @@ SCAN = [
     ("null_x", "p.x = 0;", 1),
     ("null_out", "p.out = 0;", 1),
     ("null_table", "p.tables.blocks = 0;", 1),
+    ("null_carried", "p.tables.carried = 0;", 1),
     ("max_blocks", "p.tables.max_blocks = 1;", 2),
     ("requests", "p.tables.requests = SS_MAX_REQUESTS + 1;", 7),
     ("negative", "p.B_stride[0] = -1;", 4),
@@ -109,7 +110,7 @@ static ss_packed_tables tables(void) {
   ss_packed_tables t;
   memset(&t, 0, sizeof(t));
   t.requests = 3; t.tokens = 256; t.block = 128; t.max_blocks = 5;
-  t.offsets = buf(); t.token_request = buf(); t.blocks = buf(); t.slot_map = buf(); t.counts = buf();
+  t.offsets = buf(); t.token_request = buf(); t.blocks = buf(); t.carried = buf(); t.slot_map = buf(); t.counts = buf();
   return t;
 }
 static ss_head_scan_params scan(void) {
@@ -140,7 +141,7 @@ static ss_request_tables_params tab(void) {
   ss_request_tables_params p;
   memset(&p, 0, sizeof(p));
   p.abi_version = SS_ABI_VERSION; p.requests = 3; p.tokens = 256; p.block = 128; p.max_blocks = 5;
-  p.lengths = buf(); p.offsets = buf(); p.token_request = buf(); p.token_position = buf(); p.blocks = buf(); p.slot_map = buf();
+  p.lengths = buf(); p.offsets = buf(); p.token_request = buf(); p.token_position = buf(); p.blocks = buf(); p.carried = buf(); p.slot_map = buf();
   p.counts = buf();
   return p;
 }
