@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
       for (int i = tid; i < prow; i += kScanThreads) out[t * p.so[0] + i] = from_f<T>(0.f);
     return;
   }
+  if (SUMMARY) let_next_start(); else wait_for_previous();
   const int blk = SUMMARY ? p.t.carried[blockIdx.x] : blockIdx.x;
   if (blk < 0) return;
   const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blk];
@@ -164,6 +165,8 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
 // One thread: 4 values of one head's state, along a request's blocks. The loads
 // do not wait for one another, only the sums do.
 __global__ void __launch_bounds__(256) ss_head_scan_carry_kernel(const __grid_constant__ HeadScanParams p, int pieces) {
+  let_next_start();
+  wait_for_previous();
   const int blk = p.t.carried[blockIdx.x / (p.heads * pieces)], rest = blockIdx.x % (p.heads * pieces), h = rest / pieces;
   if (blk < 0) return;
   const int4 row = reinterpret_cast<const int4 *>(p.t.blocks)[blk];
@@ -209,7 +212,7 @@ void go(const HeadScanParams &p, cudaStream_t s) {
     ss_head_scan_kernel<T, NPL, true><<<dim3(p.t.tokens / p.t.block, grid.y), kScanThreads, 0, s>>>(p);
     launch_head_scan_carry(p, s);
   }
-  ss_head_scan_kernel<T, NPL, false><<<grid, kScanThreads, 0, s>>>(p);
+  launch_after(ss_head_scan_kernel<T, NPL, false>, grid, kScanThreads, 0, s, p.split, p);
 }
 template <typename T>
 void by_states(const HeadScanParams &p, cudaStream_t s) {
@@ -226,8 +229,7 @@ cudaError_t launch_head_scan_carry(const HeadScanParams &p, cudaStream_t s) {
   const int pieces = (p.headdim * p.dstate + 1023) / 1024;
   const long long ctas = (long long)(p.t.tokens / p.t.block) * p.heads * pieces;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  ss_head_scan_carry_kernel<<<(unsigned)ctas, 256, 0, s>>>(p, pieces);
-  return cudaGetLastError();
+  return launch_after(ss_head_scan_carry_kernel, dim3((unsigned)ctas), 256, 0, s, true, p, pieces);
 }
 
 cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s) {

@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   unsigned char *ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   SumShared &sh = *reinterpret_cast<SumShared *>(ring + kSumStages * (2 + NB) * kBox);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wq = warp & 3, wg = (warp >> 2) & 3;
+  let_next_start();
   const Place at = place_of<HT, true>(p);
   if (at.r < 0) return;
   const int pc = wq * 32 + lane, hs = HT == 2 ? pc >> 6 : 0, pp = HT == 2 ? pc & 63 : pc, h = at.h0 + hs;
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const Place at = place_of<HT, false>(p);
   const int h0 = at.h0, hend = at.hend, first = at.first, size = at.size, index = at.index;
   T *out = static_cast<T *>(p.out);
+  if (at.r < 0) wait_for_previous();
   if (at.blk == p.t.max_blocks) {                       // past the last token: zeros
     const int cols = min(HT, hend - h0) * p.headdim;
     for (int t = p.t.counts[0] + warp; t < p.t.tokens; t += kTcThreads / 32)
@@ -576,6 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     fence_before();
   }
+  wait_for_previous();  // the start states
   __syncthreads();
   fence_after();
   const uint32_t tm = sh.tmem;
@@ -1101,8 +1104,7 @@ cudaError_t go(const HeadScanParams &p, const TcMaps &maps, cudaStream_t s) {
     e = launch_head_scan_carry(p, s);
     if (e != cudaSuccess) return e;
   }
-  fwd<<<(unsigned)ctas, kTcThreads, smem, s>>>(p, maps);
-  return cudaGetLastError();
+  return launch_after(fwd, dim3((unsigned)ctas), kTcThreads, smem, s, p.split, p, maps);
 }
 
 template <typename T>

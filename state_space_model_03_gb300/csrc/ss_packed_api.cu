@@ -375,9 +375,8 @@ int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int6
     }
   }
   int64_t block = (steps + best - 1) / best * step;
-  // A batch whose requests need no cut may still hold one long request. A small
-  // one is better off without the second launch.
-  if (best == 1) block = std::max(block, tc && tokens <= 8 * step ? (tokens + step - 1) / step * step : 4 * step);
+  // A batch whose requests need no cut may still hold one long request.
+  if (best == 1) block = std::max(block, (tc ? 8 : 4) * step);
   return std::min<int64_t>(std::max<int64_t>(block, step), 1 << 19);
 }
 
