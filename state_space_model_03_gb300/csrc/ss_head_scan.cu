@@ -3,9 +3,9 @@
 // token in fp32. Per request and head, with S (headdim x dstate):
 //   S = exp(dt A) S + dt x B^T;  y = S C + D x;  out = y silu(z).
 //
-// One CTA carries 64 rows of one head's state in registers through one block of
-// a request (16 lanes a row, 4 rows a lane), and stages 16 tokens at a time in
-// shared memory. It is bound by the fp32 operations, three for every state value
+// One CTA carries 64 (or 32) rows of one head's state in registers through one
+// block of a request (16 lanes a row), and stages 16 tokens at a time in shared
+// memory. It is bound by the fp32 operations, three for every state value
 // and token. When requests may have several blocks, a first launch brings every
 // block but the last from zero (the first one from the request's start) to its
 // end, a second one carries these ends on from block to block, and the third
@@ -16,12 +16,13 @@
 namespace ssk {
 namespace {
 
-constexpr int kLanes = 16, kRowsPerLane = 4, kRows = 64, kTokens = 16;
-constexpr int kScanThreads = kLanes * kRows / kRowsPerLane;
+constexpr int kLanes = 16, kScanThreads = 256, kTokens = 16;
 
-template <typename T, int NPL, bool SUMMARY>
+// NPL states and RPL rows per lane.
+template <typename T, int NPL, int RPL, bool SUMMARY>
 __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid_constant__ HeadScanParams p) {
-  constexpr int V = NPL < 4 ? NPL : 4, Q = NPL / V, NP = kLanes * NPL;
+  constexpr int V = NPL < 4 ? NPL : 4, Q = NPL / V, NP = kLanes * NPL, NF = (NPL + 1) / 2;
+  constexpr int kRows = kScanThreads / kLanes * RPL;
   __shared__ __align__(16) float xs[kTokens][kRows];
   __shared__ __align__(16) float bs[kTokens][NP];
   __shared__ __align__(16) float cs[SUMMARY ? 1 : kTokens][NP];
@@ -56,18 +57,23 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
   };
   auto decay_of = [&](int i) { return p.ws_decay + (long long)(blk - index + i) * p.heads + h; };
 
-  float s[kRowsPerLane][NPL];
-  auto each = [&](auto f) {  // f(row, state, register) over the lane's values
+  f2 s[RPL][NF];  // pairs of states; a lone one is paired with 0
+  auto each = [&](auto f) {  // f(is one, offset of row and state, value)
 #pragma unroll
-    for (int u = 0; u < kRowsPerLane; ++u)
+    for (int u = 0; u < RPL; ++u)
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int pr = rg * kRowsPerLane + u, n = V * (j + kLanes * q) + i;
-          f(pr < prow && n < p.dstate, (long long)pr * p.dstate + n, s[u][q * V + i]);
-        }
+      for (int k = 0; k < NF; ++k) {
+        float2 v = upk(s[u][k]);
+        const int pr = rg * RPL + u, n = V * (j + kLanes * (2 * k / V)) + 2 * k % V;
+        f(pr < prow && n < p.dstate, (long long)pr * p.dstate + n, v.x);
+        if (NPL > 1) f(pr < prow && n + 1 < p.dstate, (long long)pr * p.dstate + n + 1, v.y);
+        s[u][k] = pk(v.x, v.y);
+      }
   };
+#pragma unroll
+  for (int u = 0; u < RPL; ++u)
+#pragma unroll
+    for (int k = 0; k < NF; ++k) s[u][k] = pk(0.f, 0.f);
   auto load = [&](const float *src) {
     each([&](bool in, long long at, float &v) { v = src && in ? src[at] : 0.f; });
   };
@@ -113,33 +119,63 @@ __global__ void __launch_bounds__(kScanThreads) ss_head_scan_kernel(const __grid
     __syncthreads();
     for (int t = 0; t < n_tok; ++t) {
       const float dt = dts[t], keep = ex2(keeps[t]);
-      float b[NPL], c[NPL], y[kRowsPerLane], in[kRowsPerLane];
       decay += keeps[t];
+      const f2 keep2 = pk(keep, keep);
+      f2 b[NF], c[NF];
+      auto pairs = [&](const float *src, f2 (&v)[NF]) {
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          b[q * V + i] = bs[t][V * (j + kLanes * q) + i];
-          if (!SUMMARY) c[q * V + i] = cs[t][V * (j + kLanes * q) + i];
+        for (int q = 0; q < Q; ++q) {
+          const float *at = src + V * (j + kLanes * q);
+          if constexpr (V == 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(at);
+            v[2 * q] = pk(f.x, f.y);
+            v[2 * q + 1] = pk(f.z, f.w);
+          } else if constexpr (V == 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(at);
+            v[q] = pk(f.x, f.y);
+          } else {
+            v[q] = pk(*at, 0.f);
+          }
         }
+      };
+      pairs(bs[t], b);
+      if (!SUMMARY) pairs(cs[t], c);
+      float y[RPL];
 #pragma unroll
-      for (int u = 0; u < kRowsPerLane; ++u) {
-        in[u] = dt * xs[t][rg * kRowsPerLane + u];
-        y[u] = 0.f;
+      for (int u = 0; u < RPL; ++u) {
+        const float in = dt * xs[t][rg * RPL + u];
+        const f2 in2 = pk(in, in);
+        f2 acc = pk(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < NPL; ++k) {
-          s[u][k] = fmaf(keep, s[u][k], in[u] * b[k]);
-          if (!SUMMARY) y[u] = fmaf(c[k], s[u][k], y[u]);
+        for (int k = 0; k < NF; ++k) {
+          s[u][k] = fma2(keep2, s[u][k], mul2(in2, b[k]));
+          if (!SUMMARY) acc = fma2(c[k], s[u][k], acc);
         }
+        const float2 a = upk(acc);
+        y[u] = a.x + a.y;
       }
       if (!SUMMARY) {
+        // sums over the 16 lanes: with several rows a lane hands half of them over at
+        // each exchange, until it has one
+        int row = rg * RPL;
+        if constexpr (RPL == 4) {
+          const bool up = j & 8;
+          const float a0 = up ? y[0] : y[2], a1 = up ? y[1] : y[3];
+          const float k0 = up ? y[2] : y[0], k1 = up ? y[3] : y[1];
+          y[0] = k0 + __shfl_xor_sync(0xffffffffu, a0, 8);
+          y[1] = k1 + __shfl_xor_sync(0xffffffffu, a1, 8);
+          row += up ? 2 : 0;
+        }
+        constexpr int kPair = RPL == 4 ? 4 : 8;  // the exchange that leaves one row of two
+        if constexpr (RPL >= 2) {
+          const bool up = j & kPair;
+          const float a = up ? y[0] : y[1], k = up ? y[1] : y[0];
+          y[0] = k + __shfl_xor_sync(0xffffffffu, a, kPair);
+          row += up ? 1 : 0;
+        }
 #pragma unroll
-        for (int u = 0; u < kRowsPerLane; ++u)
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) y[u] += __shfl_xor_sync(0xffffffffu, y[u], o);
-#pragma unroll
-        for (int u = 0; u < kRowsPerLane; ++u)
-          if (j == u) ys[t][rg * kRowsPerLane + u] = y[u];
+        for (int o = RPL >= 2 ? kPair / 2 : 8; o > 0; o >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
+        if (j % (kLanes / RPL) == 0) ys[t][row] = y[0];
       }
     }
     if (!SUMMARY) {
@@ -205,22 +241,28 @@ __global__ void __launch_bounds__(256) ss_head_scan_carry_kernel(const __grid_co
   }
 }
 
-template <typename T, int NPL>
+template <typename T, int NPL, int RPL>
 void go(const HeadScanParams &p, cudaStream_t s) {
-  const dim3 grid(p.t.max_blocks + 1, p.heads * ((p.headdim + kRows - 1) / kRows));
+  constexpr int rows = kScanThreads / kLanes * RPL;
+  const dim3 grid(p.t.max_blocks + 1, p.heads * ((p.headdim + rows - 1) / rows));
   if (p.split) {
-    ss_head_scan_kernel<T, NPL, true><<<dim3(p.t.tokens / p.t.block, grid.y), kScanThreads, 0, s>>>(p);
+    ss_head_scan_kernel<T, NPL, RPL, true><<<dim3(p.t.tokens / p.t.block, grid.y), kScanThreads, 0, s>>>(p);
     launch_head_scan_carry(p, s);
   }
-  launch_after(ss_head_scan_kernel<T, NPL, false>, grid, kScanThreads, 0, s, p.split, p);
+  launch_after(ss_head_scan_kernel<T, NPL, RPL, false>, grid, kScanThreads, 0, s, p.split, p);
 }
-template <typename T>
+template <typename T, int RPL>
 void by_states(const HeadScanParams &p, cudaStream_t s) {
-  if (p.dstate > 128) go<T, 16>(p, s);
-  else if (p.dstate > 64) go<T, 8>(p, s);
-  else if (p.dstate > 32) go<T, 4>(p, s);
-  else if (p.dstate > 16) go<T, 2>(p, s);
-  else go<T, 1>(p, s);
+  if (p.dstate > 128) go<T, 16, RPL>(p, s);
+  else if (p.dstate > 64) go<T, 8, RPL>(p, s);
+  else if (p.dstate > 32) go<T, 4, RPL>(p, s);
+  else if (p.dstate > 16) go<T, 2, RPL>(p, s);
+  else go<T, 1, RPL>(p, s);
+}
+// 64 rows of a head's state per CTA, or 32 where that leaves fewer rows empty
+template <typename T>
+void by_rows(const HeadScanParams &p, cudaStream_t s) {
+  if ((p.headdim + 31) / 32 % 2) by_states<T, 2>(p, s); else by_states<T, 4>(p, s);
 }
 
 }  // namespace
@@ -233,9 +275,9 @@ cudaError_t launch_head_scan_carry(const HeadScanParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s) {
-  if (dtype == 0) by_states<float>(p, s);
-  else if (dtype == 1) by_states<__half>(p, s);
-  else by_states<__nv_bfloat16>(p, s);
+  if (dtype == 0) by_rows<float>(p, s);
+  else if (dtype == 1) by_rows<__half>(p, s);
+  else by_rows<__nv_bfloat16>(p, s);
   return cudaGetLastError();
 }
 
