@@ -142,7 +142,8 @@ int ss_packed_conv1d_update(const ss_packed_conv1d_update_params *p, void *strea
  *                the last two contiguous; NULL: every request starts from 0
  *                and nothing is kept.
  *   workspace    ss_head_scan_workspace_size bytes, 16-byte aligned; needed
- *                when a request may have more than one block (tokens > block).
+ *                when a request may have more than one block (tokens > block),
+ *                and for 16-bit operands that do not lie in rows of 16 bytes.
  *
  * Sizes: 1 <= headdim, dstate <= 256, heads a multiple of ngroups.
  */

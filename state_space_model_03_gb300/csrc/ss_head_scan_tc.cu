@@ -161,6 +161,22 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *tm, const void *
                : "memory");
 }
 
+// Four states of a row, `left` of them in it.
+__device__ __forceinline__ float4 get4(const float *src, int left, bool vec) {
+  if (vec) return *reinterpret_cast<const float4 *>(src);
+  return make_float4(src[0], left > 1 ? src[1] : 0.f, left > 2 ? src[2] : 0.f, left > 3 ? src[3] : 0.f);
+}
+__device__ __forceinline__ void put4(float *dst, float4 v, int left, bool vec) {
+  if (vec) {
+    *reinterpret_cast<float4 *>(dst) = v;
+  } else {
+    dst[0] = v.x;
+    if (left > 1) dst[1] = v.y;
+    if (left > 2) dst[2] = v.z;
+    if (left > 3) dst[3] = v.w;
+  }
+}
+
 // Barrier of the 8 column warps.
 __device__ __forceinline__ void sync_weighers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // One arrival per warp, after all its lanes.
@@ -495,11 +511,11 @@ __global__ void __launch_bounds__(kSumThreads, 1)
                                  __uint_as_float(v[k + 2]) * unscale, __uint_as_float(v[k + 3]) * unscale);
           if (start) {
             // the last block's entry keeps the start, which the cache loses when that block ends
-            const float4 q = *reinterpret_cast<const float4 *>(start + n + k);
-            *reinterpret_cast<float4 *>(entry_row(p, at, h, pp, at.last) + n0 + n + k) = q;
+            const float4 q = get4(start + n + k, nv - n - k, p.vec != 0);
+            put4(entry_row(p, at, h, pp, at.last) + n0 + n + k, q, nv - n - k, p.vec != 0);
             f = make_float4(fmaf(keep, q.x, f.x), fmaf(keep, q.y, f.y), fmaf(keep, q.z, f.z), fmaf(keep, q.w, f.w));
           }
-          *reinterpret_cast<float4 *>(dst + n + k) = f;
+          put4(dst + n + k, f, nv - n - k, p.vec != 0);
         }
     }
     if (pin && pp == 0 && wg == 0 && !*dead) p.ws_decay[entry_of(p, at, h, at.index)] = sh.total[hs];
@@ -545,7 +561,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int wg = (warp >> 2) & 1, wq = warp & 3;
   const int pc = wq * 32 + lane, hs = HT == 2 ? pc >> 6 : 0, pp = HT == 2 ? pc & 63 : pc;
   const bool pin = warp >= 16 && warp < 24 && h0 + hs < hend && pp < p.headdim;
-  const int n0 = wg * NH, nv = min(max(p.dstate - n0, 0), NH);  // a multiple of 8
+  const int n0 = wg * NH, nv = min(max(p.dstate - n0, 0), NH);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.full_x[i], 1);
@@ -794,7 +810,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
                   if (n + i < nv) {
-                    const float4 f = *reinterpret_cast<const float4 *>(src + n + i);
+                    const float4 f = get4(src + n + i, nv - n - i, p.vec != 0);
                     v[i] = f.x;
                     v[i + 1] = f.y;
                     v[i + 2] = f.z;
@@ -831,7 +847,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               float *dst = cache_row(p, at, h0 + hs, pp) + n0 + n;
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
-                if (n + i < nv) *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                if (n + i < nv) put4(dst + i, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), nv - n - i, p.vec != 0);
             }
           }
           if (!more) break;
@@ -1130,20 +1146,59 @@ bool map3(TensorMapEncode enc, CUtensorMap *m, const void *base, int width, int 
 
 }  // namespace
 
-// Whether the operands suit the tensor-core form: 16-bit, TMA's alignments, and
-// sizes that its tiles hold.
-bool head_scan_tc_fits(int dtype, const HeadScanParams &p) {
-  if (dtype == 0 || p.headdim > 128 || p.dstate > 128 || p.headdim % 8 || p.dstate % 8) return false;
-  auto rows = [&](const void *base, const long long *st, int n) {
-    if (!base) return true;
-    const bool a = reinterpret_cast<uintptr_t>(base) % 16 == 0;
-    return a && (n == 1 || (st[1] % 8 == 0 && st[1] > 0)) && (p.t.tokens == 1 || (st[0] % 8 == 0 && st[0] > 0));
+bool head_scan_tc_sizes(int dtype, const HeadScanParams &p) { return dtype != 0 && p.headdim <= 128 && p.dstate <= 128; }
+
+int head_scan_tc_unaligned(const HeadScanParams &p) {
+  auto off = [&](const void *base, const long long *st, int n) {
+    if (!base) return false;
+    return reinterpret_cast<uintptr_t>(base) % 16 != 0 || (n > 1 && (st[1] % 8 != 0 || st[1] == 0)) ||
+           (p.t.tokens > 1 && (st[0] % 8 != 0 || st[0] == 0));
   };
   const int groups = p.heads / p.hpg;
-  return rows(p.x, p.sx, p.heads) && rows(p.z, p.sz, p.heads) && rows(p.out, p.so, p.heads) && rows(p.B, p.sB, groups) &&
-         rows(p.C, p.sC, groups) &&
-         (!p.state || (reinterpret_cast<uintptr_t>(p.state) % 16 == 0 && (p.heads == 1 || p.ss[1] % 4 == 0) &&
-                       (p.slots <= 1 || p.ss[0] % 4 == 0)));
+  return (off(p.x, p.sx, p.heads) ? kRowsX : 0) | (off(p.B, p.sB, groups) ? kRowsB : 0) | (off(p.C, p.sC, groups) ? kRowsC : 0) |
+         (off(p.z, p.sz, p.heads) ? kRowsZ : 0) | (off(p.out, p.so, p.heads) || p.headdim % 8 != 0 ? kRowsOut : 0);
+}
+
+namespace {
+
+// One thread: 8 values of a row of the copy.
+template <bool TO>
+__global__ void __launch_bounds__(256) rows_kernel(uint16_t *strided, long long st0, long long st1, uint4 *rows, int n_rows, int width,
+                                                   long long total) {
+  const long long i = blockIdx.x * 256ll + threadIdx.x;
+  if (i >= total) return;
+  const int per = (width + 7) / 8, w = (int)(i % per) * 8;
+  const long long tr = i / per;
+  uint16_t *at = strided + tr / n_rows * st0 + tr % n_rows * st1 + w;
+  uint32_t v[4] = {};
+  if (TO) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (w + k < width) v[k / 2] |= (uint32_t)at[k] << (16 * (k % 2));
+    rows[i] = make_uint4(v[0], v[1], v[2], v[3]);
+  } else {
+    const uint4 q = rows[i];
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (w + k < width) at[k] = (uint16_t)(v[k / 2] >> (16 * (k % 2)));
+  }
+}
+template <bool TO>
+cudaError_t copy_rows(void *strided, const long long *st, void *rows, int tokens, int n, int width, cudaStream_t s) {
+  const long long total = (long long)tokens * n * ((width + 7) / 8), ctas = (total + 255) / 256;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  rows_kernel<TO><<<(unsigned)ctas, 256, 0, s>>>(static_cast<uint16_t *>(strided), st[0], st[1], static_cast<uint4 *>(rows), n, width, total);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_to_rows(const void *src, const long long *st, void *dst, int tokens, int rows, int width, cudaStream_t s) {
+  return copy_rows<true>(const_cast<void *>(src), st, dst, tokens, rows, width, s);
+}
+cudaError_t launch_from_rows(const void *src, void *dst, const long long *st, int tokens, int rows, int width, cudaStream_t s) {
+  return copy_rows<false>(dst, st, const_cast<void *>(src), tokens, rows, width, s);
 }
 
 cudaError_t launch_head_scan_tc(int dtype, const HeadScanParams &p, TensorMapEncode enc, cudaStream_t s) {

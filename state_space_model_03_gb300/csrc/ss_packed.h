@@ -58,6 +58,7 @@ struct HeadScanParams {
   int heads, headdim, dstate, hpg;
   int softplus, dt_f32;
   int split;  // a request may have several blocks: ws holds their summaries
+  int vec;    // 16-byte accesses of state rows allowed
   long long slots;
   const void *x, *dt, *B, *C, *z;
   const float *A, *D, *bias;
@@ -81,7 +82,16 @@ cudaError_t launch_head_scan_carry(const HeadScanParams &p, cudaStream_t s);  //
 // The same on the tensor cores, for 16-bit operands that TMA can describe.
 typedef void *TensorMapEncode;  // the driver's cuTensorMapEncodeTiled
 TensorMapEncode packed_map_encode();
-bool head_scan_tc_fits(int dtype, const HeadScanParams &p);
+// Whether the tensor cores' tiles hold the sizes, and which operands do not lie in
+// the 16-byte rows that TMA wants: these are copied to such rows first (and out
+// back from them), `p` then has the copies.
+bool head_scan_tc_sizes(int dtype, const HeadScanParams &p);
+enum { kRowsX = 1, kRowsB = 2, kRowsC = 4, kRowsZ = 8, kRowsOut = 16 };
+int head_scan_tc_unaligned(const HeadScanParams &p);
+// (tokens, rows, width) in 16-bit values between a strided tensor and contiguous
+// rows of `width` rounded up to 8: to_rows zeroes what is past the width.
+cudaError_t launch_to_rows(const void *src, const long long *st, void *dst, int tokens, int rows, int width, cudaStream_t s);
+cudaError_t launch_from_rows(const void *src, void *dst, const long long *st, int tokens, int rows, int width, cudaStream_t s);
 cudaError_t launch_head_scan_tc(int dtype, const HeadScanParams &p, TensorMapEncode enc, cudaStream_t s);
 
 // Programmatic dependent launch of a scan's later launches: each lets the next one

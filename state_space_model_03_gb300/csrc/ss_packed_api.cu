@@ -229,10 +229,54 @@ int validate_heads(const P *p, int64_t rows) {
 // Blocks past a request's first exist only where a request can be longer than one.
 bool may_split(const ss_packed_tables &t) { return t.tokens > t.block; }
 
-int64_t ws_need(const ss_head_scan_params *p) {
-  if (!may_split(p->tables)) return 0;
-  const int64_t entries = p->tables.max_blocks * p->heads;
-  return (entries * p->headdim * p->dstate + entries) * 4;
+ssk::HeadScanParams scan_params(const ss_head_scan_params *p) {
+  ssk::HeadScanParams k{};
+  k.heads = (int)p->heads;
+  k.headdim = (int)p->headdim;
+  k.dstate = (int)p->dstate;
+  k.hpg = (int)(p->heads / p->ngroups);
+  k.softplus = p->dt_softplus != 0;
+  k.dt_f32 = p->dt_dtype == SS_F32;
+  k.split = may_split(p->tables);
+  k.slots = p->slots;
+  k.x = p->x; k.dt = p->dt; k.B = p->B; k.C = p->C; k.z = p->z;
+  k.A = p->A; k.D = p->D; k.bias = p->dt_bias;
+  k.state = p->state;
+  k.out = p->out;
+  for (int i = 0; i < 2; ++i) {
+    k.sx[i] = p->x_stride[i]; k.sdt[i] = p->dt_stride[i]; k.sB[i] = p->B_stride[i]; k.sC[i] = p->C_stride[i];
+    k.sz[i] = p->z ? p->z_stride[i] : 0; k.so[i] = p->out_stride[i]; k.ss[i] = p->state ? p->state_stride[i] : 0;
+  }
+  k.vec = p->dstate % 4 == 0 && (!p->state || (aligned(p->state, 16) && (p->heads == 1 || k.ss[1] % 4 == 0) &&
+                                               (p->slots <= 1 || k.ss[0] % 4 == 0)));
+  k.t = tables_of(p->tables);
+  return k;
+}
+
+// Workspace: the summaries' states and decays, then copies of the operands that do
+// not lie in 16-byte rows, each on 16 bytes.
+struct Workspace {
+  int64_t states = 0, decays = 0, copies = 0, bytes = 0;  // values; offset of the copies; all
+  int64_t rows_x = 0, rows_bc = 0;                        // bytes of one copy of x, z or out; of B or C
+  int unaligned = 0;
+};
+Workspace workspace_of(const ss_head_scan_params *p) {
+  Workspace w;
+  if (p->tables.tokens == 0) return w;
+  if (may_split(p->tables)) {
+    w.decays = p->tables.max_blocks * p->heads;
+    w.states = w.decays * p->headdim * p->dstate;
+  }
+  w.copies = w.bytes = (w.states + w.decays) * 4;
+  const ssk::HeadScanParams k = scan_params(p);
+  if (!ssk::head_scan_tc_sizes(p->dtype, k) || (w.unaligned = ssk::head_scan_tc_unaligned(k)) == 0) return w;
+  w.copies = (w.bytes + 15) / 16 * 16;
+  w.rows_x = p->tables.tokens * p->heads * ((p->headdim + 7) / 8) * 16;
+  w.rows_bc = p->tables.tokens * p->ngroups * ((p->dstate + 7) / 8) * 16;
+  const int u = w.unaligned;
+  w.bytes = w.copies + w.rows_x * (!!(u & ssk::kRowsX) + !!(u & ssk::kRowsZ) + !!(u & ssk::kRowsOut)) +
+            w.rows_bc * (!!(u & ssk::kRowsB) + !!(u & ssk::kRowsC));
+  return w;
 }
 
 int validate_operands(const ss_head_scan_params *p) {
@@ -245,7 +289,7 @@ int validate_operands(const ss_head_scan_params *p) {
 int validate(const ss_head_scan_params *p) {
   const int st = validate_operands(p);
   if (st != SS_OK) return st;
-  const int64_t need = ws_need(p);
+  const int64_t need = workspace_of(p).bytes;
   if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return SS_ERR_SCRATCH;
   if (need > 0 && !aligned(p->workspace, 16)) return SS_ERR_ALIGN;
   return SS_OK;
@@ -312,7 +356,7 @@ int ss_head_scan_workspace_size(const ss_head_scan_params *p, int64_t *bytes) {
   if (!bytes) return SS_ERR_NULL;
   const int st = validate_operands(p);
   if (st != SS_OK) return st;
-  *bytes = ws_need(p);
+  *bytes = workspace_of(p).bytes;
   return SS_OK;
 }
 
@@ -321,36 +365,46 @@ int ss_head_scan(const ss_head_scan_params *p, void *stream) {
   if (st != SS_OK) return st;
   if (p->tables.tokens == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
-  ssk::HeadScanParams k{};
-  k.heads = (int)p->heads;
-  k.headdim = (int)p->headdim;
-  k.dstate = (int)p->dstate;
-  k.hpg = (int)(p->heads / p->ngroups);
-  k.softplus = p->dt_softplus != 0;
-  k.dt_f32 = p->dt_dtype == SS_F32;
-  k.split = may_split(p->tables);
-  k.slots = p->slots;
-  k.x = p->x; k.dt = p->dt; k.B = p->B; k.C = p->C; k.z = p->z;
-  k.A = p->A; k.D = p->D; k.bias = p->dt_bias;
-  k.state = p->state;
-  k.out = p->out;
-  for (int i = 0; i < 2; ++i) {
-    k.sx[i] = p->x_stride[i]; k.sdt[i] = p->dt_stride[i]; k.sB[i] = p->B_stride[i]; k.sC[i] = p->C_stride[i];
-    k.sz[i] = p->z ? p->z_stride[i] : 0; k.so[i] = p->out_stride[i]; k.ss[i] = p->state ? p->state_stride[i] : 0;
-  }
+  ssk::HeadScanParams k = scan_params(p);
+  const Workspace w = workspace_of(p);
+  const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   if (k.split) {
     k.ws_state = static_cast<float *>(p->workspace);
-    k.ws_decay = k.ws_state + p->tables.max_blocks * p->heads * p->headdim * p->dstate;
+    k.ws_decay = k.ws_state + w.states;
   }
   k.err = ssk::packed_error_word();
   if (!k.err) return SS_ERR_CUDA;
-  k.t = tables_of(p->tables);
-  if (ssk::head_scan_tc_fits(p->dtype, k)) {
-    const ssk::TensorMapEncode enc = ssk::packed_map_encode();
-    if (!enc) return SS_ERR_CUDA;
-    return launched(ssk::launch_head_scan_tc(p->dtype, k, enc, static_cast<cudaStream_t>(stream)));
+  if (!ssk::head_scan_tc_sizes(p->dtype, k)) return launched(ssk::launch_head_scan(p->dtype, k, st_));
+  const ssk::TensorMapEncode enc = ssk::packed_map_encode();
+  if (!enc) return SS_ERR_CUDA;
+  // operands that TMA cannot describe go through rows that it can: a copy of them
+  // costs a fraction of what the form without tensor cores takes
+  char *at = static_cast<char *>(p->workspace) + w.copies;
+  const int tokens = k.t.tokens, groups = (int)p->ngroups;
+  cudaError_t e = cudaSuccess;
+  auto to_rows = [&](int which, const void *&ptr, long long *strides, int rows, int width, int64_t bytes) {
+    if (!(w.unaligned & which) || e != cudaSuccess) return;
+    e = ssk::launch_to_rows(ptr, strides, at, tokens, rows, width, st_);
+    ptr = at;
+    strides[1] = (width + 7) / 8 * 8;
+    strides[0] = rows * strides[1];
+    at += bytes;
+  };
+  to_rows(ssk::kRowsX, k.x, k.sx, k.heads, k.headdim, w.rows_x);
+  to_rows(ssk::kRowsZ, k.z, k.sz, k.heads, k.headdim, w.rows_x);
+  to_rows(ssk::kRowsB, k.B, k.sB, groups, k.dstate, w.rows_bc);
+  to_rows(ssk::kRowsC, k.C, k.sC, groups, k.dstate, w.rows_bc);
+  if (e != cudaSuccess) return SS_ERR_CUDA;
+  void *const out = k.out;
+  const long long so[2] = {k.so[0], k.so[1]};
+  if (w.unaligned & ssk::kRowsOut) {
+    k.out = at;
+    k.so[1] = (k.headdim + 7) / 8 * 8;
+    k.so[0] = k.heads * k.so[1];
   }
-  return launched(ssk::launch_head_scan(p->dtype, k, static_cast<cudaStream_t>(stream)));
+  e = ssk::launch_head_scan_tc(p->dtype, k, enc, st_);
+  if (e == cudaSuccess && (w.unaligned & ssk::kRowsOut)) e = ssk::launch_from_rows(k.out, out, so, tokens, k.heads, k.headdim, st_);
+  return launched(e);
 }
 
 int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int64_t headdim, int32_t dtype, int32_t sms) {
