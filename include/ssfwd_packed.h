@@ -146,6 +146,15 @@ int ss_packed_conv1d_update(const ss_packed_conv1d_update_params *p, void *strea
  *                and for 16-bit operands that do not lie in rows of 16 bytes.
  *
  * Sizes: 1 <= headdim, dstate <= 256, heads a multiple of ngroups.
+ *
+ * 16-bit operands with headdim, dstate <= 128 run on the tensor cores, 128
+ * tokens at a time; the state stays in fp32 (its sums take every bit of bf16
+ * operands, 22 bits of each fp16 term). Two things follow from that form: a NaN
+ * or infinity in a token's x also reaches the outputs of the same request's
+ * tokens before it in its 128 (never another request's), and with fp16 operands
+ * the products C.B and the state are rounded to fp16 where they enter the
+ * output, so they have to stay below 65504. Other operands run token by token
+ * in fp32.
  */
 typedef struct ss_head_scan_params {
   int32_t abi_version, dtype, dt_dtype, dt_softplus;

@@ -164,10 +164,19 @@ PyObject *request_tables(PyObject *, PyObject *const *a, Py_ssize_t given) {
     if (tokens < 0 || block < 1) refuse(PyExc_ValueError, "num_tokens must be >= 0 and block >= 1");
     const int64_t most = tokens / block + std::min(n, tokens);
     const c10::cuda::CUDAGuard guard(len.device());
-    auto table = [&](int64_t k) { return at::empty({k}, len.options()); };
-    // one allocation each: the tables outlive one another
-    at::Tensor off = table(n + 1), req = table(tokens), pos = table(tokens), blk = at::empty({most, 4}, len.options()), slt = table(n),
-               cnt = table(4), car = table(tokens / block);
+    // one allocation for all tables, each on 16 bytes of it
+    const int64_t sizes[7] = {n + 1, tokens, tokens, 4 * most, n, 4, tokens / block};
+    int64_t start[8] = {};
+    for (int i = 0; i < 7; ++i) start[i + 1] = start[i] + (sizes[i] + 3) / 4 * 4;
+    const at::Tensor all = at::empty({start[7]}, len.options());
+    int32_t *const base = all.data_ptr<int32_t>();
+    auto table = [&](int i) {
+      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+      t.unsafeGetTensorImpl()->set_storage_offset(start[i]);
+      if (i == 3) t.unsafeGetTensorImpl()->set_sizes_contiguous({most, 4});
+      else t.unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
+      return t;
+    };
     ss_request_tables_params p{};
     p.abi_version = SS_ABI_VERSION;
     p.requests = n;
@@ -179,19 +188,18 @@ PyObject *request_tables(PyObject *, PyObject *const *a, Py_ssize_t given) {
     p.context = iptr(context.get());
     p.slots = iptr(slots.get());
     p.free_slots = iptr(free.get());
-    p.offsets = off.data_ptr<int32_t>();
-    p.token_request = req.data_ptr<int32_t>();
-    p.token_position = pos.data_ptr<int32_t>();
-    p.blocks = blk.data_ptr<int32_t>();
-    p.carried = car.data_ptr<int32_t>();
-    p.slot_map = slt.data_ptr<int32_t>();
-    p.counts = cnt.data_ptr<int32_t>();
+    p.offsets = base + start[0];
+    p.token_request = base + start[1];
+    p.token_position = base + start[2];
+    p.blocks = base + start[3];
+    p.carried = base + start[6];
+    p.slot_map = base + start[4];
+    p.counts = base + start[5];
     check(g_tables(&p, stream_of(len)));
     Plan plan{{n, tokens, block, most, p.offsets, p.token_request, p.blocks, p.carried, p.slot_map, p.counts, p.context}, len.get_device()};
     PyObject *r = PyTuple_New(10);
     if (!r) throw python_error();
-    at::Tensor *ts[6] = {&off, &req, &pos, &blk, &slt, &cnt};
-    for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(*ts[i])));
+    for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(table(i)));
     PyTuple_SET_ITEM(r, 6, PyBytes_FromStringAndSize(reinterpret_cast<const char *>(&plan), sizeof(plan)));
     PyTuple_SET_ITEM(r, 7, PyLong_FromLongLong(most));
     if (context.get()) {
@@ -200,7 +208,7 @@ PyObject *request_tables(PyObject *, PyObject *const *a, Py_ssize_t given) {
       Py_INCREF(Py_None);
       PyTuple_SET_ITEM(r, 8, Py_None);
     }
-    PyTuple_SET_ITEM(r, 9, THPVariable_Wrap(std::move(car)));
+    PyTuple_SET_ITEM(r, 9, THPVariable_Wrap(table(6)));
     return r;
   });
 }

@@ -3,9 +3,12 @@
 //   S = exp(dt A) S + dt x_p B_n;  out_p = (sum_n C_n S + D x_p) silu(z_p).
 //
 // Bound by the traffic of the fp32 states, read and written once (8 bytes per
-// value). L lanes share a state row, NV 16-byte pieces each, and a warp has ROWS
+// value). L lanes share a state row, NV 16-byte pieces each, and a warp has kPass
 // rows in flight before it uses the first; dt, the decay and the B and C pieces
-// are the same for all rows of a head and are taken once per warp.
+// are the same for all rows of a head and are taken once per warp. At 256 requests
+// x 80 heads x 64 x 128: 249 us, 5.4 TB/s (80% of the copy bandwidth); 2 rows in
+// flight 311, 8 258; CTAs of 8 warps 297, of 2 251; stores that leave the cache at
+// once, as nothing reads them before the next step, against 253 without.
 #include "ss_fwd_kernel.cuh"
 #include "ss_packed.h"
 
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32) ss_head_update_kernel(const __gri
       if (row < p.headdim && valid[q] > 0) {
         float *dst = st + (long long)row * p.dstate + 4 * (j + q * L);
         if (p.vec && valid[q] == 4) {
-          *reinterpret_cast<float4 *>(dst) = make_float4(s[u][q][0], s[u][q][1], s[u][q][2], s[u][q][3]);
+          __stcs(reinterpret_cast<float4 *>(dst), make_float4(s[u][q][0], s[u][q][1], s[u][q][2], s[u][q][3]));
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
