@@ -8,8 +8,6 @@ twice the unit bounds it: 4e-3 and 5e-4. fp32 outputs and states are sums of a
 few hundred products in fp32, each with a decay whose exponent (up to some tens)
 is rounded to 2^-24: 2e-5 leaves a factor of about ten.
 """
-import math
-
 import numpy as np
 import pytest
 import torch
@@ -252,6 +250,92 @@ def test_scan_step_sizes(dtype, scale):
     p["dt"] = p["dt"].abs() * scale
     t["context"].fill_(1)
     _run_scan(p, t, st, lengths, 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("block", [256, 4096])
+@pytest.mark.parametrize("large_first", [True, False])
+def test_scan_steps_of_different_size(dtype, block, large_first):
+    """Tokens whose steps are next to nothing after ordinary ones, and before: no term overflows or is lost."""
+    lengths = [700]
+    p, t, st = _scan_problem(lengths, 2, 1, 64, 64, dtype, z=False, dt32=True, seed=11)
+    p |= {"dt_bias": None, "dt_softplus": False}
+    p["dt"] = p["dt"].abs() * 0.02
+    part = slice(200, 700) if large_first else slice(0, 500)
+    p["dt"][part] *= 1e-8
+    p["x"][100] *= 100
+    t["context"].fill_(1)
+    _run_scan(p, t, st, lengths, block)
+
+
+def test_steps_and_prompts_in_a_cuda_graph():
+    lengths = [130, 7]
+    p, t, st = _scan_problem(lengths, 2, 1, 64, 64, torch.bfloat16, seed=12)
+    c, _ = _conv_problem(lengths, 40, 4, torch.bfloat16, seed=12)
+    length = _i32(lengths)
+
+    def work():
+        tables = ssm.request_tables(length, 137, block=64, **t)
+        a = ssm.packed_conv1d_fn(c["x"], c["weight"], tables, bias=c["bias"], conv_state=c["conv_state"])
+        b = ssm.head_scan_fn(**p, tables=tables, state=st)
+        q = {k: (v[:2] if k in ("x", "dt", "B", "C", "z") else v) for k, v in p.items()}
+        d = ssm.head_state_update(st, slots=t["slots"], **q)
+        e = ssm.packed_conv1d_update(c["x"][:2], c["conv_state"], c["weight"], slots=t["slots"])
+        return a, b, d, e, st, c["conv_state"]
+
+    keep = st.clone(), c["conv_state"].clone()
+
+    def reset():
+        st.copy_(keep[0])
+        c["conv_state"].copy_(keep[1])
+
+    want = [v.clone() for v in work()]
+    reset()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for _ in range(2):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_caches_and_operands_of_other_strides(dtype):
+    """Slots inside a larger cache, dt of another order, operands without unit stride (copied)."""
+    lengths = [60, 150, 3]
+    p, t, _ = _scan_problem(lengths, 2, 1, 64, 32, dtype, seed=13)
+    big = _rand(_gen(14), 7, 5, 64, 32, std=0.5)
+    st, rest = big[1:6, 2:4], big.clone()
+    p["dt"] = p["dt"].t().contiguous().t()
+    p["B"] = p["B"].transpose(1, 2).contiguous().transpose(1, 2)
+    p["z"] = p["z"].flip(2).contiguous().flip(2)
+    _run_scan(p, t, st, lengths, 64)
+    rest[1:6, 2:4] = st
+    assert torch.equal(big, rest)  # nothing outside the view
+    q = {k: (v[:3] if k in ("x", "dt", "B", "C", "z") else v) for k, v in p.items()}
+    want, wst = oracle.head_scan(**q, lengths=_i32([1] * 3), state=st, slots=t["slots"], context=_i32([1] * 3))
+    _close(ssm.head_state_update(st, slots=t["slots"], **q), want, TOL[dtype])
+    _close(st, wst, STATE_TOL)
+    rest[1:6, 2:4] = st
+    assert torch.equal(big, rest)
+    c, ct = _conv_problem(lengths, 24, 4, dtype, seed=15)
+    wide = _rand(_gen(16), 5, 40, 3, dtype=dtype)
+    c["conv_state"] = wide[:, 8:32]
+    rest = wide.clone()
+    want, wst = oracle.packed_conv1d(**c, lengths=_i32(lengths), **ct)
+    out = ssm.packed_conv1d_fn(c["x"], c["weight"], ssm.request_tables(_i32(lengths), 213, **ct), bias=c["bias"],
+                               conv_state=c["conv_state"])
+    _close(out, want, TOL[dtype])
+    rest[:, 8:32] = torch.from_numpy(wst).to(dtype).cuda()
+    assert torch.equal(wide, rest)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
