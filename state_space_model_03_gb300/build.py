@@ -1,7 +1,8 @@
 """Builds libssfwd.so in-tree (state_space_model_03_gb300/_build/) with nvcc
 for sm_103a only. Translation units compile in parallel; the library links the
 CUDA runtime statically and reaches the driver's tensor-map encoder through the
-runtime's driver entry-point query, so it needs no libcuda at link time.
+runtime's driver entry-point query, so it needs no libcuda at link time. The
+packed operators' Python binding (_packed_bind.so) is built beside it with g++.
 """
 from __future__ import annotations
 
