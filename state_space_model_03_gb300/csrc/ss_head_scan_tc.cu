@@ -71,11 +71,14 @@ struct Shared {
   uint32_t tmem;
   int dead;
   // of chunk c in stage c % 4, by head of the tile
-  float tot[4][2][4];                   // log2 decay of each 32 tokens
+  alignas(16) float tot[4][2][4];       // log2 decay of each 32 tokens
   float top[4][2][4];                   // largest |colf| of each 32 tokens (fp16)
   alignas(16) float nl[4][2][128];      // minus the log2 decay since the start of the 32
   alignas(16) float dt[4][2][128];
   alignas(16) float colf[4][2][128];    // dt times the decay to the end of the 32
+  // pairs of 16 columns on the diagonal that are at or before a row, by the row's
+  // place in its 32 and the half of them that the columns are
+  alignas(16) uint32_t before[2][32][8];
 };
 
 // The code runs once per chunk in several roles at once, so its size counts (the
@@ -603,6 +606,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     sh.dead = 0;
     fence_barrier_init();
   }
+  if (tid < 512) {
+    const int half = tid >> 8, row = (tid >> 3) & 31, c = 16 * half + 2 * (tid & 7);
+    sh.before[half][row][tid & 7] = (c <= row ? 0xffffu : 0u) | (c + 1 <= row ? 0xffff0000u : 0u);
+  }
   if (warp == 25) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -961,7 +968,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t m[8];
             float l = -sh.nl[st][h][trow];
             if (j < wq) {
-              for (int k = j + 1; k < wq; ++k) l += sh.tot[st][h][k];
+              const float4 t4 = *reinterpret_cast<const float4 *>(sh.tot[st][h]);  // those between the two
+              l += (j < 1 && wq > 1 ? t4.y : 0.f) + (j < 2 && wq > 2 ? t4.z : 0.f);
               l = ex2(l);
               const f2 rf = pk(l, l);
               const float *colf = sh.colf[st][h] + 16 * jb;
@@ -973,7 +981,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             } else {
               const float *nl = sh.nl[st][h] + 16 * jb, *dt = sh.dt[st][h] + 16 * jb;
-              const int d = trow - 16 * jb;  // columns up to d are at or before the row
+              const uint32_t *before = sh.before[jb & 1][lane];
               const f2 l2 = pk(l, l);
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
@@ -981,8 +989,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float2 a = upk(add2(l2, pk(n4.x, n4.y))), b = upk(add2(l2, pk(n4.z, n4.w)));
                 const float2 u = upk(mul2(mul2(pk(ex2(a.x), ex2(a.y)), pk(d4.x, d4.y)), pku(g[i], g[i + 1])));
                 const float2 v = upk(mul2(mul2(pk(ex2(b.x), ex2(b.y)), pk(d4.z, d4.w)), pku(g[i + 2], g[i + 3])));
-                m[i / 2] = pack2<T>(i <= d ? u.x : 0.f, i + 1 <= d ? u.y : 0.f);
-                m[i / 2 + 1] = pack2<T>(i + 2 <= d ? v.x : 0.f, i + 3 <= d ? v.y : 0.f);
+                const uint2 keep = *reinterpret_cast<const uint2 *>(before + i / 2);
+                m[i / 2] = pack2<T>(u.x, u.y) & keep.x;
+                m[i / 2 + 1] = pack2<T>(v.x, v.y) & keep.y;
               }
             }
             tm_st8(tg + 8 * h, m);
@@ -991,7 +1000,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // Y = e^L (C S^T), 32 columns
         {
           float e = -sh.nl[st][ho][trow];
-          for (int k = 0; k < wq; ++k) e += sh.tot[st][ho][k];
+          const float4 t4 = *reinterpret_cast<const float4 *>(sh.tot[st][ho]);
+          e += (wq > 0 ? t4.x : 0.f) + (wq > 1 ? t4.y : 0.f) + (wq > 2 ? t4.z : 0.f);
           e = ex2(e);
           const uint32_t ty = tm + lane_at + kColY + 32 * rg;
           uint32_t y[2][16];

@@ -164,7 +164,7 @@ __device__ __forceinline__ void advance(const float (&w)[W][V], const float (&b)
 // is repeated for every unrolled token and the loop no longer fits the
 // instruction cache (125 us instead of 31 at 16384 x 1792 bf16).
 template <typename T, int V, int W, int STEP>
-__global__ void __launch_bounds__(kConvCta, 4) ss_packed_conv1d_kernel(const __grid_constant__ PackedConvParams p, const int run) {
+__global__ void __launch_bounds__(kConvCta, V == 1 ? 4 : 3) ss_packed_conv1d_kernel(const __grid_constant__ PackedConvParams p, const int run) {
   constexpr int H = W - 1;
   // a warp is 32 channel pieces wide, so that few lanes pass the last channel
   const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * V;
@@ -304,14 +304,15 @@ __global__ void __launch_bounds__(kConvCta) ss_packed_conv1d_update_kernel(const
 
 template <typename T, int V, int W>
 void go(const PackedConvParams &p, cudaStream_t s) {
-  // Runs that fill the SMs once: 4 CTAs of the 16-byte form fit one SM (128
-  // registers a thread), 10 of the other. Longer ones leave SMs idle, shorter ones
+  // Runs that fill the SMs once: 3 CTAs of the 16-byte form fit one SM (168
+  // registers a thread, for 16 loads under way; with 8 and 4 CTAs 25.3 us against
+  // 24.4 at 16384 x 1792 bf16), 10 of the other. Longer ones leave SMs idle, shorter ones
   // a part of a second wave (31.5 us against 28.8 at 16384 x 1792 bf16, runs of 32
   // against 56).
-  constexpr int STEP = V == 1 ? 16 : 8, resident = V == 1 ? 10 : 4;
+  constexpr int STEP = V == 1 ? 8 : 16, resident = V == 1 ? 10 : 3;
   const int cols = (p.dim + 32 * V - 1) / (32 * V), warps = 152 * resident * (kConvCta / 32);
   const long long want = ((long long)p.t.tokens * cols + warps - 1) / warps;
-  const int run = (int)(want < 16 ? 16 : want > 128 ? 128 : (want + STEP - 1) / STEP * STEP);
+  const int run = (int)(want < STEP ? STEP : want > 128 ? 128 : (want + STEP - 1) / STEP * STEP);
   const int per = run * (kConvCta / 32);
   ss_packed_conv1d_kernel<T, V, W, STEP><<<dim3((p.t.tokens + per - 1) / per, cols), kConvCta, 0, s>>>(p, run);
 }
