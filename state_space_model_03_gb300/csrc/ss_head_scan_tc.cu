@@ -29,9 +29,10 @@
 // What bounds it: the instructions of the scaling warps. A chunk of two heads of 64
 // with 128 states is 56 products (2,500 cycles of the tensor pipe) and about 16,000
 // warp instructions, a third of them the split of w X into exact terms; it takes
-// about 4.4 us (5.3 with the gate). 8 requests x 2048 tokens x 24 heads: 93 us on 96
-// CTAs; 65536 tokens x 32 heads: 359 us, of which the summaries take 90. The first
-// form, one group of warps that did all steps in turn with its loops unrolled, took
+// about 4.2 us (5.1 with the gate). 8 requests x 2048 tokens x 24 heads: 91 us on 96
+// CTAs; 65536 tokens x 32 heads: 347 us, of which the summaries take 90. To let the
+// row warps weigh a quarter of the next chunk, which shortens the column warps' part,
+// changed nothing (91 and 355): it is the sum that counts. The first form, one group of warps that did all steps in turn with its loops unrolled, took
 // 204 and 802 us and spent half of that waiting for instructions.
 //
 // Rounding. C B^T takes the stored B and C; its masked form and the S that C
