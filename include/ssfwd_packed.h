@@ -86,7 +86,7 @@ typedef struct ss_packed_tables {
  * with slot -1, leaves the cache alone. out is 0 past the last token.
  *
  *   x, out       (tokens, dim) in dtype, dim stride 1.
- *   weight       (dim, width) fp32, contiguous; 2 <= width <= 4.
+ *   weight       (dim, width) fp32, contiguous; 2 <= width <= 4, dim <= 2^20.
  *   bias         (dim,) fp32, or NULL.
  *   conv_state   (slots, dim, width-1) in dtype, contiguous but for its slot
  *                stride; NULL: every request starts from 0 and nothing is kept.
@@ -145,7 +145,7 @@ int ss_packed_conv1d_update(const ss_packed_conv1d_update_params *p, void *strea
  *                when a request may have more than one block (tokens > block),
  *                and for 16-bit operands that do not lie in rows of 16 bytes.
  *
- * Sizes: 1 <= headdim, dstate <= 256, heads a multiple of ngroups.
+ * Sizes: 1 <= headdim, dstate <= 256, heads <= 8192 and a multiple of ngroups.
  *
  * 16-bit operands with headdim, dstate <= 128 run on the tensor cores, 128
  * tokens at a time; the state stays in fp32 (its sums take every bit of bf16

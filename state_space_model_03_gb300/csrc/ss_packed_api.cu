@@ -127,7 +127,7 @@ int validate_conv(const P *p, int64_t rows) {
   if (bad_dtype(p->dtype)) return SS_ERR_DTYPE;
   if (p->activation != SS_ACT_NONE && p->activation != SS_ACT_SILU) return SS_ERR_UNSUPPORTED;
   if (p->dim < 1 || p->slots < 0) return SS_ERR_SHAPE;
-  if (p->width < 2 || p->width > 4 || p->dim > (int64_t(1) << 22) || p->slots > (int64_t(1) << 31)) return SS_ERR_UNSUPPORTED;
+  if (p->width < 2 || p->width > 4 || p->dim > (int64_t(1) << 20) || p->slots > (int64_t(1) << 31)) return SS_ERR_UNSUPPORTED;
   if (rows == 0) return SS_OK;
   if (!p->x || !p->weight || !p->out) return SS_ERR_NULL;
   if (bad_stride(p->x_stride) || bad_stride(p->out_stride) || (p->conv_state && bad_stride(p->state_stride))) return SS_ERR_STRIDE;
@@ -188,7 +188,7 @@ int validate_heads(const P *p, int64_t rows) {
   if (bad_dtype(p->dtype) || (p->dt_dtype != SS_F32 && p->dt_dtype != p->dtype)) return SS_ERR_DTYPE;
   if (p->heads < 1 || p->headdim < 1 || p->dstate < 1 || p->ngroups < 1 || p->heads % p->ngroups != 0 || p->slots < 0)
     return SS_ERR_SHAPE;
-  if (p->headdim > 256 || p->dstate > 256 || p->heads > 16383 || p->slots > (int64_t(1) << 31)) return SS_ERR_UNSUPPORTED;
+  if (p->headdim > 256 || p->dstate > 256 || p->heads > 8192 || p->slots > (int64_t(1) << 31)) return SS_ERR_UNSUPPORTED;
   if (rows == 0) return SS_OK;
   if (!p->x || !p->dt || !p->A || !p->B || !p->C || !p->out) return SS_ERR_NULL;
   for (int i = 0; i < 2; ++i)

@@ -44,6 +44,7 @@ SCAN = [
     ("headdim0", "p.headdim = 0;", 2),
     ("headdim257", "p.headdim = 257;", 7),
     ("dstate257", "p.dstate = 257;", 7),
+    ("heads8193", "p.heads = 8193;", 7),
     ("null_x", "p.x = 0;", 1),
     ("null_out", "p.out = 0;", 1),
     ("null_table", "p.tables.blocks = 0;", 1),
@@ -69,6 +70,7 @@ CONV = [
     ("good", "", 0),
     ("width1", "p.width = 1;", 7),
     ("width5", "p.width = 5;", 7),
+    ("dim_large", "p.dim = (1 << 20) + 8;", 7),
     ("act", "p.activation = 7;", 7),
     ("dim", "p.dim = 0;", 2),
     ("null_w", "p.weight = 0;", 1),
