@@ -27,8 +27,8 @@
 // as the product's A operand (128); Y (128); S (128); w X as A operand (128).
 //
 // What bounds it: the instructions of the scaling warps. A chunk of two heads of 64
-// with 128 states is 56 products (2,500 cycles of the tensor pipe) and about 16,000
-// warp instructions, a third of them the split of w X into exact terms; it takes
+// with 128 states is 56 products (2,500 cycles of the tensor pipe) and about 20,000
+// warp instructions, a quarter of them the split of w X into exact terms; it takes
 // about 4.2 us (5.1 with the gate). 8 requests x 2048 tokens x 24 heads: 91 us on 96
 // CTAs; 65536 tokens x 32 heads: 347 us, of which the summaries take 90. To let the
 // row warps weigh a quarter of the next chunk, which shortens the column warps' part,

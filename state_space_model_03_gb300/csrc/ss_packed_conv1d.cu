@@ -10,7 +10,7 @@
 // rows before each run. The thread that has a request's first token also takes
 // its first W-1 ones past the end of its run, so that it alone reads the kept
 // window and can replace it at once: the exchange needs no second pass.
-// 16384 x 1792 bf16, width 4: 26.7 us, 4.4 TB/s (65% of the copy bandwidth); the
+// 16384 x 1792 bf16, width 4: 25.8 us, 4.6 TB/s (67% of the copy bandwidth); the
 // step at 512 x 5376: 14.3 us, 3.1 TB/s.
 #include "ss_fwd_kernel.cuh"
 #include "ss_packed.h"
