@@ -29,11 +29,12 @@
 // What bounds it: the instructions of the scaling warps. A chunk of two heads of 64
 // with 128 states is 56 products (2,500 cycles of the tensor pipe) and about 20,000
 // warp instructions, a quarter of them the split of w X into exact terms; it takes
-// about 4.2 us (5.1 with the gate). 8 requests x 2048 tokens x 24 heads: 91 us on 96
-// CTAs; 65536 tokens x 32 heads: 347 us, of which the summaries take 90. To let the
+// about 4.1 us (5 with the gate). 8 requests x 2048 tokens x 24 heads: 90 us on 96
+// CTAs; 65536 tokens x 32 heads: 340 us, of which the summaries take 90. To let the
 // row warps weigh a quarter of the next chunk, which shortens the column warps' part,
-// changed nothing (91 and 355): it is the sum that counts. The first form, one group of warps that did all steps in turn with its loops unrolled, took
-// 204 and 802 us and spent half of that waiting for instructions.
+// changed nothing (91 and 355, against 91 and 347): it is the sum that counts. The
+// first form, one group of warps that did all steps in turn with its loops unrolled,
+// took 204 and 802 us and spent half of that waiting for instructions.
 //
 // Rounding. C B^T takes the stored B and C; its masked form and the S that C
 // multiplies are rounded to 16 bits, about what rounding the output costs. S
@@ -96,7 +97,7 @@ __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile 
   return false;
 }
 __device__ __forceinline__ bool wait_tc(uint64_t *bar, uint32_t parity, volatile int *dead, int32_t *err) {
-  return mbar_test(bar, parity) || wait_long(bar, parity, dead, err);
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, dead, err);
 }
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
