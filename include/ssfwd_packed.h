@@ -147,14 +147,19 @@ int ss_packed_conv1d_update(const ss_packed_conv1d_update_params *p, void *strea
  *
  * Sizes: 1 <= headdim, dstate <= 256, heads <= 8192 and a multiple of ngroups.
  *
+ * A may have either sign; negative A is what decays.
+ *
  * 16-bit operands with headdim, dstate <= 128 run on the tensor cores, 128
- * tokens at a time; the state stays in fp32 (its sums take every bit of bf16
- * operands, 22 bits of each fp16 term). Two things follow from that form: a NaN
- * or infinity in a token's x also reaches the outputs of the same request's
- * tokens before it in its 128 (never another request's), and with fp16 operands
- * the products C.B and the state are rounded to fp16 where they enter the
- * output, so they have to stay below 65504. Other operands run token by token
- * in fp32.
+ * tokens at a time; the state stays in fp32. Its sums take every bit of bf16
+ * operands. A term dt x B of fp16 operands is off by at most 2^-22 of itself, or
+ * by 2^-24 of the largest weight (dt times the decay to the end) of its 128
+ * tokens, or of its block where the request has several. Two things follow from
+ * that form: a NaN or infinity in a token's x also reaches the outputs of the
+ * same request's tokens before it in its 128 (never another request's), and with
+ * fp16 operands the state, and the product of C.B, the decay between two tokens
+ * and the earlier one's dt, are rounded to fp16 where they enter the output: they
+ * have to stay below 65504, and below 6e-5 they keep an absolute 3e-8. Other
+ * operands run token by token in fp32.
  */
 typedef struct ss_head_scan_params {
   int32_t abi_version, dtype, dt_dtype, dt_softplus;

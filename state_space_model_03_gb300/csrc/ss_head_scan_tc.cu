@@ -39,8 +39,9 @@
 // Rounding. C B^T takes the stored B and C; its masked form and the S that C
 // multiplies are rounded to 16 bits, about what rounding the output costs. S
 // itself stays in fp32 from chunk to chunk: w X enters in three bf16 terms (24
-// bits, exact) or two fp16 terms (22 bits, w scaled by a power of two per chunk
-// and head so that the smaller one does not underflow).
+// bits, exact) or two fp16 terms, with w scaled by a power of two per head and
+// chunk (summaries: block) that brings its largest to [1/2, 1). No x then leaves
+// fp16, and a term is off by at most 2^-22 of itself or 2^-24 of the largest w.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -402,31 +403,52 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     if (tp < HT) {
       const int hp = at.h0 + tp < at.hend ? at.h0 + tp : at.h0;
       const float A2 = p.A[hp] * kLog2e, bias = p.bias ? p.bias[hp] : 0.f;
-      auto load_dt = [&](int i) -> float {
-        const int t = (chunks - 1 - i) * 128 + trow;
-        if (i >= chunks || t >= at.size) return 0.f;
+      auto raw_at = [&](int t) -> float {  // token t of the block
+        if (t >= at.size) return 0.f;
         const long long k = (long long)(at.first + t) * p.sdt[0] + hp * p.sdt[1];
         return p.dt_f32 ? static_cast<const float *>(p.dt)[k] : to_f<T>(static_cast<const T *>(p.dt)[k]);
       };
+      auto load_dt = [&](int i) -> float { return i < chunks ? raw_at((chunks - 1 - i) * 128 + trow) : 0.f; };
       float later = 0.f, scale = 1.f, raw_dt = load_dt(0);  // later: log2 decay of the chunks after this one
       if (NT == 2) {
-        // One power of two for the whole block, that brings its largest dt to [8, 16):
-        // no w is larger (A <= 0), so that w X stays below 65504 for |x| < 4094, and
-        // terms of a thousandth of that still keep 18 bits.
-        float m = 0.f;
+        // One power of two for the whole block, that brings its largest w to [1/2, 1), as
+        // the scan does for a chunk: w X then stays within fp16 for every x. A thread
+        // walks a run of the block's tokens from its end; what follows a run is joined
+        // afterwards. The margin covers what the order of these sums makes of w.
+        float m = 0.f, run = 0.f;  // largest w of the run, with the decay to its end; log2 decay of the run
 #pragma unroll 8
-        for (int i = 0; i < chunks; ++i) {
-          const float raw = load_dt(i) + bias;
-          const bool in = (chunks - 1 - i) * 128 + trow < at.size;
-          m = fmaxf(m, !in ? 0.f : p.softplus ? softplus_f(raw) : fabsf(raw));
+        for (int i = chunks - 1; i >= 0; --i) {
+          const int t = trow * chunks + i;
+          float dt = raw_at(t) + bias;
+          if (p.softplus) dt = softplus_f(dt);
+          if (t >= at.size) dt = 0.f;
+          m = fmaxf(m, fabsf(dt) * ex2(run));
+          run = fmaf(dt, A2, run);
         }
+        float to_end = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float dn = __shfl_down_sync(0xffffffffu, to_end, o);
+          if (lane + o < 32) to_end += dn;
+        }
+        const float nx = __shfl_down_sync(0xffffffffu, to_end, 1);
+        m *= ex2(lane < 31 ? nx : 0.f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) sh.top[tp][wq] = m;
+        if (lane == 0) {
+          sh.top[tp][wq] = m;
+          sh.part[1][tp][wq] = to_end;  // read before the barrier of the first chunk, written after it
+        }
         asm volatile("bar.sync %0, 128;" ::"r"(2 + tp) : "memory");
-        m = fmaxf(fmaxf(sh.top[tp][0], sh.top[tp][1]), fmaxf(sh.top[tp][2], sh.top[tp][3]));
-        const int e = (int)(__float_as_uint(m) >> 23);
-        scale = e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(257 - e) << 23);
+        float after = 0.f;
+        m = 0.f;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          m = fmaxf(m, sh.top[tp][k] * ex2(after));
+          after += sh.part[1][tp][k];
+        }
+        const int e = (int)(__float_as_uint(m * 1.015625f) >> 23);
+        scale = e < 64 || e > 190 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
       }
 #pragma unroll 1
       for (int i = 0; i < chunks; ++i) {

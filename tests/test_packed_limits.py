@@ -1,0 +1,88 @@
+"""Packed operators on the GPU at the edges of what their types hold, against the
+fp64 oracle (oracle/packed.py). Tolerances of norms are those of test_packed.py.
+"""
+import pytest
+import torch
+
+import state_space_model_03_gb300 as ssm
+from oracle import packed as oracle
+from state_space_model_03_gb300 import api
+from test_packed import STATE_TOL, TOL, TYPES, _close, _i32, _run_scan, _scan_problem
+
+pytestmark = pytest.mark.gpu
+
+HALF = [torch.bfloat16, torch.float16]
+
+
+# ---- large inputs and steps in requests of several blocks ----
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("block", [128, 256, 384, 4096])
+@pytest.mark.parametrize("headdim,dstate", [(64, 64), (128, 128)])
+def test_large_inputs_do_not_depend_on_the_block(dtype, block, headdim, dstate):
+    """|x| from 4100 to 60000 at the tokens with the largest steps, which end blocks: states of a
+    few thousand and outputs of some hundred, far below 65504, whatever the block."""
+    n = 700
+    p, t, st = _scan_problem([n], 2, 1, headdim, dstate, dtype, z=False, dt32=True, seed=21, fused=False)
+    p |= {"dt_bias": None, "dt_softplus": False, "D": None}
+    p["dt"] = p["dt"].abs() * 0.005
+    at = torch.arange(127, n, 128, device="cuda")
+    p["dt"][at] = 0.0987
+    size = torch.linspace(4100, 60000, headdim, device="cuda") * (1 - 2 * (torch.arange(headdim, device="cuda") % 2))
+    p["x"][at] = size.to(dtype)
+    p["B"] *= 0.25
+    p["C"] *= 0.01
+    t["context"].fill_(1)
+    _run_scan(p, t, st, [n], block)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [128, 4096])
+def test_growing_states(dtype, block):
+    """A > 0: the weights of a block's first tokens are the largest."""
+    n = 260
+    p, t, st = _scan_problem([n], 2, 1, 64, 64, dtype, z=False, dt32=True, seed=22, fused=False)
+    p |= {"dt_bias": None, "dt_softplus": False, "D": None}
+    p["A"] = torch.tensor([1.5, 0.3], device="cuda")
+    p["dt"] = p["dt"].abs() * 0.02
+    p["x"] *= 100
+    p["C"] *= 0.02
+    t["context"].fill_(1)
+    _run_scan(p, t, st, [n], block)
+
+
+# ---- blocks of many chunks, and other forms in several blocks ----
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("block", [384, 512, 640, 1100])
+@pytest.mark.parametrize("headdim,dstate", [(64, 64), (64, 128), (128, 64), (128, 128)])
+def test_blocks_of_many_chunks(dtype, block, headdim, dstate):
+    """Summaries of 3 to 9 chunks, the last of them partial, in requests of several blocks."""
+    lengths = [3 * block + 37, 5, 2 * block, block + 1]
+    p, t, st = _scan_problem(lengths, 3, 1, headdim, dstate, dtype, z=block == 512, pad=2, seed=block, A_max=2.0)
+    p["dt_bias"] = p["dt_bias"] - 2  # states that last for hundreds of tokens
+    t["context"].fill_(1)
+    _run_scan(p, t, st, lengths, block)
+
+
+@pytest.mark.parametrize("dtype", HALF)
+def test_the_blocks_that_the_rule_gives(dtype):
+    """One long request of a few heads, cut as head_scan_block says."""
+    n = 9001
+    block = ssm.head_scan_block(n, 1, 4, 64, dtype=dtype)
+    assert 128 < block < n
+    p, t, st = _scan_problem([n], 4, 2, 64, 64, dtype, z=False, seed=26, A_max=2.0)
+    p["dt_bias"] = p["dt_bias"] - 2
+    t["context"].fill_(1)
+    _run_scan(p, t, st, [n], block)
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("block", [16, 50, 128])
+@pytest.mark.parametrize("headdim,dstate", [(200, 24), (33, 256)])
+def test_large_heads_and_states_in_several_blocks(dtype, block, headdim, dstate):
+    """The token-by-token form for 16-bit operands."""
+    lengths = [70, 0, 1, 129, 3 * block + 5]
+    p, t, st = _scan_problem(lengths, 2, 1, headdim, dstate, dtype, pad=3, seed=block)
+    t["context"].fill_(1)
+    _run_scan(p, t, st, lengths, block)
