@@ -247,6 +247,16 @@ template <> struct Terms<__half> {
   }
 };
 
+// log2 of a step's decay (the product with A first: A log2(e) may be infinite where
+// dt A is not). Below -128 nothing is left (ex2 gives 0); in sums of which differences
+// are taken, a larger number would only round away the steps beside it, or make the
+// difference one of infinities. Sums over 32 tokens so end at 4096, where a unit is
+// 5e-4. NaN stays NaN.
+__device__ __forceinline__ float log2_step(float dt, float A) {
+  const float l = dt * A * kLog2e;
+  return l < -128.f ? -128.f : l;
+}
+
 // Instruction descriptor of a product of two T operands into fp32, M = 128.
 template <typename T>
 constexpr uint32_t kIdesc = (1u << 4) | ((Terms<T>::N == 3 ? 1u : 0u) << 7) | ((Terms<T>::N == 3 ? 1u : 0u) << 10) | (8u << 24);
@@ -402,7 +412,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     const int tp = wg, trow = pc;
     if (tp < HT) {
       const int hp = at.h0 + tp < at.hend ? at.h0 + tp : at.h0;
-      const float A2 = p.A[hp] * kLog2e, bias = p.bias ? p.bias[hp] : 0.f;
+      const float A = p.A[hp], bias = p.bias ? p.bias[hp] : 0.f;
       auto raw_at = [&](int t) -> float {  // token t of the block
         if (t >= at.size) return 0.f;
         const long long k = (long long)(at.first + t) * p.sdt[0] + hp * p.sdt[1];
@@ -421,9 +431,9 @@ __global__ void __launch_bounds__(kSumThreads, 1)
           const int t = trow * chunks + i;
           float dt = raw_at(t) + bias;
           if (p.softplus) dt = softplus_f(dt);
-          if (t >= at.size) dt = 0.f;
+          if (t >= at.size) continue;
           m = fmaxf(m, fabsf(dt) * ex2(run));
-          run = fmaf(dt, A2, run);
+          run += log2_step(dt, A);
         }
         float to_end = run;
 #pragma unroll
@@ -454,9 +464,10 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       for (int i = 0; i < chunks; ++i) {
         float dt = raw_dt + bias;
         if (p.softplus) dt = softplus_f(dt);
-        if ((chunks - 1 - i) * 128 + trow >= at.size) dt = 0.f;
+        const bool in = (chunks - 1 - i) * 128 + trow < at.size;
+        if (!in) dt = 0.f;
         raw_dt = load_dt(i + 1);
-        float to_end = dt * A2;
+        float to_end = in ? log2_step(dt, A) : 0.f;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const float dn = __shfl_down_sync(0xffffffffu, to_end, o);
@@ -949,7 +960,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int hp = prepares && h0 + tp < hend ? h0 + tp : h0;
     const int ho = HT == 2 ? rg >> 1 : 0;                       // the head of the columns in the tile
     const bool hin = h0 + ho < hend;
-    const float A2 = p.A[hp] * kLog2e, bias = p.bias ? p.bias[hp] : 0.f, skip = p.D ? p.D[hin ? h0 + ho : h0] : 0.f;
+    const float A = p.A[hp], bias = p.bias ? p.bias[hp] : 0.f, skip = p.D ? p.D[hin ? h0 + ho : h0] : 0.f;
     const int trow = wq * 32 + lane;
     auto load_dt = [&](int c) -> float {
       const int t = c * 128 + trow;
@@ -1051,8 +1062,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int st = cp & 3;
         float dt = raw_dt + bias;
         if (p.softplus) dt = softplus_f(dt);
-        if (cp * 128 + trow >= size) dt = 0.f;
-        float l = dt * A2, to_end = l;
+        const bool in = cp * 128 + trow < size;
+        if (!in) dt = 0.f;
+        float l = in ? log2_step(dt, A) : 0.f, to_end = l;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const float up = __shfl_up_sync(0xffffffffu, l, o), dn = __shfl_down_sync(0xffffffffu, to_end, o);

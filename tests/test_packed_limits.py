@@ -51,6 +51,39 @@ def test_growing_states(dtype, block):
     _run_scan(p, t, st, [n], block)
 
 
+# ---- steps that leave nothing of what was before ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [128, 4096])
+@pytest.mark.parametrize("A", [-3e38, -float("inf")])
+def test_steps_that_end_everything(dtype, block, A):
+    """dt A past the largest number: a decay of 0, as token by token, not a difference of infinities."""
+    n = 300
+    p, t, st = _scan_problem([n], 2, 1, 64, 64, dtype, z=False, dt32=True, seed=23)
+    p |= {"dt_bias": None, "dt_softplus": False}
+    p["A"] = torch.tensor([A, -2.0], device="cuda")
+    p["dt"] = 1 + p["dt"].abs()
+    t["context"].fill_(1)
+    _run_scan(p, t, st, [n], block)
+
+
+@pytest.mark.parametrize("block", [128, 4096])
+@pytest.mark.parametrize("step", [1e3, 1e6])
+def test_ordinary_steps_after_huge_ones(block, step):
+    """One huge step in each 32 tokens (with nothing to add) leaves the decays of those after it exact
+    to bf16: the rounding of a prefix that holds it would be as large as the steps themselves."""
+    n = 300
+    p, t, st = _scan_problem([n], 2, 1, 64, 64, torch.bfloat16, z=False, dt32=True, seed=24, fused=False)
+    p |= {"dt_bias": None, "dt_softplus": False, "D": None}
+    p["dt"] = p["dt"].abs() * 0.05
+    at = torch.arange(3, n, 32, device="cuda")
+    p["dt"][at] = step
+    p["x"][at] = 0
+    p["B"][at] = 0
+    t["context"].fill_(1)
+    _run_scan(p, t, st, [n], block)
+
+
 # ---- blocks of many chunks, and other forms in several blocks ----
 
 @pytest.mark.parametrize("dtype", HALF)
