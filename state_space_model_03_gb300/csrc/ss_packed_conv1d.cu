@@ -15,8 +15,6 @@
 #include "ss_fwd_kernel.cuh"
 #include "ss_packed.h"
 
-#include <type_traits>
-
 namespace ssk {
 namespace {
 
@@ -141,7 +139,7 @@ __device__ __forceinline__ void load_taps(const float *weight, const float *bias
 }
 
 // One output of V channels from their window and the new input, which the window takes in.
-template <typename T, int V, int W>
+template <int V, int W>
 __device__ __forceinline__ void advance(const float (&w)[W][V], const float (&b)[V], float (&win)[W - 1][V], const float (&v)[V],
                                         int act, float (&y)[V]) {
   constexpr int H = W - 1;
@@ -151,8 +149,7 @@ __device__ __forceinline__ void advance(const float (&w)[W][V], const float (&b)
 #pragma unroll
     for (int k = 0; k < H; ++k) acc = fmaf(w[k][i], win[k][i], acc);
     acc = fmaf(w[H][i], v[i], acc);
-    // bf16 takes the form with one MUFU operation (2^-11), well inside its rounding
-    y[i] = !act ? acc : std::is_same<T, __nv_bfloat16>::value ? silu_fast(acc) : silu_f(acc);
+    y[i] = act ? silu_f(acc) : acc;
 #pragma unroll
     for (int k = 0; k + 1 < H; ++k) win[k][i] = win[k + 1][i];
     win[H - 1][i] = v[i];
@@ -243,7 +240,7 @@ __global__ void __launch_bounds__(kConvCta, V == 1 ? 4 : 3) ss_packed_conv1d_ker
       for (int s = 0; s < STEP; ++s) {
         float v[V], y[V];
         in[s].widen(v);
-        advance<T, V, W>(w, b, win, v, p.act, y);
+        advance<V, W>(w, b, win, v, p.act, y);
         store_v<T, V>(op + s * p.so, y);
       }
       xp += STEP * p.sx;
@@ -253,7 +250,7 @@ __global__ void __launch_bounds__(kConvCta, V == 1 ? 4 : 3) ss_packed_conv1d_ker
     for (; t < to; ++t) {
       float v[V], y[V];
       load_v<T, V>(xp, v);
-      advance<T, V, W>(w, b, win, v, p.act, y);
+      advance<V, W>(w, b, win, v, p.act, y);
       store_v<T, V>(op, y);
       xp += p.sx;
       op += p.so;
@@ -295,7 +292,7 @@ __global__ void __launch_bounds__(kConvCta) ss_packed_conv1d_update_kernel(const
     if (slot[i] >= 0 && slot[i] < p.slots) {
       float v[V];
       in[i].widen(v);
-      advance<T, V, W>(w, b, win[i], v, p.act, y);
+      advance<V, W>(w, b, win[i], v, p.act, y);
       store_window<T, V, H>(static_cast<T *>(p.state) + slot[i] * p.ss + (long long)c * H, win[i]);
     }
     store_v<T, V>(out, y);

@@ -1,6 +1,8 @@
 """Packed operators on the GPU at the edges of what their types hold, against the
-fp64 oracle (oracle/packed.py). Tolerances of norms are those of test_packed.py.
+fp64 oracle (oracle/packed.py). Tolerances of norms are those of test_packed.py;
+those of single elements are derived where they stand.
 """
+import numpy as np
 import pytest
 import torch
 
@@ -82,6 +84,48 @@ def test_ordinary_steps_after_huge_ones(block, step):
     p["B"][at] = 0
     t["context"].fill_(1)
     _run_scan(p, t, st, [n], block)
+
+
+# ---- silu, element by element ----
+
+# Half a unit of the last place is at most 2^-8, 2^-11 and 2^-24 of the value (in fp16 at least 2^-25).
+# silu in fp32 adds the rounding of its exponent (58 in log2 at z = -40, to 2^-24 of it and of log2 e),
+# of ex2 and of rcp (2^-22 each): below 5e-6.
+ELEMENT = {torch.bfloat16: 2.0 ** -8 + 5e-6, torch.float16: 2.0 ** -11 + 5e-6, torch.float32: 5e-6}
+
+
+def _gates(dtype):
+    z = torch.linspace(-12.0 if dtype == torch.float16 else -40.0, 10.0, 2048).to(dtype)
+    return z.cuda(), oracle.silu(z.double().numpy())
+
+
+def _elements(got, want, dtype):
+    off = np.abs(got.double().cpu().numpy() - want)
+    bound = ELEMENT[dtype] * np.abs(want) + (2.0 ** -25 if dtype == torch.float16 else 0)
+    worst = int(np.argmax(off - bound))
+    assert (off <= bound).all(), (worst, got.flatten()[worst].item(), want.flat[worst])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_silu_of_the_convolutions(dtype):
+    z, want = _gates(dtype)
+    x, w = z.view(64, 32), torch.tensor([0.0, 1.0], device="cuda").repeat(32, 1)
+    tables = ssm.request_tables(_i32([64]), 64)
+    _elements(ssm.packed_conv1d_fn(x, w, tables, activation="silu"), want.reshape(64, 32), dtype)
+    st = torch.zeros(64, 32, 1, dtype=dtype, device="cuda")
+    _elements(ssm.packed_conv1d_update(x, st, w, activation="silu"), want.reshape(64, 32), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_silu_of_the_gate(dtype):
+    """x = D = 1 and B = 0 leave silu(z); the prompt's and the step's agree to their rounding."""
+    z, want = _gates(dtype)
+    z, want = z.view(32, 1, 64), want.reshape(32, 1, 64)
+    x, bc = torch.ones_like(z), torch.zeros(32, 1, 64, dtype=dtype, device="cuda")
+    dt, A, D = torch.zeros(32, 1, dtype=dtype, device="cuda"), -torch.ones(1, device="cuda"), torch.ones(1, device="cuda")
+    _elements(ssm.head_scan_fn(x, dt, A, bc, bc, ssm.request_tables(_i32([32]), 32), D=D, z=z), want, dtype)
+    st = torch.zeros(32, 1, 64, 64, device="cuda")
+    _elements(ssm.head_state_update(st, x, dt, A, bc, bc, D=D, z=z), want, dtype)
 
 
 # ---- blocks of many chunks, and other forms in several blocks ----
