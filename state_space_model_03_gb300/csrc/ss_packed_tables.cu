@@ -7,10 +7,16 @@
 // table, each entry found by bisection. A second launch, or a hand-over from CTA to
 // CTA, would cost more than the sums. Bound by latency: 7.5 us for 66 requests and
 // 1100 tokens, 8.7 for 1000 and 200000 (cold; two sums and one bisection each).
+#include <atomic>
+
 #include "ss_packed.h"
+#include "ssfwd_packed.h"
 
 namespace ssk {
 namespace {
+
+// Shared memory of three tables over the requests.
+constexpr int table_bytes(int requests) { return 3 * (requests + 1) * (int)sizeof(int); }
 
 constexpr int kThreads = 512;
 constexpr int kTokensPerCta = kThreads * 4;
@@ -170,11 +176,19 @@ cudaError_t launch_request_tables(const TablesParams &p, cudaStream_t s) {
   // at most one CTA per SM, so that the sums are repeated no more often than that
   const long long want = ((long long)p.tokens + kTokensPerCta - 1) / kTokensPerCta;
   const int grid = (int)(want < 1 ? 1 : want > 152 ? 152 : want);
-  const int smem = 3 * (p.requests + 1) * (int)sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute((const void *)&ss_request_tables_kernel,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = table_bytes(p.requests);
+  // Opted in once per device (the attribute is per device), always to what the most
+  // requests need: a call's own size could be put in place of another thread's larger
+  // one, and the 48 KB that need no opt-in have to hold the kernel's static part too.
+  static std::atomic<bool> opted[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !opted[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute((const void *)&ss_request_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             table_bytes(SS_MAX_REQUESTS));
     if (e != cudaSuccess) return e;
+    if (dev < 64) opted[dev].store(true, std::memory_order_relaxed);
   }
   ss_request_tables_kernel<<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();

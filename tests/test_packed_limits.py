@@ -128,6 +128,32 @@ def test_silu_of_the_gate(dtype):
     _elements(ssm.head_state_update(st, x, dt, A, bc, bc, D=D, z=z), want, dtype)
 
 
+# ---- number of requests ----
+
+TABLES_IN_A_FRESH_PROCESS = """
+import torch
+import state_space_model_03_gb300 as ssm
+from oracle import packed as oracle
+for n in (4084, 4085, 4090, 4095, 4096, 16384):
+    lengths = torch.arange(n, dtype=torch.int32, device="cuda") % 3
+    t = ssm.request_tables(lengths, n, block=2)
+    want = oracle.request_tables(lengths, n, block=2)
+    for k, v in want.items():
+        assert (getattr(t, k).cpu().numpy() == v).all(), (n, k)
+print("tables ok")
+"""
+
+
+def test_tables_of_any_number_of_requests_in_a_fresh_process():
+    """Numbers whose tables just pass the shared memory that needs no request, before any larger call."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", TABLES_IN_A_FRESH_PROCESS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "tables ok" in r.stdout, r.stderr[-2000:]
+
+
 # ---- blocks of many chunks, and other forms in several blocks ----
 
 @pytest.mark.parametrize("dtype", HALF)
