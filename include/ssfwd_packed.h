@@ -145,7 +145,9 @@ int ss_packed_conv1d_update(const ss_packed_conv1d_update_params *p, void *strea
  *                when a request may have more than one block (tokens > block),
  *                and for 16-bit operands that do not lie in rows of 16 bytes.
  *
- * Sizes: 1 <= headdim, dstate <= 256, heads <= 8192 and a multiple of ngroups.
+ * Sizes: 1 <= headdim, dstate <= 256, heads <= 8192 and a multiple of ngroups;
+ * tokens / block x heads x ceil(headdim x dstate / 1024) and, on the tensor cores,
+ * (max_blocks + 1) x tiles (of two heads of a group, or one above 64) < 2^31.
  *
  * A may have either sign; negative A is what decays.
  *

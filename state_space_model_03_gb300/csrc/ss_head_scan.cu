@@ -243,43 +243,41 @@ __global__ void __launch_bounds__(256) ss_head_scan_carry_kernel(const __grid_co
 }
 
 template <typename T, int NPL, int RPL>
-void go(const HeadScanParams &p, cudaStream_t s) {
+cudaError_t go(const HeadScanParams &p, cudaStream_t s) {
   constexpr int rows = kScanThreads / kLanes * RPL;
   const dim3 grid(p.t.max_blocks + 1, p.heads * ((p.headdim + rows - 1) / rows));
   if (p.split) {
     ss_head_scan_kernel<T, NPL, RPL, true><<<dim3(p.t.tokens / p.t.block, grid.y), kScanThreads, 0, s>>>(p);
-    launch_head_scan_carry(p, s);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_head_scan_carry(p, s);
+    if (e != cudaSuccess) return e;  // the scan would start from what no one has written
   }
-  launch_after(ss_head_scan_kernel<T, NPL, RPL, false>, grid, kScanThreads, 0, s, p.split, p);
+  return launch_after(ss_head_scan_kernel<T, NPL, RPL, false>, grid, kScanThreads, 0, s, p.split, p);
 }
 template <typename T, int RPL>
-void by_states(const HeadScanParams &p, cudaStream_t s) {
-  if (p.dstate > 128) go<T, 16, RPL>(p, s);
-  else if (p.dstate > 64) go<T, 8, RPL>(p, s);
-  else if (p.dstate > 32) go<T, 4, RPL>(p, s);
-  else if (p.dstate > 16) go<T, 2, RPL>(p, s);
-  else go<T, 1, RPL>(p, s);
+cudaError_t by_states(const HeadScanParams &p, cudaStream_t s) {
+  if (p.dstate > 128) return go<T, 16, RPL>(p, s);
+  if (p.dstate > 64) return go<T, 8, RPL>(p, s);
+  if (p.dstate > 32) return go<T, 4, RPL>(p, s);
+  if (p.dstate > 16) return go<T, 2, RPL>(p, s);
+  return go<T, 1, RPL>(p, s);
 }
 // 64 rows of a head's state per CTA, or 32 where that leaves fewer rows empty
 template <typename T>
-void by_rows(const HeadScanParams &p, cudaStream_t s) {
-  if ((p.headdim + 31) / 32 % 2) by_states<T, 2>(p, s); else by_states<T, 4>(p, s);
+cudaError_t by_rows(const HeadScanParams &p, cudaStream_t s) {
+  return (p.headdim + 31) / 32 % 2 ? by_states<T, 2>(p, s) : by_states<T, 4>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_head_scan_carry(const HeadScanParams &p, cudaStream_t s) {
-  const int pieces = (p.headdim * p.dstate + 1023) / 1024;
-  const long long ctas = (long long)(p.t.tokens / p.t.block) * p.heads * pieces;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_after(ss_head_scan_carry_kernel, dim3((unsigned)ctas), 256, 0, s, true, p, pieces);
+  return launch_after(ss_head_scan_carry_kernel, dim3((unsigned)head_scan_carry_ctas(p)), 256, 0, s, true, p,
+                      head_scan_carry_pieces(p));
 }
 
 cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s) {
-  if (dtype == 0) by_rows<float>(p, s);
-  else if (dtype == 1) by_rows<__half>(p, s);
-  else by_rows<__nv_bfloat16>(p, s);
-  return cudaGetLastError();
+  if (dtype == 0) return by_rows<float>(p, s);
+  return dtype == 1 ? by_rows<__half>(p, s) : by_rows<__nv_bfloat16>(p, s);
 }
 
 }  // namespace ssk

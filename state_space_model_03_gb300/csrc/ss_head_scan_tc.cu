@@ -45,6 +45,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "ss_fwd_kernel.cuh"
 #include "ss_packed.h"
 
@@ -1155,26 +1157,24 @@ template <typename T, int PW, int NS, bool GATE>
 cudaError_t go(const HeadScanParams &p, const TcMaps &maps, cudaStream_t s) {
   constexpr int smem = kBoxes * kBox + NS / 64 * kBox + (int)sizeof(Shared) + 1024;
   constexpr int sum_smem = kSumStages * (2 + NS / 64) * kBox + (int)sizeof(SumShared) + 1024;
-  const int ht = 128 / PW;
-  const long long tiles = (long long)(p.heads / p.hpg) * ((p.hpg + ht - 1) / ht);
-  const long long ctas = tiles * (p.t.max_blocks + 1);
-  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const long long tiles = head_scan_tc_tiles(p), ctas = tiles * (p.t.max_blocks + 1);
   auto sum = ss_head_scan_sum_tc_kernel<T, PW, NS>;
   auto fwd = ss_head_scan_tc_kernel<T, PW, NS, GATE>;
-  static bool set[64] = {};  // the attribute is per device
+  static std::atomic<bool> set[64];  // the attribute is per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !set[dev]) {
+  if (dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
     e = cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, sum_smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    if (dev < 64) set[dev] = true;
+    if (dev < 64) set[dev].store(true, std::memory_order_relaxed);
   }
   if (p.split) {
     sum<<<(unsigned)(tiles * (p.t.tokens / p.t.block)), kSumThreads, sum_smem, s>>>(p, maps);
-    e = launch_head_scan_carry(p, s);
-    if (e != cudaSuccess) return e;
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_head_scan_carry(p, s);
+    if (e != cudaSuccess) return e;  // the scan would start from what no one has written
   }
   return launch_after(fwd, dim3((unsigned)ctas), kTcThreads, smem, s, p.split, p, maps);
 }
@@ -1242,8 +1242,7 @@ __global__ void __launch_bounds__(256) rows_kernel(uint16_t *strided, long long 
 }
 template <bool TO>
 cudaError_t copy_rows(void *strided, const long long *st, void *rows, int tokens, int n, int width, cudaStream_t s) {
-  const long long total = (long long)tokens * n * ((width + 7) / 8), ctas = (total + 255) / 256;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const long long total = (long long)tokens * n * ((width + 7) / 8), ctas = copy_rows_ctas(tokens, n, width);
   rows_kernel<TO><<<(unsigned)ctas, 256, 0, s>>>(static_cast<uint16_t *>(strided), st[0], st[1], static_cast<uint4 *>(rows), n, width, total);
   return cudaGetLastError();
 }

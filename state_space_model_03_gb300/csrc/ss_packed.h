@@ -78,6 +78,10 @@ struct HeadScanParams {
 };
 cudaError_t launch_head_scan(int dtype, const HeadScanParams &p, cudaStream_t s);
 cudaError_t launch_head_scan_carry(const HeadScanParams &p, cudaStream_t s);  // the second launch
+inline int head_scan_carry_pieces(const HeadScanParams &p) { return (p.headdim * p.dstate + 1023) / 1024; }  // CTAs of a head's state
+inline long long head_scan_carry_ctas(const HeadScanParams &p) {
+  return (long long)(p.t.tokens / p.t.block) * p.heads * head_scan_carry_pieces(p);
+}
 
 // The same on the tensor cores, for 16-bit operands that TMA can describe.
 typedef void *TensorMapEncode;  // the driver's cuTensorMapEncodeTiled
@@ -88,6 +92,15 @@ TensorMapEncode packed_map_encode();
 bool head_scan_tc_sizes(int dtype, const HeadScanParams &p);
 enum { kRowsX = 1, kRowsB = 2, kRowsC = 4, kRowsZ = 8, kRowsOut = 16 };
 int head_scan_tc_unaligned(const HeadScanParams &p);
+// Tiles of 128 (head, p) columns, two heads of up to 64 or one: a CTA for each and
+// for each row of the block table, and one more.
+inline long long head_scan_tc_tiles(const HeadScanParams &p) {
+  const int ht = p.headdim <= 64 ? 2 : 1;
+  return (long long)(p.heads / p.hpg) * ((p.hpg + ht - 1) / ht);
+}
+inline long long copy_rows_ctas(int tokens, int rows, int width) {
+  return ((long long)tokens * rows * ((width + 7) / 8) + 255) / 256;
+}
 // (tokens, rows, width) in 16-bit values between a strided tensor and contiguous
 // rows of `width` rounded up to 8: to_rows zeroes what is past the width.
 cudaError_t launch_to_rows(const void *src, const long long *st, void *dst, int tokens, int rows, int width, cudaStream_t s);

@@ -279,11 +279,27 @@ Workspace workspace_of(const ss_head_scan_params *p) {
   return w;
 }
 
+// Whether every launch of the scan is one that a grid holds (its second dimension
+// does at all sizes that validate_heads lets through).
+bool grids_fit(const ss_head_scan_params *p) {
+  constexpr int64_t most = 0x7fffffff;
+  const ssk::HeadScanParams k = scan_params(p);
+  if (k.split && ssk::head_scan_carry_ctas(k) > most) return false;
+  if (!ssk::head_scan_tc_sizes(p->dtype, k)) return true;
+  if (ssk::head_scan_tc_tiles(k) * (p->tables.max_blocks + 1) > most) return false;
+  const int u = ssk::head_scan_tc_unaligned(k);
+  const bool wide = u & (ssk::kRowsX | ssk::kRowsZ | ssk::kRowsOut), narrow = u & (ssk::kRowsB | ssk::kRowsC);
+  return !(wide && ssk::copy_rows_ctas(k.t.tokens, k.heads, k.headdim) > most) &&
+         !(narrow && ssk::copy_rows_ctas(k.t.tokens, (int)p->ngroups, k.dstate) > most);
+}
+
 int validate_operands(const ss_head_scan_params *p) {
   if (!p) return SS_ERR_NULL;
   if (p->abi_version != SS_ABI_VERSION) return SS_ERR_VERSION;
-  const int st = validate(p->tables);
-  return st != SS_OK ? st : validate_heads(p, p->tables.tokens);
+  int st = validate(p->tables);
+  if (st == SS_OK) st = validate_heads(p, p->tables.tokens);
+  if (st != SS_OK || p->tables.tokens == 0) return st;
+  return grids_fit(p) ? SS_OK : SS_ERR_UNSUPPORTED;
 }
 
 int validate(const ss_head_scan_params *p) {
