@@ -99,6 +99,11 @@ int64_t integer(PyObject *o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
+bool flag(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v == 1;
+}
 void *stream_of(const at::Tensor &x) { return c10::cuda::getCurrentCUDAStream(x.get_device()).stream(); }
 
 // The tables as the operators take them, in a bytes object.
@@ -368,7 +373,7 @@ PyObject *head_scan(PyObject *, PyObject *const *a, Py_ssize_t given) {
     const at::Tensor &x = need(a[0], "x");
     ss_head_scan_params p{};
     const Heads h = head_operands(p, x, need(a[1], "dt"), need(a[2], "A"), need(a[3], "B"), need(a[4], "C"), opt(a[6], "D"),
-                                  opt(a[7], "z"), opt(a[8], "dt_bias"), PyObject_IsTrue(a[9]) == 1, opt(a[10], "state"));
+                                  opt(a[7], "z"), opt(a[8], "dt_bias"), flag(a[9]), opt(a[10], "state"));
     p.tables = plan_of(a[5], x).t;
     const c10::cuda::CUDAGuard guard(x.device());
     at::Tensor out = at::empty(x.sizes(), x.options()), ws;
@@ -389,7 +394,7 @@ PyObject *head_state_update(PyObject *, PyObject *const *a, Py_ssize_t given) {
     const at::Tensor &x = need(a[1], "x");
     ss_head_state_update_params p{};
     const Heads h = head_operands(p, x, need(a[2], "dt"), need(a[3], "A"), need(a[4], "B"), need(a[5], "C"), opt(a[6], "D"),
-                                  opt(a[7], "z"), opt(a[8], "dt_bias"), PyObject_IsTrue(a[9]) == 1, &need(a[0], "state"));
+                                  opt(a[7], "z"), opt(a[8], "dt_bias"), flag(a[9]), &need(a[0], "state"));
     p.requests = x.size(0);
     const Held slots = int32(opt(a[10], "slots"), "slots", x.size(0), x);
     p.slot_map = iptr(slots.get());

@@ -4,8 +4,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
-from state_space_model_03_gb300 import api
+from state_space_model_03_gb300 import api, packed
 from state_space_model_03_gb300 import build as ssbuild
 from test_packed_abi import ROOT, _program
 
@@ -62,3 +63,17 @@ def test_grids_are_checked_before_anything_is_enqueued(lib, tmp_path):
     got = dict(line.split(" ", 1) for line in r.stdout.strip().splitlines())
     for name, _, status in GRIDS:
         assert got[name] == f"{status} {status}", (name, got[name])
+
+
+class _Undecided:
+    def __bool__(self):
+        raise ValueError("neither")
+
+
+def test_flags_that_are_neither_true_nor_false(lib):
+    b = packed._bind()
+    h = torch.zeros(2, 2, 8)
+    with pytest.raises(ValueError, match="neither"):
+        b.head_state_update(torch.zeros(2, 2, 8, 8), h, h[:, :, 0], torch.zeros(2), h, h, None, None, None, _Undecided(), None)
+    with pytest.raises(ValueError, match="neither"):
+        b.head_scan(h, h[:, :, 0], torch.zeros(2), h, h, b"", None, None, None, _Undecided(), None)
