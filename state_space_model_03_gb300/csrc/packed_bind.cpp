@@ -83,9 +83,10 @@ void on(const at::Tensor *t, const at::Tensor &x, const char *name) {
   if (t && t->device() != x.device()) refuse(PyExc_ValueError, std::string(name) + " must be on " + x.device().str());
 }
 void no_grad(std::initializer_list<const at::Tensor *> ts) {
-  if (!c10::GradMode::is_enabled()) return;
+  const bool backward = c10::GradMode::is_enabled();
   for (const at::Tensor *t : ts)
-    if (t && t->requires_grad()) refuse(PyExc_NotImplementedError, "the packed operators are forward only");
+    if (t && ((backward && t->requires_grad()) || t->_fw_grad(0).defined()))
+      refuse(PyExc_NotImplementedError, "the packed operators are forward only: no gradients and no tangents");
 }
 Held int32(const at::Tensor *t, const char *name, int64_t n, const at::Tensor &x) {
   if (!t) return Held{};

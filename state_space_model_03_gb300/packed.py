@@ -7,7 +7,9 @@ of states. ``request_tables`` builds the batch's tables on the GPU;
 and ``head_state_update`` one token per request.
 
 As in api.py this is argument marshalling only, on the current stream, and there
-is no CPU fallback. The checks and the call are in csrc/packed_bind.cpp.
+is no CPU fallback. The checks and the call are in csrc/packed_bind.cpp. The
+operators are forward only: inputs that require a gradient or carry a tangent are
+refused.
 """
 from __future__ import annotations
 

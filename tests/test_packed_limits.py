@@ -8,8 +8,7 @@ import torch
 
 import state_space_model_03_gb300 as ssm
 from oracle import packed as oracle
-from state_space_model_03_gb300 import api
-from test_packed import STATE_TOL, TOL, TYPES, _close, _i32, _run_scan, _scan_problem
+from test_packed import TYPES, _i32, _run_scan, _scan_problem
 
 pytestmark = pytest.mark.gpu
 

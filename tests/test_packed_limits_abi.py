@@ -5,6 +5,7 @@ import subprocess
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fwad
 
 from state_space_model_03_gb300 import api, packed
 from state_space_model_03_gb300 import build as ssbuild
@@ -77,3 +78,14 @@ def test_flags_that_are_neither_true_nor_false(lib):
         b.head_state_update(torch.zeros(2, 2, 8, 8), h, h[:, :, 0], torch.zeros(2), h, h, None, None, None, _Undecided(), None)
     with pytest.raises(ValueError, match="neither"):
         b.head_scan(h, h[:, :, 0], torch.zeros(2), h, h, b"", None, None, None, _Undecided(), None)
+
+
+def test_forward_mode_tangents_are_refused(lib):
+    b = packed._bind()
+    h, x, w = torch.zeros(2, 2, 8), torch.zeros(2, 4), torch.zeros(4, 3)
+    with fwad.dual_level():
+        with pytest.raises(NotImplementedError):
+            b.head_state_update(torch.zeros(2, 2, 8, 8), fwad.make_dual(h, torch.ones_like(h)), h[:, :, 0], torch.zeros(2), h, h,
+                                None, None, None, False, None)
+        with pytest.raises(NotImplementedError):
+            b.packed_conv1d_update(fwad.make_dual(x, torch.ones_like(x)), torch.zeros(2, 4, 2), w, None, None, 0)
