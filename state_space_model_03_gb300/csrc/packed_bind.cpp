@@ -88,6 +88,10 @@ void no_grad(std::initializer_list<const at::Tensor *> ts) {
     if (t && ((backward && t->requires_grad()) || t->_fw_grad(0).defined()))
       refuse(PyExc_NotImplementedError, "the packed operators are forward only: no gradients and no tangents");
 }
+// A cache was updated in place: what autograd has saved of it is known to be old.
+void changed(const at::Tensor *t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
 Held int32(const at::Tensor *t, const char *name, int64_t n, const at::Tensor &x) {
   if (!t) return Held{};
   if (t->scalar_type() != at::kInt || t->dim() != 1 || t->size(0) != n)
@@ -268,12 +272,14 @@ PyObject *packed_conv1d(PyObject *, PyObject *const *a, Py_ssize_t given) {
   return guarded(given, 6, [&]() -> PyObject * {
     const at::Tensor &x = need(a[0], "x");
     ss_packed_conv1d_params p{};
-    const Conv c = conv_operands(p, x, need(a[1], "weight"), opt(a[3], "bias"), opt(a[4], "conv_state"), integer(a[5]));
+    const at::Tensor *state = opt(a[4], "conv_state");
+    const Conv c = conv_operands(p, x, need(a[1], "weight"), opt(a[3], "bias"), state, integer(a[5]));
     p.tables = plan_of(a[2], x).t;
     const c10::cuda::CUDAGuard guard(x.device());
     at::Tensor out = at::empty(x.sizes(), x.options());
     p.out = out.data_ptr();
     check(g_conv(&p, stream_of(x)));
+    changed(state);
     return THPVariable_Wrap(std::move(out));
   });
 }
@@ -281,9 +287,9 @@ PyObject *packed_conv1d(PyObject *, PyObject *const *a, Py_ssize_t given) {
 // packed_conv1d_update(x, conv_state, weight, bias, slots, activation) -> out
 PyObject *packed_conv1d_update(PyObject *, PyObject *const *a, Py_ssize_t given) {
   return guarded(given, 6, [&]() -> PyObject * {
-    const at::Tensor &x = need(a[0], "x");
+    const at::Tensor &x = need(a[0], "x"), &state = need(a[1], "conv_state");
     ss_packed_conv1d_update_params p{};
-    const Conv c = conv_operands(p, x, need(a[2], "weight"), opt(a[3], "bias"), &need(a[1], "conv_state"), integer(a[5]));
+    const Conv c = conv_operands(p, x, need(a[2], "weight"), opt(a[3], "bias"), &state, integer(a[5]));
     p.requests = x.size(0);
     const Held slots = int32(opt(a[4], "slots"), "slots", x.size(0), x);
     p.slot_map = iptr(slots.get());
@@ -291,6 +297,7 @@ PyObject *packed_conv1d_update(PyObject *, PyObject *const *a, Py_ssize_t given)
     at::Tensor out = at::empty(x.sizes(), x.options());
     p.out = out.data_ptr();
     check(g_conv_update(&p, stream_of(x)));
+    changed(&state);
     return THPVariable_Wrap(std::move(out));
   });
 }
@@ -371,10 +378,10 @@ Heads head_operands(P &p, const at::Tensor &x, const at::Tensor &dt, const at::T
 // head_scan(x, dt, A, B, C, plan, D, z, dt_bias, dt_softplus, state) -> out
 PyObject *head_scan(PyObject *, PyObject *const *a, Py_ssize_t given) {
   return guarded(given, 11, [&]() -> PyObject * {
-    const at::Tensor &x = need(a[0], "x");
+    const at::Tensor &x = need(a[0], "x"), *state = opt(a[10], "state");
     ss_head_scan_params p{};
     const Heads h = head_operands(p, x, need(a[1], "dt"), need(a[2], "A"), need(a[3], "B"), need(a[4], "C"), opt(a[6], "D"),
-                                  opt(a[7], "z"), opt(a[8], "dt_bias"), flag(a[9]), opt(a[10], "state"));
+                                  opt(a[7], "z"), opt(a[8], "dt_bias"), flag(a[9]), state);
     p.tables = plan_of(a[5], x).t;
     const c10::cuda::CUDAGuard guard(x.device());
     at::Tensor out = at::empty(x.sizes(), x.options()), ws;
@@ -385,6 +392,7 @@ PyObject *head_scan(PyObject *, PyObject *const *a, Py_ssize_t given) {
       p.workspace = ws.data_ptr();
     }
     check(g_scan(&p, stream_of(x)));
+    changed(state);
     return THPVariable_Wrap(std::move(out));
   });
 }
@@ -392,10 +400,10 @@ PyObject *head_scan(PyObject *, PyObject *const *a, Py_ssize_t given) {
 // head_state_update(state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, slots) -> out
 PyObject *head_state_update(PyObject *, PyObject *const *a, Py_ssize_t given) {
   return guarded(given, 11, [&]() -> PyObject * {
-    const at::Tensor &x = need(a[1], "x");
+    const at::Tensor &x = need(a[1], "x"), &state = need(a[0], "state");
     ss_head_state_update_params p{};
     const Heads h = head_operands(p, x, need(a[2], "dt"), need(a[3], "A"), need(a[4], "B"), need(a[5], "C"), opt(a[6], "D"),
-                                  opt(a[7], "z"), opt(a[8], "dt_bias"), flag(a[9]), &need(a[0], "state"));
+                                  opt(a[7], "z"), opt(a[8], "dt_bias"), flag(a[9]), &state);
     p.requests = x.size(0);
     const Held slots = int32(opt(a[10], "slots"), "slots", x.size(0), x);
     p.slot_map = iptr(slots.get());
@@ -403,6 +411,7 @@ PyObject *head_state_update(PyObject *, PyObject *const *a, Py_ssize_t given) {
     at::Tensor out = at::empty(x.sizes(), x.options());
     p.out = out.data_ptr();
     check(g_update(&p, stream_of(x)));
+    changed(&state);
     return THPVariable_Wrap(std::move(out));
   });
 }

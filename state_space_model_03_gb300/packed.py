@@ -9,7 +9,7 @@ and ``head_state_update`` one token per request.
 As in api.py this is argument marshalling only, on the current stream, and there
 is no CPU fallback. The checks and the call are in csrc/packed_bind.cpp. The
 operators are forward only: inputs that require a gradient or carry a tangent are
-refused.
+refused, and a cache that is updated in place counts as changed for autograd.
 """
 from __future__ import annotations
 

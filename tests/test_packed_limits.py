@@ -153,6 +153,32 @@ def test_tables_of_any_number_of_requests_in_a_fresh_process():
     assert r.returncode == 0 and "tables ok" in r.stdout, r.stderr[-2000:]
 
 
+# ---- caches under autograd ----
+
+def test_caches_count_their_versions():
+    """A cache that autograd saved is known to have changed; one made in inference mode still works."""
+    p, t, st = _scan_problem([1] * 3, 2, 1, 16, 16, torch.float32, seed=25)
+    tables = ssm.request_tables(_i32([1, 1, 1]), 3, context=_i32([1, 1, 1]))
+    x, w = torch.randn(3, 8, device="cuda"), torch.randn(8, 4, device="cuda")
+    win = torch.zeros(3, 8, 3, device="cuda")
+    calls = [(st, lambda s: ssm.head_scan_fn(**p, tables=tables, state=s)),
+             (st, lambda s: ssm.head_state_update(s, **p)),
+             (win, lambda s: ssm.packed_conv1d_fn(x, w, tables, conv_state=s)),
+             (win, lambda s: ssm.packed_conv1d_update(x, s, w))]
+    for cache, call in calls:
+        before = cache._version
+        call(cache)
+        assert cache._version > before
+        factor = torch.ones((), device="cuda", requires_grad=True)
+        y = (cache * factor).sum()
+        call(cache)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        with torch.inference_mode():
+            frozen = cache.clone()
+        call(frozen)
+
+
 # ---- blocks of many chunks, and other forms in several blocks ----
 
 @pytest.mark.parametrize("dtype", HALF)
