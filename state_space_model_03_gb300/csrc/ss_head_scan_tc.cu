@@ -388,6 +388,10 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       for (int i = max(0, n - kSumStages); i < n; ++i)
         for (uint32_t k = 0; k < kMaxWaitIters; ++k)
           if (mbar_try_wait(&sh.full[i % kSumStages], (i / kSumStages) & 1)) break;
+      // The tensor cores arrive on these after what the other warps wait for: the CTA
+      // stays until they have, or they would write to shared memory that is another's.
+      for (int i = max(0, chunks - kSumStages); i < chunks && !*dead; ++i)
+        wait_tc(&sh.empty[i % kSumStages], (i / kSumStages) & 1, dead, p.err);
     }
   } else if (warp == 25) {
     // ---- products ----
@@ -704,6 +708,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int i = max(0, nb - 2); i < nb; ++i) landed(&sh.full_b[i & 1], (i >> 1) & 1);
       for (int i = max(0, nz - 2); i < nz; ++i) landed(&sh.full_z[i & 1], (i >> 1) & 1);
       if (nc > 0) landed(&sh.full_c, (nc - 1) & 1);
+      // The tensor cores' last arrivals, after what the other warps wait for (with the
+      // gate, load_z has waited for them): they have to find this CTA still there.
+      if (!GATE)
+        for (int c = max(0, chunks - 2); c < chunks && !*dead; ++c) wait_tc(&sh.empty_b[c & 1], (c >> 1) & 1, dead, p.err);
     }
   } else if (warp == 25) {
     // ---- products for Y ----
