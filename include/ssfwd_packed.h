@@ -83,7 +83,8 @@ typedef struct ss_packed_tables {
  * where the tokens before the first of t's request are its slot's window
  * (conv_state[slot, c, :], oldest first) when context > 0, else 0. Afterwards
  * the window holds the request's last W-1 inputs. A request without tokens, or
- * with slot -1, leaves the cache alone. out is 0 past the last token.
+ * with slot -1, leaves the cache alone. Two requests must not share a slot. out
+ * is 0 past the last token.
  *
  *   x, out       (tokens, dim) in dtype, dim stride 1.
  *   weight       (dim, width) fp32, contiguous; 2 <= width <= 4, dim <= 2^20.
@@ -131,7 +132,7 @@ int ss_packed_conv1d_update(const ss_packed_conv1d_update_params *p, void *strea
  *
  * S starts as state[slot, h] when context > 0, else 0, and ends in
  * state[slot, h]. A request without tokens, or with slot -1, leaves the cache
- * alone. out is 0 past the last token.
+ * alone. Two requests must not share a slot. out is 0 past the last token.
  *
  *   x, z, out    (tokens, heads, headdim) in dtype, last stride 1; stride
  *                {token, head}. z may be NULL.
@@ -155,13 +156,15 @@ int ss_packed_conv1d_update(const ss_packed_conv1d_update_params *p, void *strea
  * tokens at a time; the state stays in fp32. Its sums take every bit of bf16
  * operands. A term dt x B of fp16 operands is off by at most 2^-22 of itself, or
  * by 2^-24 of the largest weight (dt times the decay to the end) of its 128
- * tokens, or of its block where the request has several. Two things follow from
+ * tokens, or of its block where the request has several; where that weight is
+ * below 1e-19 it counts as 0. Two things follow from
  * that form: a NaN or infinity in a token's x also reaches the outputs of the
- * same request's tokens before it in its 128 (never another request's), and with
- * fp16 operands the state, and the product of C.B, the decay between two tokens
- * and the earlier one's dt, are rounded to fp16 where they enter the output: they
- * have to stay below 65504, and below 6e-5 they keep an absolute 3e-8. Other
- * operands run token by token in fp32.
+ * same request's tokens before it in its 128 (never another request's), and the
+ * state, and the product of C.B, the decay between two tokens and the earlier
+ * one's dt, are rounded to the operands' type where they enter the output, which
+ * adds about as much as the output's own rounding (the state that is kept has
+ * none of it). In fp16 these have to stay below 65504, and below 6e-5 they keep
+ * an absolute 3e-8. Other operands run token by token in fp32.
  */
 typedef struct ss_head_scan_params {
   int32_t abi_version, dtype, dt_dtype, dt_softplus;

@@ -27,9 +27,9 @@
 // as the product's A operand (128); Y (128); S (128); w X as A operand (128).
 //
 // What bounds it: the instructions of the scaling warps. A chunk of two heads of 64
-// with 128 states is 56 products (2,500 cycles of the tensor pipe) and about 20,000
+// with 128 states is 56 products (2,500 cycles of the tensor pipe) and about 19,000
 // warp instructions, a quarter of them the split of w X into exact terms; it takes
-// about 4.1 us (5 with the gate). 8 requests x 2048 tokens x 24 heads: 90 us on 96
+// about 4.1 us (5.2 with the gate). 8 requests x 2048 tokens x 24 heads: 92 us on 96
 // CTAs; 65536 tokens x 32 heads: 340 us, of which the summaries take 90. To let the
 // row warps weigh a quarter of the next chunk, which shortens the column warps' part,
 // changed nothing (91 and 355, against 91 and 347): it is the sum that counts. The

@@ -428,7 +428,12 @@ int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int6
   // Requests of the average length, cut into `cut` blocks each: the waves of CTAs,
   // each of so many steps (of 128 tokens on the tensor cores, else of 16), the
   // summaries of all blocks but the last (a third of a step's work) and two more
-  // launches.
+  // launches. The weights are estimates; against other blocks (captured graphs, us):
+  //   65536 tokens x 32 heads bf16    3456: 339    2688 397, 4736 424, 8192 362
+  //   2 x 8192 tokens x 24 heads bf16 1408: 99     1024 136, 2048 126, 8192 299
+  //   8 x 2048 tokens x 24 heads bf16 2048: 92     1024 126, 512 133
+  //   8 ragged, 4096 x 24 heads fp32   176: 276    128 304, 256 360, 64 312
+  //   5 ragged, 777 x 6 heads fp32      16: 22     32 24, 64 35, 1024 95
   const bool tc = dtype != SS_F32 && headdim <= 128;
   const int64_t tiles = tc ? (headdim <= 64 ? (heads + 1) / 2 : heads) : heads * ((headdim + 63) / 64);
   const int64_t resident = tc ? sms : 4 * sms, step = tc ? 128 : 16;
@@ -445,7 +450,8 @@ int64_t ss_head_scan_block(int64_t tokens, int64_t requests, int64_t heads, int6
     }
   }
   int64_t block = (steps + best - 1) / best * step;
-  // A batch whose requests need no cut may still hold one long request.
+  // A batch whose requests need no cut may still hold one long request (40 ragged
+  // requests, 6001 tokens x 16 heads fp16, rule 1024: 46 us; 512 57, 256 58).
   if (best == 1) block = std::max(block, (tc ? 8 : 4) * step);
   return std::min<int64_t>(std::max<int64_t>(block, step), 1 << 19);
 }

@@ -10,7 +10,7 @@
 // rows before each run. The thread that has a request's first token also takes
 // its first W-1 ones past the end of its run, so that it alone reads the kept
 // window and can replace it at once: the exchange needs no second pass.
-// 16384 x 1792 bf16, width 4: 25.8 us, 4.6 TB/s (67% of the copy bandwidth); the
+// 16384 x 1792 bf16, width 4: 26.9 us, 4.4 TB/s (65% of the copy bandwidth); the
 // step at 512 x 5376: 14.3 us, 3.1 TB/s.
 #include "ss_fwd_kernel.cuh"
 #include "ss_packed.h"
@@ -303,9 +303,9 @@ template <typename T, int V, int W>
 void go(const PackedConvParams &p, cudaStream_t s) {
   // Runs that fill the SMs once: 3 CTAs of the 16-byte form fit one SM (168
   // registers a thread, for 16 loads under way; with 8 and 4 CTAs 25.3 us against
-  // 24.4 at 16384 x 1792 bf16), 10 of the other. Longer ones leave SMs idle, shorter ones
-  // a part of a second wave (31.5 us against 28.8 at 16384 x 1792 bf16, runs of 32
-  // against 56).
+  // 24.4 at 16384 x 1792 bf16), 9 or 10 of the other (56 to 48 registers). Longer ones
+  // leave SMs idle, shorter ones a part of a second wave (31.5 us against 28.8 at
+  // 16384 x 1792 bf16, runs of 32 against 56).
   constexpr int STEP = V == 1 ? 8 : 16, resident = V == 1 ? 10 : 3;
   const int cols = (p.dim + 32 * V - 1) / (32 * V), warps = 152 * resident * (kConvCta / 32);
   const long long want = ((long long)p.t.tokens * cols + warps - 1) / warps;

@@ -6,7 +6,8 @@
 // shared memory, then writes its own share of the token maps and of the block
 // table, each entry found by bisection. A second launch, or a hand-over from CTA to
 // CTA, would cost more than the sums. Bound by latency: 7.5 us for 66 requests and
-// 1100 tokens, 8.7 for 1000 and 200000 (cold; two sums and one bisection each).
+// 1100 tokens, 8.9 for 1000 and 200000 (cold; two sums and one bisection each); 5.0
+// and 6.0 in a captured graph.
 #include <atomic>
 
 #include "ss_packed.h"

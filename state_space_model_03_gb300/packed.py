@@ -77,12 +77,13 @@ class RequestTables:
 def request_tables(lengths, num_tokens, context=None, slots=None, free_slots=None, block=512):
     """Tables of a packed batch from its request lengths, built on the GPU.
 
-    lengths: (requests,) int32 new tokens per request, 0 allowed. num_tokens:
-    rows of the packed tensors; rows past the last request's are padding.
-    context: (requests,) int32 tokens that each request has had before; where it
-    is above 0 the operators go on from the request's slot (None: all start from
-    zero). slots: (requests,) int32 slot of each request, -1 for one that has
-    none yet and takes the next of free_slots (None: request r has slot r).
+    lengths: (requests,) int32 new tokens per request, 0 allowed, at least one
+    request. num_tokens: rows of the packed tensors; rows past the last
+    request's are padding. context: (requests,) int32 tokens that each request
+    has had before; where it is above 0 the operators go on from the request's
+    slot (None: all start from zero). slots: (requests,) int32 slot of each
+    request, -1 for one that has none yet and takes the next of free_slots
+    (None: request r has slot r); no two requests with tokens may share one.
     block: tokens per unit of work of ``head_scan_fn`` (see
     ``head_scan_block``). Lengths that do not fit are cut and reported in
     counts[3] (``RequestTables.check``). The context is kept, not copied.
