@@ -5,7 +5,9 @@
 kernels of ``libssfwd.so`` through its C ABI (``include/ssfwd.h``). Packed
 requests (``include/ssfwd_packed.h``) have ``request_tables``,
 ``packed_conv1d_fn``, ``packed_conv1d_update``, ``head_scan_fn`` and
-``head_state_update``. There is no CPU fallback: the calls raise if the CUDA
+``head_state_update``. A gated recurrent layer (``include/ssfwd_layer.h``) has
+``gated_scan_fn``, ``packed_gated_scan_fn``, ``gated_state_update``,
+``rms_norm_fn`` and ``rms_norm_quant_fn``. There is no CPU fallback: the calls raise if the CUDA
 library is missing or no GPU is present.
 """
 
@@ -13,7 +15,8 @@ __all__ = ["selective_scan_fn", "selective_scan_fn_host", "selective_scan_bwd", 
            "selective_state_update", "causal_conv1d_fn", "causal_conv1d_update"]
 _PACKED = ["request_tables", "RequestTables", "packed_conv1d_fn", "packed_conv1d_update", "head_scan_fn",
            "head_scan_block", "head_state_update"]
-__all__ += _PACKED
+_LAYER = ["gated_scan_fn", "packed_gated_scan_fn", "gated_state_update", "rms_norm_fn", "rms_norm_quant_fn"]
+__all__ += _PACKED + _LAYER
 
 
 def __getattr__(name):
@@ -22,6 +25,9 @@ def __getattr__(name):
     if name in _PACKED:
         from . import packed
         return getattr(packed, name)
+    if name in _LAYER:
+        from . import layer
+        return getattr(layer, name)
     if name in __all__:
         from . import api
         return getattr(api, name)

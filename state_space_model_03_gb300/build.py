@@ -2,7 +2,7 @@
 for sm_103a only. Translation units compile in parallel; the library links the
 CUDA runtime statically and reaches the driver's tensor-map encoder through the
 runtime's driver entry-point query, so it needs no libcuda at link time. The
-packed operators' Python binding (_packed_bind.so) is built beside it with g++.
+Python bindings of the packed and the layer operators are built beside it with g++.
 """
 from __future__ import annotations
 
@@ -19,10 +19,13 @@ OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libssfwd.so")
 SOURCES = ["ssfwd_api.cu", "ss_fwd_f32.cu", "ss_fwd_f16.cu", "ss_fwd_bf16.cu", "ss_fwd_lane.cu", "ss_state_update.cu", "ss_conv1d.cu", "ss_bwd.cu", "ss_fwd_complex.cu",
            "ss_packed_api.cu", "ss_packed_tables.cu", "ss_packed_conv1d.cu", "ss_head_update.cu", "ss_head_scan.cu",
-           "ss_head_scan_tc.cu"]
-HEADERS = ["ss_dispatch.h", "ss_fwd_kernel.cuh", "ss_fwd_instances.cuh", "ss_packed.h"]
+           "ss_head_scan_tc.cu", "ss_layer_api.cu", "ss_gated_scan.cu", "ss_gated_bwd.cu", "ss_gated_update.cu",
+           "ss_rms_norm.cu", "ss_rms_norm_quant.cu", "ss_rms_norm_bwd.cu"]
+HEADERS = ["ss_dispatch.h", "ss_fwd_kernel.cuh", "ss_fwd_instances.cuh", "ss_packed.h", "ss_checks.h", "ss_layer.h",
+           "ss_gated.cuh", "ss_norm.cuh", "ss_rms_norm.cuh", "bind_common.h"]
 NVCC = os.environ.get("NVCC", "nvcc")
-BIND_SOURCE = "packed_bind.cpp"  # Python binding of the packed operators
+# Python bindings of the packed and of the layer operators, and what they are built into
+BINDS = {"packed_bind.cpp": "_packed_bind.so", "layer_bind.cpp": "_layer_bind.so"}
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-lineinfo",
          "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
@@ -31,7 +34,7 @@ def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
     deps = [src] + [os.path.join(os.path.dirname(src), h) for h in HEADERS] + [
-        os.path.join(ROOT, "include", h) for h in ("ssfwd.h", "ssfwd_packed.h")]
+        os.path.join(ROOT, "include", h) for h in ("ssfwd.h", "ssfwd_packed.h", "ssfwd_layer.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 
@@ -70,8 +73,8 @@ def build(force: bool = False, verbose: bool = False, out_dir: str = OUT, extra_
         if verbose:
             print(r.stderr, file=sys.stderr)
 
-    def compile_bind():
-        src, out = os.path.join(csrc, BIND_SOURCE), os.path.join(out_dir, "_packed_bind.so")
+    def compile_bind(source):
+        src, out = os.path.join(csrc, source), os.path.join(out_dir, BINDS[source])
         if not (force or _stale(out, src)):
             return
         tmp = out + f".tmp{os.getpid()}"
@@ -80,10 +83,11 @@ def build(force: bool = False, verbose: bool = False, out_dir: str = OUT, extra_
             raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, out)
 
-    with ThreadPoolExecutor(len(jobs) + 1) as ex:
-        bind = ex.submit(compile_bind)
+    with ThreadPoolExecutor(len(jobs) + len(BINDS)) as ex:
+        binds = [ex.submit(compile_bind, source) for source in BINDS]
         list(ex.map(compile_one, jobs))
-        bind.result()
+        for bind in binds:
+            bind.result()
     objs = [os.path.join(out_dir, s.replace(".cu", ".o")) for s in SOURCES]
     if force or jobs or not os.path.exists(lib):
         tmp = lib + f".tmp{os.getpid()}"

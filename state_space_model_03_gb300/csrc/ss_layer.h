@@ -1,0 +1,91 @@
+// Kernel parameters and launchers of the layer operators (include/ssfwd_layer.h).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ssk {
+
+// The recurrence runs in tiles of kGatedTile tokens by kGatedCh channels; the states
+// that the backward pass starts from are kept at each tile's first token.
+constexpr int kGatedTile = 64;
+constexpr int kGatedCh = 64;
+constexpr int kGatedMostCluster = 8;
+
+struct GatedScanParams {
+  int tokens, dim;      // per sequence
+  int batch, channel_tiles, tiles;  // sequences; tiles of channels; tiles of tokens per sequence
+  int cluster;          // CTAs that take consecutive tiles of a sequence's channels together
+  float rate;
+  const void *x, *gate, *igate;
+  const float *decay, *init;  // init (batch, dim) or NULL
+  void *out;
+  float *last;  // (batch, dim) or NULL
+  float *kept;  // (batch, tiles, dim) or NULL: the state before each tile
+  long long sx[2], sg[2], si[2], so[2];  // sequence, token
+  // packed requests (token_request given): one sequence, states by slot
+  const int32_t *token_request, *slot_map, *context;
+  float *state;
+  long long slots, state_stride;
+};
+cudaError_t launch_gated_scan(int dtype, bool pair, const GatedScanParams &p, cudaStream_t s);
+
+struct GatedBwdParams {
+  int tokens, dim, batch, channel_tiles, tiles, cluster;
+  float rate;
+  const void *x, *gate, *igate, *dout;
+  const float *decay, *kept, *dlast;  // dlast (batch, dim) or NULL
+  void *dx, *dgate, *digate;          // NULL: not wanted
+  float *ddecay, *dinit;
+  float *parts;  // (batch * cluster, dim): sums for ddecay
+  long long sx[2], sg[2], si[2], sd[2], sdx[2], sdg[2], sdi[2];
+};
+cudaError_t launch_gated_bwd(int dtype, bool pair, const GatedBwdParams &p, cudaStream_t s);
+
+// CTAs of a cluster along the sequence, for so many (sequence, channel tile) pairs.
+int gated_cluster(long long units, int tiles, int sms);
+
+struct GatedUpdateParams {
+  int rows, dim, vec;  // vec: 16-byte accesses of state rows, and 4 values at once of the others
+  float rate;
+  long long slots;
+  const void *x, *gate, *igate;
+  const float *decay;
+  const int32_t *slot_map;
+  float *state;
+  void *out;
+  long long sx, sg, si, so, ss;
+};
+cudaError_t launch_gated_update(int dtype, const GatedUpdateParams &p, cudaStream_t s);
+
+struct NormParams {
+  long long rows;
+  int dim;
+  int weight_f32;
+  float eps;
+  const void *x, *residual, *weight;  // residual NULL: the sum is x
+  void *out, *sum;                    // sum NULL: not wanted
+  float *rstd;                        // NULL: not wanted
+  long long sx, sr, so, ss;
+  // quantised
+  int group, e8m0;  // group 0: the row
+  void *scale;      // (rows, groups)
+  int groups;
+};
+cudaError_t launch_rms_norm(int dtype, int residual_dtype, bool vec, const NormParams &p, int sms, cudaStream_t s);
+cudaError_t launch_rms_norm_quant(int dtype, int residual_dtype, bool vec, const NormParams &p, int sms, cudaStream_t s);
+
+struct NormBwdParams {
+  long long rows;
+  int dim;
+  int weight_f32;
+  const void *dout, *dsum, *sum, *weight;  // dsum NULL: 0
+  const float *rstd;
+  void *dx, *dresidual, *dweight;  // NULL: not wanted
+  float *parts;                    // (ctas, dim): sums for dweight
+  int ctas;
+  long long sd, sds, ss, sdx, sdr;
+};
+int norm_bwd_ctas(long long rows, int dim);
+cudaError_t launch_rms_norm_bwd(int dtype, int residual_dtype, bool vec, const NormBwdParams &p, cudaStream_t s);
+
+}  // namespace ssk

@@ -23,22 +23,29 @@ import torch
 from . import api
 from .api import _DT, _activation
 
-_BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "_packed_bind.so")
 _bind_module = None
+
+
+def _load_extension(name, entry_points):
+    """The extension `name` of the build folder, given the library's entry points."""
+    lib = api.load_library()
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", name + ".so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{name}.so is not built ({path}); build it with "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`")
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+    loader.exec_module(module)
+    module.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in entry_points), api.SSError)
+    return module
 
 
 def _load_bind():
     global _bind_module
-    lib = api.load_library()
-    if not os.path.exists(_BIND_PATH):
-        raise RuntimeError(f"_packed_bind.so is not built ({_BIND_PATH}); build it with "
-                           "`python -c 'import __graft_entry__ as g; g.build()'`")
-    loader = importlib.machinery.ExtensionFileLoader("_packed_bind", _BIND_PATH)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_packed_bind", loader))
-    loader.exec_module(module)
     names = ("ss_request_tables", "ss_packed_conv1d", "ss_packed_conv1d_update", "ss_head_scan",
              "ss_head_scan_workspace_size", "ss_head_state_update", "ss_status_string")
-    module.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names), api.SSError)
+    module = _load_extension("_packed_bind", names)
+    lib = api.load_library()
     lib.ss_head_scan_block.argtypes = [ctypes.c_int64] * 4 + [ctypes.c_int32] * 2
     lib.ss_head_scan_block.restype = ctypes.c_int64
     _bind_module = module
