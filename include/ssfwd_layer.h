@@ -44,7 +44,7 @@ extern "C" {
  *                NULL: the state before every SS_GATED_TILE-th token, from which
  *                the backward takes up the recurrence.
  *
- * batch * ceil(dim / 64) < 2^28, seqlen and dim < 2^31 - 2^20. out overlaps no input.
+ * batch * ceil(dim / 32) < 2^28, seqlen and dim < 2^31 - 2^20. out overlaps no input.
  */
 #define SS_GATED_TILE 64
 

@@ -12,6 +12,11 @@
 //
 // Two channels at a time, in packed fp32 pairs.
 #pragma once
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "ss_fwd_kernel.cuh"
 #include "ss_layer.h"
 
@@ -67,22 +72,22 @@ __device__ __forceinline__ f2 root2(f2 n, f2 &inverse) {
   return mul2(m, inverse);
 }
 
-// One token, and one token's map (n, b) after a run's (N, E).
+// One token; as well one token's map (n, b) after a run's (N, E), part by part.
 __device__ __forceinline__ f2 step2(f2 n, f2 h, f2 b) { return add2(h, fma2(n, h, b)); }
 
 // A lane's two channels as they are stored: neighbours in one access (PAIR), or one
-// 32 channels after the other where rows do not start on such accesses.
+// 16 channels after the other where rows do not start on such accesses.
 template <typename T, bool PAIR>
 struct Two {
   T a, b;
   __device__ __forceinline__ void load(const T *src, bool ok0, bool ok1) {
     a = ok0 ? src[0] : from_f<T>(0.f);
-    b = ok1 ? src[32] : from_f<T>(0.f);
+    b = ok1 ? src[16] : from_f<T>(0.f);
   }
   __device__ __forceinline__ f2 widen() const { return pk(to_f<T>(a), to_f<T>(b)); }
   static __device__ __forceinline__ void store(T *dst, float2 v, bool ok0, bool ok1) {
     if (ok0) dst[0] = from_f<T>(v.x);
-    if (ok1) dst[32] = from_f<T>(v.y);
+    if (ok1) dst[16] = from_f<T>(v.y);
   }
 };
 template <typename T>
@@ -106,6 +111,15 @@ struct Two<float, true> {
   }
 };
 
+// How rows come and go: single values, pairs, or tiles by TMA (pairs in shared memory).
+// A tile is kGatedTile tokens by kGatedCh channels: runs of kRun tokens, two to a warp,
+// whose halves have 16 lanes of two channels each.
+constexpr int kRun = 8;
+constexpr int kRuns = kGatedTile / kRun;
+constexpr int kGatedWarps = kRuns / 2;
+constexpr int kGatedThreads = kGatedWarps * 32;
+enum RowAccess { kSingles, kPairs, kTma };
+
 // The exchange within a cluster.
 __device__ __forceinline__ uint32_t remote_of(const void *p, int rank) {
   uint32_t r;
@@ -118,8 +132,41 @@ __device__ __forceinline__ void store_remote(void *p, int rank, ulonglong2 v) {
 __device__ __forceinline__ void store_remote(void *p, int rank, f2 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote_of(p, rank)), "l"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
+}
+
+// Tiles by TMA: loads of a CTA's tile (thread 0), stores of a warp's rows.
+__device__ __forceinline__ void store_rows(const CUtensorMap *tm, const void *src, int c, int t, int b) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(c), "r"(t), "r"(b), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void commit_stores() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// (dim, tokens, batch) in boxes of 32 channels by `rows` tokens. A dimension of one
+// element may have any stride.
+inline bool rows_map(TensorMapEncode enc, CUtensorMap *m, int esize, const void *base, int dim, int tokens, int batch, const long long *st, int rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)tokens, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {tokens > 1 ? (cuuint64_t)st[1] * esize : 16, batch > 1 ? (cuuint64_t)st[0] * esize : 16};
+  const cuuint32_t box[3] = {kGatedCh, (cuuint32_t)rows, 1}, es[3] = {1, 1, 1};
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(enc)(
+             m, esize == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs of a cluster along the sequence: as many as the SMs hold of `resident` CTAs
+// each, so that all run at once, if that is two or more and there are tiles for them.
+inline int gated_cluster(long long units, int tiles, int sms, int resident) {
+  const long long k = (long long)sms * resident / units;
+  return (int)std::max<long long>(1, std::min<long long>(std::min(k, (long long)kGatedMostCluster), tiles));
 }
 
 }  // namespace ssk

@@ -6,33 +6,61 @@
 // one that the forward kept before each tile of 64 tokens (1/32 of an operand in 16
 // bits), so that both recurrences are local to a tile but for e.
 //
-// Tiles, warps and clusters are the forward's, the tiles in falling order. A warp's
-// map has three parts: the product of its a (both directions'), the forward's end
-// and the backward's. The sum over tokens for the decay's gradient stays in
-// registers, then goes by CTA to the workspace and is added up by a second launch:
-// no atomics, the same result in every call.
+// Tiles, runs and clusters are the forward's, the tiles in falling order. A run's map
+// has three parts: N (both directions'), the forward's end and the backward's. Of a
+// token, n, the state before it and 1 / sqrt(1 - a^2) stay in registers; its gates are
+// taken again from the tile in shared memory for the gradients, which costs less than
+// registers that would halve the CTAs of an SM. The sum over tokens for the decay's
+// gradient stays in registers, then goes by CTA to the workspace and is added up by a
+// second launch: no atomics, the same result in every call.
 #include "ss_gated.cuh"
 
 namespace ssk {
 namespace {
 
-constexpr int kSteps = 4;  // tokens of a warp: all that a token needs stays in registers
-constexpr int kWarps = kGatedTile / kSteps;
-constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 2;
+constexpr int kResident = 4;  // CTAs that an SM holds at least
 
-template <typename T, bool PAIR, bool IG>
-__global__ void __launch_bounds__(kThreads, 1) ss_gated_bwd_kernel(const __grid_constant__ GatedBwdParams p) {
-  __shared__ f2 prod[2][kWarps][32], fwd[2][kWarps][32], rev[2][kWarps][32];
-  __shared__ ulonglong2 tiles[2][kGatedMostCluster][32];  // (N, R) of whole tiles
-  __shared__ f2 carry[2][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int K = p.cluster, rank = blockIdx.x % K, unit = blockIdx.x / K;
+struct BwdMaps {
+  CUtensorMap x, gate, igate, dout, dx, dgate, digate;
+};
+template <typename T>
+struct BwdSmem {
+  T rows[kStages][4][kGatedTile][kGatedCh];
+  T out[kGatedWarps][3][2 * kRun][kGatedCh];
+  uint64_t full[kStages];
+};
+
+template <typename T, int ROWS, bool IG, bool CL>
+__global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) == 4 ? 2 : 5)
+    ss_gated_bwd_kernel(const __grid_constant__ GatedBwdParams p, const __grid_constant__ BwdMaps tm) {
+  constexpr int S = kRun;
+  constexpr bool TMA = ROWS == kTma, PAIR = ROWS != kSingles;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  BwdSmem<T> &sm = *reinterpret_cast<BwdSmem<T> *>(dyn);
+  __shared__ ulonglong2 maps[2][kRuns][16];  // (N, E) of the lane's channels, by run
+  __shared__ f2 backs[2][kRuns][16];         // R
+  __shared__ ulonglong2 tiles[CL ? 2 : 1][kGatedMostCluster][16];  // (N, R) of whole tiles
+  __shared__ f2 carry[2][16];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), l = lane & 15, half = lane >> 4;
+  const int K = CL ? p.cluster : 1, rank = CL ? blockIdx.x % K : 0, unit = CL ? blockIdx.x / K : blockIdx.x;
   const int ct = unit % p.channel_tiles, b = unit / p.channel_tiles;
-  const int c0 = ct * kGatedCh + (PAIR ? 2 * lane : lane), c1 = c0 + (PAIR ? 1 : 32);
+  const int run = 2 * warp + half;
+  const int c0 = ct * kGatedCh + (PAIR ? 2 * l : l), c1 = c0 + (PAIR ? 1 : 16);
   const bool ok0 = c0 < p.dim, ok1 = c1 < p.dim;
   const float2 most = make_float2(ok0 ? -p.rate * softplus_f(p.decay[c0]) : 0.f, ok1 ? -p.rate * softplus_f(p.decay[c1]) : 0.f);
   const bool near = __all_sync(~0u, most.x >= -0.5f && most.y >= -0.5f);
   const f2 open = pk(most);  // L of an open gate
+  auto pair_at = [&](const float *q) { return pk(ok0 ? q[c0] : 0.f, ok1 ? q[c1] : 0.f); };
+  auto put_pair = [&](float *q, f2 v) {
+    const float2 w = upk(v);
+    if (ok0) q[c0] = w.x;
+    if (ok1) q[c1] = w.y;
+  };
+  const int rounds = (p.tiles + K - 1) / K;
+
+  constexpr int H = TMA ? 1 : S;
+  Two<T, PAIR> rx[H], rg[H], ri[H], rd[H];
   const T *const x = static_cast<const T *>(p.x) + b * p.sx[0] + c0;
   const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + c0;
   const T *const igate = IG ? static_cast<const T *>(p.igate) + b * p.si[0] + c0 : nullptr;
@@ -40,125 +68,205 @@ __global__ void __launch_bounds__(kThreads, 1) ss_gated_bwd_kernel(const __grid_
   T *const dx = p.dx ? static_cast<T *>(p.dx) + b * p.sdx[0] + c0 : nullptr;
   T *const dgate = p.dgate ? static_cast<T *>(p.dgate) + b * p.sdg[0] + c0 : nullptr;
   T *const digate = IG && p.digate ? static_cast<T *>(p.digate) + b * p.sdi[0] + c0 : nullptr;
-  auto pair_at = [&](const float *q) { return pk(ok0 ? q[c0] : 0.f, ok1 ? q[c1] : 0.f); };
-
-  Two<T, PAIR> rx[kSteps], rg[kSteps], ri[IG ? kSteps : 1], rd[kSteps];
-  f2 next = 0;  // the state before the tile that comes next
-  auto load = [&](int tile) {
-    const int t0 = tile * kGatedTile + warp * kSteps;
+  bool fine = true;
+  // turns count up while the tiles go down: turn k has tile (rounds - 1 - k) K + rank
+  auto tile_of = [&](int turn) { return (rounds - 1 - turn) * K + rank; };
+  auto load = [&](int turn) {
+    const int first = tile_of(turn) * kGatedTile;
+    if constexpr (TMA) {
+      if (threadIdx.x == 0) {
+        const int s = turn % kStages;
+        mbar_arrive_expect_tx(&sm.full[s], (IG ? 4 : 3) * sizeof(sm.rows[0][0]));
+        tma_load_3d(sm.rows[s][0], &tm.x, &sm.full[s], ct * kGatedCh, first, b);
+        tma_load_3d(sm.rows[s][1], &tm.gate, &sm.full[s], ct * kGatedCh, first, b);
+        if constexpr (IG) tma_load_3d(sm.rows[s][2], &tm.igate, &sm.full[s], ct * kGatedCh, first, b);
+        tma_load_3d(sm.rows[s][3], &tm.dout, &sm.full[s], ct * kGatedCh, first, b);
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const bool in = t0 + j < p.tokens;
-      const long long t = t0 + j;
-      rx[j].load(x + t * p.sx[1], ok0 && in, ok1 && in);
-      rg[j].load(gate + t * p.sg[1], ok0 && in, ok1 && in);
-      if constexpr (IG) ri[j].load(igate + t * p.si[1], ok0 && in, ok1 && in);
-      rd[j].load(dout + t * p.sd[1], ok0 && in, ok1 && in);
+      for (int j = 0; j < S; ++j) {
+        const int t = first + run * S + j;
+        const bool in = t < p.tokens;
+        rx[j].load(x + t * p.sx[1], ok0 && in, ok1 && in);
+        rg[j].load(gate + t * p.sg[1], ok0 && in, ok1 && in);
+        if constexpr (IG) ri[j].load(igate + t * p.si[1], ok0 && in, ok1 && in);
+        rd[j].load(dout + t * p.sd[1], ok0 && in, ok1 && in);
+      }
     }
-    next = tile < p.tiles ? pair_at(p.kept + ((long long)b * p.tiles + tile) * p.dim) : 0;
   };
-  const int rounds = (p.tiles + K - 1) / K;
-  load((rounds - 1) * K + rank);
-  f2 e = 0, sum = 0;
-  if (p.dlast) e = pair_at(p.dlast + (long long)b * p.dim);
-  if (K > 1) cluster_sync();
+  auto kept_of = [&](int turn) {
+    const int tile = tile_of(turn);
+    return tile < p.tiles ? pair_at(p.kept + ((long long)b * p.tiles + tile) * p.dim) : 0;
+  };
+  if constexpr (TMA) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1);
+      fence_barrier_init();
+      for (int s = 0; s < kStages && s < rounds; ++s) load(s);
+    }
+  }
+  f2 next = kept_of(0);  // the state before the tile that comes next
+  f2 e, sum = 0;
+  // what comes back from past the last token, as if from a turn before the first
+  if (threadIdx.x < 16) carry[1][l] = p.dlast ? pair_at(p.dlast + (long long)b * p.dim) : 0;
+  if constexpr (CL) cluster_sync();
+  else __syncthreads();
   const f2 one = both(1.f), minus = both(-1.f);
-  for (int it = rounds - 1; it >= 0; --it) {
-    const int buf = it & 1, tile = it * K + rank, t0 = tile * kGatedTile + warp * kSteps;
-    f2 xv[kSteps], d[kSteps], r[kSteps], i[kSteps], n[kSteps], root[kSteps], inv[kSteps], h[kSteps];
+  for (int turn = 0; turn < rounds; ++turn) {
+    const int buf = turn & 1, stage = turn % kStages, t0 = tile_of(turn) * kGatedTile + run * S;
+    const bool whole = (tile_of(turn) + 1) * kGatedTile <= p.tokens;
+    f2 n[S], inv[S], h[S];
     f2 N = 0, E = 0, R = 0, start = next;
+    if constexpr (TMA) {
+      fine = mbar_wait(&sm.full[stage], (turn / kStages) & 1, p.err, kErrWaitFull, fine ? kMaxWaitIters : 1) && fine;
+    } else {
+      load(turn);
+    }
+    // a token's rows, from shared memory or from the registers that they were loaded to
+    auto get = [&](int which, int j) {
+      Two<T, PAIR> v;
+      if constexpr (TMA) {
+        v.load(&sm.rows[stage][which][run * S + j][2 * l], true, true);
+      } else {
+        v = which == 0 ? rx[j] : which == 1 ? rg[j] : which == 2 ? ri[IG ? j : 0] : rd[j];
+      }
+      return v.widen();
+    };
+    // past the end: L = 0, a = 1, and x = dout = 0
+    auto open_of = [&](int j) { return whole || t0 + j < p.tokens ? sigmoid2(get(1, j)) : 0; };
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      xv[j] = rx[j].widen();
-      d[j] = rd[j].widen();
-      r[j] = sigmoid2(rg[j].widen());
-      i[j] = one;
-      if constexpr (IG) i[j] = sigmoid2(ri[j].widen());
-      if (t0 + j >= p.tokens) r[j] = 0;  // past the end: L = 0, a = 1, and x = dout = 0
-      n[j] = decay2(mul2(open, r[j]), near);
-      root[j] = root2(n[j], inv[j]);
-      h[j] = mul2(root[j], mul2(i[j], xv[j]));  // b; the state before later
+    for (int j = 0; j < S; ++j) {
+      n[j] = decay2(mul2(open, open_of(j)), near);
+      f2 u = get(0, j);
+      if constexpr (IG) u = mul2(u, sigmoid2(get(2, j)));
+      h[j] = mul2(root2(n[j], inv[j]), u);  // b; the state before later
       N = step2(n[j], N, n[j]);
       E = step2(n[j], E, h[j]);
     }
 #pragma unroll
-    for (int j = kSteps - 1; j >= 0; --j) {
-      const f2 g = add2(d[j], R);
+    for (int j = S - 1; j >= 0; --j) {
+      const f2 g = add2(get(3, j), R);
       R = fma2(n[j], g, g);
     }
-    if (it > 0) load(tile - K);
-    prod[buf][warp][lane] = N;
-    fwd[buf][warp][lane] = E;
-    rev[buf][warp][lane] = R;
+    maps[buf][run][l] = make_ulonglong2(N, E);
+    backs[buf][run][l] = R;
+    if (turn + 1 < rounds) next = kept_of(turn + 1);
     __syncthreads();
-    if (K > 1) {
+    // every warp is done with the tile before this one, whose place the next one takes
+    if (TMA && turn > 0 && turn + 1 < rounds) load(turn + 1);
+    if constexpr (CL) {
       if (warp == 0) {
         ulonglong2 all = make_ulonglong2(0, 0);
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-          const f2 q = prod[buf][w][lane];
-          all.y = step2(q, all.y, rev[buf][w][lane]);
+        for (int r = kRuns - 1; r >= 0; --r) {
+          const f2 q = maps[buf][r][l].x;
+          all.y = step2(q, all.y, backs[buf][r][l]);
           all.x = step2(q, all.x, q);
         }
-        for (int c = 0; c < K; ++c) store_remote(&tiles[buf][rank][lane], c, all);
+        for (int r = half; r < K; r += 2) store_remote(&tiles[buf][rank][l], r, all);
       }
+      __syncwarp();
       cluster_sync();
     }
-    if (it + 1 < rounds) e = carry[buf ^ 1][lane];
-    for (int c = K - 1; c > rank; --c) {
-      const ulonglong2 q = tiles[buf][c][lane];
-      e = step2(q.x, e, q.y);
+    e = carry[buf ^ 1][l];
+    if constexpr (CL) {
+      for (int c = K - 1; c > rank; --c) {
+        const ulonglong2 q = tiles[buf][c][l];
+        e = step2(q.x, e, q.y);
+      }
     }
 #pragma unroll
-    for (int w = kWarps - 1; w > 0; --w)
-      if (w > warp) e = step2(prod[buf][w][lane], e, rev[buf][w][lane]);
+    for (int w = kGatedWarps - 1; w >= 0; --w) {
+      if (w > warp) {
+        e = step2(maps[buf][2 * w + 1][l].x, e, backs[buf][2 * w + 1][l]);
+        e = step2(maps[buf][2 * w][l].x, e, backs[buf][2 * w][l]);
+      }
+    }
 #pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-      if (w < warp) start = step2(prod[buf][w][lane], start, fwd[buf][w][lane]);
+    for (int w = 0; w < kGatedWarps; ++w) {
+      if (w < warp) {
+        const ulonglong2 q = maps[buf][2 * w][l], r = maps[buf][2 * w + 1][l];
+        start = step2(r.x, step2(q.x, start, q.y), r.y);
+      }
+    }
+    if (half) {
+      const ulonglong2 q = maps[buf][2 * warp][l];
+      start = step2(q.x, start, q.y);
+    } else {
+      e = step2(maps[buf][2 * warp + 1][l].x, e, backs[buf][2 * warp + 1][l]);
+    }
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
+    for (int j = 0; j < S; ++j) {
       const f2 v = h[j];
       h[j] = start;
       start = step2(n[j], start, v);
     }
+    if constexpr (TMA) {  // the rows before these have left
+      if (lane == 0) stores_read();
+      __syncwarp();
+    }
 #pragma unroll
-    for (int j = kSteps - 1; j >= 0; --j) {
-      const f2 g = add2(d[j], e), a = add2(n[j], one), L = mul2(open, r[j]), u = mul2(i[j], xv[j]);
+    for (int j = S - 1; j >= 0; --j) {
+      const f2 r = open_of(j), xv = get(0, j);
+      f2 i = one;
+      if constexpr (IG) i = sigmoid2(get(2, j));
+      const f2 g = add2(get(3, j), e), a = add2(n[j], one), u = mul2(i, xv);
       e = fma2(n[j], g, g);
       // G = g L a (h - u a / sqrt(1 - a^2))
-      const f2 G = mul2(mul2(g, mul2(L, a)), fma2(mul2(mul2(u, a), inv[j]), minus, h[j]));
+      const f2 G = mul2(mul2(g, mul2(mul2(open, r), a)), fma2(mul2(mul2(u, a), inv[j]), minus, h[j]));
       sum = add2(sum, G);
-      if (t0 + j < p.tokens) {
+      // sqrt(1 - a^2) = (1 - a^2) / sqrt(1 - a^2)
+      const f2 gr = mul2(g, mul2(fma2(n[j], fma2(n[j], minus, both(-2.f)), both(1e-36f)), inv[j]));
+      const f2 vx = mul2(gr, i), vg = mul2(G, fma2(r, minus, one)), vi = mul2(mul2(gr, u), fma2(i, minus, one));
+      if constexpr (TMA) {
+        const int row = half * S + j;
+        Two<T, PAIR>::store(&sm.out[warp][0][row][2 * l], upk(vx), true, true);
+        Two<T, PAIR>::store(&sm.out[warp][1][row][2 * l], upk(vg), true, true);
+        if constexpr (IG) Two<T, PAIR>::store(&sm.out[warp][2][row][2 * l], upk(vi), true, true);
+      } else if (t0 + j < p.tokens) {
         const long long t = t0 + j;
-        const f2 gr = mul2(g, root[j]);
-        if (dx) Two<T, PAIR>::store(dx + t * p.sdx[1], upk(mul2(gr, i[j])), ok0, ok1);
-        if (dgate) Two<T, PAIR>::store(dgate + t * p.sdg[1], upk(mul2(G, fma2(r[j], minus, one))), ok0, ok1);
-        if (IG && digate) Two<T, PAIR>::store(digate + t * p.sdi[1], upk(mul2(mul2(gr, u), fma2(i[j], minus, one))), ok0, ok1);
+        if (dx) Two<T, PAIR>::store(dx + t * p.sdx[1], upk(vx), ok0, ok1);
+        if (dgate) Two<T, PAIR>::store(dgate + t * p.sdg[1], upk(vg), ok0, ok1);
+        if (IG && digate) Two<T, PAIR>::store(digate + t * p.sdi[1], upk(vi), ok0, ok1);
       }
     }
-    if (warp == 0) {
-      if (K == 1) {
-        carry[buf][lane] = e;
-      } else if (rank == 0) {
-        for (int c = 0; c < K; ++c) store_remote(&carry[buf][lane], c, e);
+    if constexpr (TMA) {
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0 && t0 < p.tokens) {
+        if (dx) store_rows(&tm.dx, sm.out[warp][0], ct * kGatedCh, t0, b);
+        if (dgate) store_rows(&tm.dgate, sm.out[warp][1], ct * kGatedCh, t0, b);
+        if (IG && digate) store_rows(&tm.digate, sm.out[warp][2], ct * kGatedCh, t0, b);
+        commit_stores();
+      }
+    }
+    if constexpr (!CL) {
+      if (threadIdx.x < 16) carry[buf][l] = e;
+    } else {
+      if (rank == 0 && threadIdx.x < 16) {
+        for (int c = 0; c < K; ++c) store_remote(&carry[buf][l], c, e);
       }
     }
   }
-  auto put_pair = [&](float *q, f2 v) {
-    const float2 w = upk(v);
-    if (ok0) q[c0] = w.x;
-    if (ok1) q[c1] = w.y;
-  };
-  if (p.dinit && rank == 0 && warp == 0) put_pair(p.dinit + (long long)b * p.dim, e);
+  if (p.dinit && rank == 0 && threadIdx.x < 16) put_pair(p.dinit + (long long)b * p.dim, e);
   __syncthreads();
-  prod[0][warp][lane] = sum;
+  backs[0][run][l] = sum;
   __syncthreads();
-  if (p.parts && warp == 0) {
-    f2 s = prod[0][0][lane];
-    for (int w = 1; w < kWarps; ++w) s = add2(s, prod[0][w][lane]);
+  if (p.parts && threadIdx.x < 16) {
+    f2 s = backs[0][0][l];
+    for (int r = 1; r < kRuns; ++r) s = add2(s, backs[0][r][l]);
     put_pair(p.parts + ((long long)b * K + rank) * p.dim, s);
   }
-  if (K > 1) cluster_sync();
+  if constexpr (TMA) {
+    if (lane == 0) stores_done();
+    if (!fine && threadIdx.x == 0) {  // a wait gave up: the copies under way land before the CTA leaves
+      for (int s = 0; s < kStages && s < rounds; ++s) {
+        const int turn = (rounds - 1 - s) / kStages * kStages + s;
+        mbar_wait(&sm.full[s], (turn / kStages) & 1, p.err, kErrWaitFull);
+      }
+    }
+  }
+  if constexpr (CL) cluster_sync();  // nobody leaves while its shared memory is written to
 }
 
 // ddecay = sigmoid(decay) / softplus(decay) times the sum over the parts.
@@ -180,30 +288,56 @@ __global__ void __launch_bounds__(256) ss_gated_ddecay_kernel(const float *parts
   }
 }
 
-template <typename T, bool PAIR, bool IG>
-cudaError_t launch(const GatedBwdParams &p, cudaStream_t s) {
+template <typename T, int ROWS, bool IG, bool CL>
+cudaError_t launch(const GatedBwdParams &p, const BwdMaps &tm, cudaStream_t s) {
+  const auto kernel = ss_gated_bwd_kernel<T, ROWS, IG, CL>;
+  const int smem = ROWS == kTma ? sizeof(BwdSmem<T>) : 0;
+  if (smem) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = p.cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((long long)p.batch * p.channel_tiles * p.cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kGatedThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = p.cluster > 1;
-  return cudaLaunchKernelEx(&cfg, ss_gated_bwd_kernel<T, PAIR, IG>, p);
+  cfg.numAttrs = CL;
+  return cudaLaunchKernelEx(&cfg, kernel, p, tm);
+}
+template <typename T, int ROWS>
+cudaError_t form(const GatedBwdParams &p, const BwdMaps &tm, cudaStream_t s) {
+  if (p.igate) return p.cluster > 1 ? launch<T, ROWS, true, true>(p, tm, s) : launch<T, ROWS, true, false>(p, tm, s);
+  return p.cluster > 1 ? launch<T, ROWS, false, true>(p, tm, s) : launch<T, ROWS, false, false>(p, tm, s);
 }
 template <typename T>
-cudaError_t pick(bool pair, const GatedBwdParams &p, cudaStream_t s) {
-  if (pair) return p.igate ? launch<T, true, true>(p, s) : launch<T, true, false>(p, s);
-  return p.igate ? launch<T, false, true>(p, s) : launch<T, false, false>(p, s);
+cudaError_t pick(int rows, TensorMapEncode enc, const GatedBwdParams &p, cudaStream_t s) {
+  BwdMaps tm;
+  if (rows == kTma) {
+    // what is not there has the map of what is
+    auto map = [&](CUtensorMap *m, const void *base, const long long *st, int box) {
+      return base ? rows_map(enc, m, sizeof(T), base, p.dim, p.tokens, p.batch, st, box) : rows_map(enc, m, sizeof(T), p.x, p.dim, p.tokens, p.batch, p.sx, box);
+    };
+    if (!map(&tm.x, p.x, p.sx, kGatedTile) || !map(&tm.gate, p.gate, p.sg, kGatedTile) || !map(&tm.igate, p.igate, p.si, kGatedTile) ||
+        !map(&tm.dout, p.dout, p.sd, kGatedTile) || !map(&tm.dx, p.dx, p.sdx, 2 * kRun) || !map(&tm.dgate, p.dgate, p.sdg, 2 * kRun) ||
+        !map(&tm.digate, p.digate, p.sdi, 2 * kRun))
+      return cudaErrorInvalidValue;
+    return form<T, kTma>(p, tm, s);
+  }
+  return rows == kPairs ? form<T, kPairs>(p, tm, s) : form<T, kSingles>(p, tm, s);
 }
 
 }  // namespace
 
-cudaError_t launch_gated_bwd(int dtype, bool pair, const GatedBwdParams &p, cudaStream_t s) {
-  cudaError_t e = dtype == 0 ? pick<float>(pair, p, s) : dtype == 1 ? pick<__half>(pair, p, s) : pick<__nv_bfloat16>(pair, p, s);
+cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, GatedBwdParams p, int sms, cudaStream_t s) {
+  p.cluster = gated_cluster((long long)p.batch * p.channel_tiles, p.tiles, sms, kResident);
+  cudaError_t e = dtype == 0   ? pick<float>(rows, enc, p, s)
+                  : dtype == 1 ? pick<__half>(rows, enc, p, s)
+                               : pick<__nv_bfloat16>(rows, enc, p, s);
   if (e != cudaSuccess || !p.ddecay) return e;
   ss_gated_ddecay_kernel<<<(p.dim + 31) / 32, 256, 0, s>>>(p.parts, p.batch * p.cluster, p.dim, p.decay, p.ddecay);
   return cudaGetLastError();

@@ -3,35 +3,40 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ss_packed.h"
+
 namespace ssk {
 
 // The recurrence runs in tiles of kGatedTile tokens by kGatedCh channels; the states
-// that the backward pass starts from are kept at each tile's first token.
+// that the backward pass starts from are kept before each tile.
 constexpr int kGatedTile = 64;
-constexpr int kGatedCh = 64;
+constexpr int kGatedCh = 32;
 constexpr int kGatedMostCluster = 8;
 
 struct GatedScanParams {
   int tokens, dim;      // per sequence
-  int batch, channel_tiles, tiles;  // sequences; tiles of channels; tiles of tokens per sequence
-  int cluster;          // CTAs that take consecutive tiles of a sequence's channels together
+  int batch, channel_tiles;  // sequences; tiles of channels
+  int tiles, cluster;        // tiles of tokens; CTAs that take consecutive ones together (the launcher's choice)
   float rate;
+  int32_t *err;
   const void *x, *gate, *igate;
   const float *decay, *init;  // init (batch, dim) or NULL
   void *out;
   float *last;  // (batch, dim) or NULL
-  float *kept;  // (batch, tiles, dim) or NULL: the state before each tile
+  float *kept;  // (batch, tiles, dim) or NULL
   long long sx[2], sg[2], si[2], so[2];  // sequence, token
   // packed requests (token_request given): one sequence, states by slot
   const int32_t *token_request, *slot_map, *context;
   float *state;
   long long slots, state_stride;
 };
-cudaError_t launch_gated_scan(int dtype, bool pair, const GatedScanParams &p, cudaStream_t s);
+// rows: a RowAccess (ss_gated.cuh); enc: the tensor-map encoder, for kTma.
+cudaError_t launch_gated_scan(int dtype, int rows, TensorMapEncode enc, GatedScanParams p, int sms, cudaStream_t s);
 
 struct GatedBwdParams {
-  int tokens, dim, batch, channel_tiles, tiles, cluster;
+  int tokens, dim, batch, channel_tiles, tiles, cluster;  // as above
   float rate;
+  int32_t *err;
   const void *x, *gate, *igate, *dout;
   const float *decay, *kept, *dlast;  // dlast (batch, dim) or NULL
   void *dx, *dgate, *digate;          // NULL: not wanted
@@ -39,10 +44,7 @@ struct GatedBwdParams {
   float *parts;  // (batch * cluster, dim): sums for ddecay
   long long sx[2], sg[2], si[2], sd[2], sdx[2], sdg[2], sdi[2];
 };
-cudaError_t launch_gated_bwd(int dtype, bool pair, const GatedBwdParams &p, cudaStream_t s);
-
-// CTAs of a cluster along the sequence, for so many (sequence, channel tile) pairs.
-int gated_cluster(long long units, int tiles, int sms);
+cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, GatedBwdParams p, int sms, cudaStream_t s);
 
 struct GatedUpdateParams {
   int rows, dim, vec;  // vec: 16-byte accesses of state rows, and 4 values at once of the others

@@ -15,10 +15,12 @@ constexpr int64_t kMaxUnits = int64_t(1) << 28;  // (sequence, channel tile) pai
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// SMs of the current device (0 on failure).
+// SMs of the current device (0 on failure), whose context is made current: a thread's
+// first call (autograd runs backward passes on threads of its own) finds none, and
+// the tensor-map encoder wants one.
 int device_sms() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   return n;
 }
 
@@ -66,6 +68,17 @@ bool pairs(std::initializer_list<Rows> all, int64_t dim) {
   for (const Rows &r : all)
     if (r.ptr && (!aligned(r.ptr, 2 * r.es) || (r.rows > 1 && r.stride[1] % 2) || (r.outer > 1 && r.stride[0] % 2))) return false;
   return true;
+}
+// How the recurrence's rows come and go: by TMA where every row starts on 16 bytes
+// (broadcast rows do not), else in pairs or single values.
+int rows_kind(std::initializer_list<Rows> all, int64_t dim) {
+  auto off = [](int64_t bytes) { return bytes == 0 || bytes % 16 || bytes >> 40; };
+  bool tma = true;
+  for (const Rows &r : all)
+    if (r.ptr && (!aligned(r.ptr, 16) || (r.rows > 1 && off(r.stride[1] * r.es)) ||
+                  (r.outer > 1 && off(r.stride[0] * r.es))))
+      tma = false;
+  return tma ? 2 : pairs(all, dim) ? 1 : 0;
 }
 // 16-byte accesses.
 bool sixteens(std::initializer_list<Rows> all, int64_t dim, int v) {
@@ -327,14 +340,15 @@ int ss_gated_scan(const ss_gated_scan_params *p, void *stream) {
   if (p->batch == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
   const int sms = device_sms();
-  if (!sms) return SS_ERR_CUDA;
+  const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedScanParams k{};
+  k.err = ssk::packed_error_word();
+  if (!sms || !enc || !k.err) return SS_ERR_CUDA;
   k.tokens = (int)p->seqlen;
   k.dim = (int)p->dim;
   k.batch = (int)p->batch;
   k.channel_tiles = (int)up(p->dim, ssk::kGatedCh);
   k.tiles = (int)up(p->seqlen, ssk::kGatedTile);
-  k.cluster = ssk::gated_cluster((long long)k.batch * k.channel_tiles, k.tiles, sms);
   k.rate = p->rate;
   k.x = p->x; k.gate = p->gate; k.igate = p->input_gate;
   k.decay = p->decay; k.init = p->initial_state;
@@ -343,9 +357,9 @@ int ss_gated_scan(const ss_gated_scan_params *p, void *stream) {
     k.sx[i] = p->x_stride[i]; k.sg[i] = p->gate_stride[i]; k.si[i] = p->input_gate_stride[i]; k.so[i] = p->out_stride[i];
   }
   const int es = elem_size(p->dtype);
-  const bool pair = pairs({SS_ROWS3(p, p->x, p->x_stride, false), SS_ROWS3(p, p->gate, p->gate_stride, false),
+  const int rows = rows_kind({SS_ROWS3(p, p->x, p->x_stride, false), SS_ROWS3(p, p->gate, p->gate_stride, false),
                            SS_ROWS3(p, p->input_gate, p->input_gate_stride, false), SS_ROWS3(p, p->out, p->out_stride, true)}, p->dim);
-  return launched(ssk::launch_gated_scan(p->dtype, pair, k, static_cast<cudaStream_t>(stream)));
+  return launched(ssk::launch_gated_scan(p->dtype, rows, enc, k, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int ss_gated_scan_bwd_validate(const ss_gated_scan_bwd_params *p) { return validate(p); }
@@ -365,14 +379,15 @@ int ss_gated_scan_bwd(const ss_gated_scan_bwd_params *p, void *stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p->batch == 0) return p->ddecay ? launched(cudaMemsetAsync(p->ddecay, 0, 4 * p->dim, s)) : SS_OK;
   const int sms = device_sms();
-  if (!sms) return SS_ERR_CUDA;
+  const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedBwdParams k{};
+  k.err = ssk::packed_error_word();
+  if (!sms || !enc || !k.err) return SS_ERR_CUDA;
   k.tokens = (int)p->seqlen;
   k.dim = (int)p->dim;
   k.batch = (int)p->batch;
   k.channel_tiles = (int)up(p->dim, ssk::kGatedCh);
   k.tiles = (int)up(p->seqlen, ssk::kGatedTile);
-  k.cluster = ssk::gated_cluster((long long)k.batch * k.channel_tiles, k.tiles, sms);
   k.rate = p->rate;
   k.x = p->x; k.gate = p->gate; k.igate = p->input_gate; k.dout = p->dout;
   k.decay = p->decay; k.kept = p->kept; k.dlast = p->dlast;
@@ -384,11 +399,11 @@ int ss_gated_scan_bwd(const ss_gated_scan_bwd_params *p, void *stream) {
     k.sdx[i] = p->dx_stride[i]; k.sdg[i] = p->dgate_stride[i]; k.sdi[i] = p->dinput_gate_stride[i];
   }
   const int es = elem_size(p->dtype);
-  const bool pair = pairs({SS_ROWS3(p, p->x, p->x_stride, false), SS_ROWS3(p, p->gate, p->gate_stride, false),
+  const int rows = rows_kind({SS_ROWS3(p, p->x, p->x_stride, false), SS_ROWS3(p, p->gate, p->gate_stride, false),
                            SS_ROWS3(p, p->input_gate, p->input_gate_stride, false), SS_ROWS3(p, p->dout, p->dout_stride, false),
                            SS_ROWS3(p, p->dx, p->dx_stride, true), SS_ROWS3(p, p->dgate, p->dgate_stride, true),
                            SS_ROWS3(p, p->dinput_gate, p->dinput_gate_stride, true)}, p->dim);
-  return launched(ssk::launch_gated_bwd(p->dtype, pair, k, s));
+  return launched(ssk::launch_gated_bwd(p->dtype, rows, enc, k, sms, s));
 }
 
 int ss_packed_gated_scan_validate(const ss_packed_gated_scan_params *p) { return validate(p); }
@@ -400,14 +415,15 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   if (tokens == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
   const int sms = device_sms();
-  if (!sms) return SS_ERR_CUDA;
+  const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedScanParams k{};
+  k.err = ssk::packed_error_word();
+  if (!sms || !enc || !k.err) return SS_ERR_CUDA;
   k.tokens = (int)tokens;
   k.dim = (int)p->dim;
   k.batch = 1;
   k.channel_tiles = (int)up(p->dim, ssk::kGatedCh);
   k.tiles = (int)up(tokens, ssk::kGatedTile);
-  k.cluster = ssk::gated_cluster(k.channel_tiles, k.tiles, sms);
   k.rate = p->rate;
   k.x = p->x; k.gate = p->gate; k.igate = p->input_gate;
   k.decay = p->decay;
@@ -420,9 +436,9 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   k.slots = p->slots;
   k.state_stride = p->state_stride;
   const int es = elem_size(p->dtype);
-  const bool pair = pairs({SS_ROWS2(tokens, p->x, p->x_stride, false), SS_ROWS2(tokens, p->gate, p->gate_stride, false),
+  const int rows = rows_kind({SS_ROWS2(tokens, p->x, p->x_stride, false), SS_ROWS2(tokens, p->gate, p->gate_stride, false),
                            SS_ROWS2(tokens, p->input_gate, p->input_gate_stride, false), SS_ROWS2(tokens, p->out, p->out_stride, true)}, p->dim);
-  return launched(ssk::launch_gated_scan(p->dtype, pair, k, static_cast<cudaStream_t>(stream)));
+  return launched(ssk::launch_gated_scan(p->dtype, rows, enc, k, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int ss_gated_state_update_validate(const ss_gated_state_update_params *p) { return validate(p); }

@@ -66,6 +66,8 @@ SHAPES = [
     # one token; one channel; under, at and over a warp's 8 and a tile's 64 tokens; clusters; odd widths
     (1, 1, 1), (2, 1, 64), (1, 7, 3), (3, 8, 66), (2, 63, 130), (1, 64, 128), (1, 65, 32), (2, 127, 200), (1, 128, 33),
     (1, 129, 64), (1, 513, 96), (1, 1500, 10), (2, 1025, 31), (5, 300, 2), (700, 3, 64),
+    # enough sequences and channels without clusters; long ones with them, in rows of 16 bytes and not
+    (16, 200, 1288), (24, 131, 903), (350, 130, 48), (1, 5000, 64), (2, 3333, 40), (1, 2100, 81),
 ]
 
 
