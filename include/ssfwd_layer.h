@@ -44,7 +44,11 @@ extern "C" {
  *                NULL: the state before every SS_GATED_TILE-th token, from which
  *                the backward takes up the recurrence.
  *
- * batch * ceil(dim / 32) < 2^28, seqlen and dim < 2^31 - 2^20. out overlaps no input.
+ *   workspace    ss_gated_scan_workspace_size bytes, 16-byte aligned (0 bytes where
+ *                sequences and channels alone fill the device): maps of parts of a
+ *                sequence, which run side by side.
+ *
+ * batch * ceil(dim / 32) < 2^24, seqlen and dim < 2^31 - 2^20. out overlaps no input.
  */
 #define SS_GATED_TILE 64
 
@@ -58,9 +62,12 @@ typedef struct ss_gated_scan_params {
   void *out;
   float *last_state, *kept;
   int64_t x_stride[2], gate_stride[2], input_gate_stride[2], out_stride[2];
+  void *workspace;
+  int64_t workspace_bytes;
 } ss_gated_scan_params;
 
 int ss_gated_scan_validate(const ss_gated_scan_params *p);
+int ss_gated_scan_workspace_size(const ss_gated_scan_params *p, int64_t *bytes);
 int ss_gated_scan(const ss_gated_scan_params *p, void *stream);
 
 /*
@@ -105,6 +112,7 @@ int ss_gated_scan_bwd(const ss_gated_scan_bwd_params *p, void *stream);
  *   x, gate, input_gate, out  (tokens, dim) in dtype, dim stride 1.
  *   state        (slots, dim) fp32, rows of state_stride; NULL: every request starts
  *                from 0 and nothing is kept.
+ *   workspace    ss_packed_gated_scan_workspace_size bytes, 16-byte aligned.
  */
 typedef struct ss_packed_gated_scan_params {
   int32_t abi_version, dtype;
@@ -117,9 +125,12 @@ typedef struct ss_packed_gated_scan_params {
   void *out;
   int64_t x_stride, gate_stride, input_gate_stride, out_stride, state_stride;
   ss_packed_tables tables;
+  void *workspace;
+  int64_t workspace_bytes;
 } ss_packed_gated_scan_params;
 
 int ss_packed_gated_scan_validate(const ss_packed_gated_scan_params *p);
+int ss_packed_gated_scan_workspace_size(const ss_packed_gated_scan_params *p, int64_t *bytes);
 int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream);
 
 /* One token per request: row r goes with state slot_map[r] (or r, when slot_map

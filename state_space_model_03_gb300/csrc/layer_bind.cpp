@@ -15,6 +15,8 @@
 namespace {
 
 int (*g_scan)(const ss_gated_scan_params *, void *);
+int (*g_scan_ws)(const ss_gated_scan_params *, int64_t *);
+int (*g_packed_ws)(const ss_packed_gated_scan_params *, int64_t *);
 int (*g_scan_bwd)(const ss_gated_scan_bwd_params *, void *);
 int (*g_scan_bwd_ws)(const ss_gated_scan_bwd_params *, int64_t *);
 int (*g_packed)(const ss_packed_gated_scan_params *, void *);
@@ -25,7 +27,7 @@ int (*g_norm_bwd_ws)(const ss_rms_norm_bwd_params *, int64_t *);
 int (*g_quant)(const ss_rms_norm_quant_params *, void *);
 
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded(n, 11, [&]() -> PyObject * {
+  return guarded(n, 13, [&]() -> PyObject * {
     auto at_ = [&](int i) { return reinterpret_cast<void *>(integer(a[i])); };
     g_scan = reinterpret_cast<decltype(g_scan)>(at_(0));
     g_scan_bwd = reinterpret_cast<decltype(g_scan_bwd)>(at_(1));
@@ -36,9 +38,11 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(at_(6));
     g_norm_bwd_ws = reinterpret_cast<decltype(g_norm_bwd_ws)>(at_(7));
     g_quant = reinterpret_cast<decltype(g_quant)>(at_(8));
-    g_text = reinterpret_cast<decltype(g_text)>(at_(9));
-    Py_INCREF(a[10]);
-    g_error = a[10];
+    g_scan_ws = reinterpret_cast<decltype(g_scan_ws)>(at_(9));
+    g_packed_ws = reinterpret_cast<decltype(g_packed_ws)>(at_(10));
+    g_text = reinterpret_cast<decltype(g_text)>(at_(11));
+    Py_INCREF(a[12]);
+    g_error = a[12];
     Py_RETURN_NONE;
   });
 }
@@ -139,6 +143,9 @@ Scanned scan_forward(const at::Tensor &x, const at::Tensor &gate, const at::Tens
   p.last_state = static_cast<float *>(place(r.last));
   p.kept = static_cast<float *>(place(r.kept));
   strides(p.out_stride, r.out);
+  check(g_scan_ws(&p, &p.workspace_bytes));
+  const at::Tensor ws = workspace(p.workspace_bytes, x);
+  p.workspace = place(ws);
   check(g_scan(&p, stream_of(x)));
   return r;
 }
@@ -300,6 +307,9 @@ PyObject *packed_gated_scan(PyObject *, PyObject *const *a, Py_ssize_t given) {
     const c10::cuda::CUDAGuard guard(x.device());
     at::Tensor out = at::empty(x.sizes(), x.options());
     p.out = out.data_ptr();
+    check(g_packed_ws(&p, &p.workspace_bytes));
+    const at::Tensor ws = workspace(p.workspace_bytes, x);
+    p.workspace = place(ws);
     check(g_packed(&p, stream_of(x)));
     changed(state);
     return THPVariable_Wrap(std::move(out));

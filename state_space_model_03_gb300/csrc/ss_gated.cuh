@@ -30,32 +30,53 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
 __device__ __forceinline__ f2 both(float v) { return pk(v, v); }
 __device__ __forceinline__ f2 pk(float2 v) { return pk(v.x, v.y); }
 
+// What follows takes N pairs at a time, step by step, so that the instructions of one
+// step, which do not wait for one another, stand together.
+
 // e^L - 1 for L <= 0. In [-1/2, 0] as L (1 + L/2 + ...): a polynomial of degree 5
 // interpolating (e^L - 1) / L at Chebyshev nodes (3e-9 off, coefficients in fp32).
 // `near`: |L| <= 1/2 for every token of the warp's channels (|L| is at most rate
 // softplus(decay)), so that the other form is not needed.
-__device__ __forceinline__ f2 decay2(f2 L, bool near) {
-  f2 q = both(1.1234042468e-03f);
-  q = fma2(q, L, both(8.1896139309e-03f));
-  q = fma2(q, L, both(4.1630074382e-02f));
-  q = fma2(q, L, both(1.6666242480e-01f));
-  q = fma2(q, L, both(4.9999982119e-01f));
-  q = fma2(q, L, both(1.f));
-  f2 n = mul2(q, L);
-  if (!near) {
-    const float2 l = upk(L);
-    float2 v = upk(n);
-    if (l.x < -0.5f) v.x = ex2(l.x * kLog2e) - 1.f;
-    if (l.y < -0.5f) v.y = ex2(l.y * kLog2e) - 1.f;
-    n = pk(v);
+template <int N>
+__device__ __forceinline__ void decay2(const f2 (&L)[N], bool near, f2 (&n)[N]) {
+  constexpr float c[5] = {8.1896139309e-03f, 4.1630074382e-02f, 1.6666242480e-01f, 4.9999982119e-01f, 1.f};
+#pragma unroll
+  for (int j = 0; j < N; ++j) n[j] = fma2(both(1.1234042468e-03f), L[j], both(c[0]));
+#pragma unroll
+  for (int k = 1; k < 5; ++k) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) n[j] = fma2(n[j], L[j], both(c[k]));
   }
-  return n;
+#pragma unroll
+  for (int j = 0; j < N; ++j) n[j] = mul2(n[j], L[j]);
+  if (!near) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float2 l = upk(L[j]);
+      float2 v = upk(n[j]);
+      if (l.x < -0.5f) v.x = ex2(l.x * kLog2e) - 1.f;
+      if (l.y < -0.5f) v.y = ex2(l.y * kLog2e) - 1.f;
+      n[j] = pk(v);
+    }
+  }
 }
 
-__device__ __forceinline__ f2 sigmoid2(f2 v) {
-  float2 e = upk(mul2(v, both(-kLog2e)));
-  e = upk(add2(pk(ex2(e.x), ex2(e.y)), both(1.f)));
-  return pk(rcp(e.x), rcp(e.y));
+template <int N>
+__device__ __forceinline__ void sigmoid2(f2 (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = mul2(v[j], both(-kLog2e));
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float2 e = upk(v[j]);
+    v[j] = pk(ex2(e.x), ex2(e.y));
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = add2(v[j], both(1.f));
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float2 e = upk(v[j]);
+    v[j] = pk(rcp(e.x), rcp(e.y));
+  }
 }
 
 __device__ __forceinline__ float rsqrt_ftz(float v) {
@@ -65,11 +86,19 @@ __device__ __forceinline__ float rsqrt_ftz(float v) {
 }
 // sqrt(1 - a^2) and its reciprocal. 1e-36 more under the root keeps both finite where
 // a is 1; there the root is 1e-18.
-__device__ __forceinline__ f2 root2(f2 n, f2 &inverse) {
-  const f2 m = fma2(n, fma2(n, both(-1.f), both(-2.f)), both(1e-36f));
-  const float2 v = upk(m);
-  inverse = pk(rsqrt_ftz(v.x), rsqrt_ftz(v.y));
-  return mul2(m, inverse);
+template <int N>
+__device__ __forceinline__ void root2(const f2 (&n)[N], f2 (&root)[N], f2 (&inverse)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) root[j] = fma2(n[j], both(-1.f), both(-2.f));
+#pragma unroll
+  for (int j = 0; j < N; ++j) root[j] = fma2(n[j], root[j], both(1e-36f));
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float2 v = upk(root[j]);
+    inverse[j] = pk(rsqrt_ftz(v.x), rsqrt_ftz(v.y));
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) root[j] = mul2(root[j], inverse[j]);
 }
 
 // One token; as well one token's map (n, b) after a run's (N, E), part by part.
@@ -126,11 +155,12 @@ __device__ __forceinline__ uint32_t remote_of(const void *p, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void store_remote(void *p, int rank, ulonglong2 v) {
-  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(remote_of(p, rank)), "l"(v.x), "l"(v.y) : "memory");
-}
-__device__ __forceinline__ void store_remote(void *p, int rank, f2 v) {
-  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote_of(p, rank)), "l"(v) : "memory");
+// 16 bytes to a place of CTA `rank`, counted by a barrier of that CTA: the data and its
+// arrival in one, without a fence or a barrier of the whole cluster.
+__device__ __forceinline__ void send(ulonglong2 *p, uint64_t *bar, int rank, ulonglong2 v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(remote_of(p, rank)),
+               "l"(v.x), "l"(v.y), "r"(remote_of(bar, rank))
+               : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -162,11 +192,9 @@ inline bool rows_map(TensorMapEncode enc, CUtensorMap *m, int esize, const void 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs of a cluster along the sequence: as many as the SMs hold of `resident` CTAs
-// each, so that all run at once, if that is two or more and there are tiles for them.
-inline int gated_cluster(long long units, int tiles, int sms, int resident) {
-  const long long k = (long long)sms * resident / units;
-  return (int)std::max<long long>(1, std::min<long long>(std::min(k, (long long)kGatedMostCluster), tiles));
+// The maps of a unit's segments, one for each lane of a half warp.
+__device__ __forceinline__ ulonglong2 *segment_maps(void *maps, long long unit, int segs, int seg) {
+  return static_cast<ulonglong2 *>(maps) + (unit * segs + seg) * 16;
 }
 
 }  // namespace ssk

@@ -19,7 +19,7 @@ namespace ssk {
 namespace {
 
 constexpr int kStages = 2;
-constexpr int kResident = 4;  // CTAs that an SM holds at least
+constexpr int G = 4;  // tokens whose gates are taken side by side
 
 struct BwdMaps {
   CUtensorMap x, gate, igate, dout, dx, dgate, digate;
@@ -31,6 +31,67 @@ struct BwdSmem {
   uint64_t full[kStages];
 };
 
+// The maps (N, R) of all segments but the first: each half warp takes a part of the
+// segment's tokens that no other comes between.
+template <typename T, bool PAIR>
+__global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_bwd_maps_kernel(const __grid_constant__ GatedBwdParams p) {
+  __shared__ ulonglong2 maps[kRuns][16];
+  let_next_start();
+  const int segs = p.plan.segs - 1, seg = blockIdx.x % segs + 1, unit = blockIdx.x / segs;
+  const int ct = unit % p.channel_tiles, b = unit / p.channel_tiles, l = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int c0 = ct * kGatedCh + (PAIR ? 2 * l : l), c1 = c0 + (PAIR ? 1 : 16);
+  const bool ok0 = c0 < p.dim, ok1 = c1 < p.dim;
+  const float2 most = make_float2(ok0 ? -p.rate * softplus_f(p.decay[c0]) : 0.f, ok1 ? -p.rate * softplus_f(p.decay[c1]) : 0.f);
+  const bool near = __all_sync(~0u, most.x >= -0.5f && most.y >= -0.5f);
+  const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + c0;
+  const T *const dout = static_cast<const T *>(p.dout) + b * p.sd[0] + c0;
+  const int first = (seg * kRuns + run) * p.plan.seg_tiles * kRun;
+  Two<T, PAIR> rg[kRun], rd[kRun];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const long long t = first + k * kRun + j;
+      const bool in = t < p.tokens;
+      rg[j].load(gate + t * p.sg[1], ok0 && in, ok1 && in);
+      rd[j].load(dout + t * p.sd[1], ok0 && in, ok1 && in);
+    }
+  };
+  load(p.plan.seg_tiles - 1);
+  f2 N = 0, R = 0;
+#pragma unroll 1
+  for (int k = p.plan.seg_tiles - 1; k >= 0; --k) {
+    f2 L[kRun], n[kRun], d[kRun];
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      L[j] = rg[j].widen();
+      d[j] = rd[j].widen();
+    }
+    if (k > 0) load(k - 1);
+    sigmoid2(L);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) L[j] = first + k * kRun + j < p.tokens ? mul2(pk(most), L[j]) : 0;
+    decay2(L, near, n);
+#pragma unroll
+    for (int j = kRun - 1; j >= 0; --j) {
+      const f2 g = add2(d[j], R);
+      R = fma2(n[j], g, g);
+      N = step2(n[j], N, n[j]);
+    }
+  }
+  maps[run][l] = make_ulonglong2(N, R);
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    N = R = 0;
+#pragma unroll
+    for (int r = kRuns - 1; r >= 0; --r) {
+      const ulonglong2 q = maps[r][l];
+      R = step2(q.x, R, q.y);
+      N = step2(q.x, N, q.x);
+    }
+    *(segment_maps(p.maps, unit, p.plan.segs, seg) + l) = make_ulonglong2(N, R);
+  }
+}
+
 template <typename T, int ROWS, bool IG, bool CL>
 __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) == 4 ? 2 : 5)
     ss_gated_bwd_kernel(const __grid_constant__ GatedBwdParams p, const __grid_constant__ BwdMaps tm) {
@@ -40,10 +101,12 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
   BwdSmem<T> &sm = *reinterpret_cast<BwdSmem<T> *>(dyn);
   __shared__ ulonglong2 maps[2][kRuns][16];  // (N, E) of the lane's channels, by run
   __shared__ f2 backs[2][kRuns][16];         // R
-  __shared__ ulonglong2 tiles[CL ? 2 : 1][kGatedMostCluster][16];  // (N, R) of whole tiles
+  __shared__ ulonglong2 tiles[CL ? 2 : 1][kGatedMostCluster][16];  // CL: (N, R) of whole tiles
+  __shared__ uint64_t here[2];                                     // CL: they have come
   __shared__ f2 carry[2][16];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), l = lane & 15, half = lane >> 4;
-  const int K = CL ? p.cluster : 1, rank = CL ? blockIdx.x % K : 0, unit = CL ? blockIdx.x / K : blockIdx.x;
+  // CL: a unit's CTAs are a cluster; else they have a segment each
+  const int K = CL ? p.plan.cluster : 1, share = CL ? K : p.plan.segs, rank = blockIdx.x % share, unit = blockIdx.x / share;
   const int ct = unit % p.channel_tiles, b = unit / p.channel_tiles;
   const int run = 2 * warp + half;
   const int c0 = ct * kGatedCh + (PAIR ? 2 * l : l), c1 = c0 + (PAIR ? 1 : 16);
@@ -57,7 +120,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
     if (ok0) q[c0] = w.x;
     if (ok1) q[c1] = w.y;
   };
-  const int rounds = (p.tiles + K - 1) / K;
+  const int rounds = CL ? (p.tiles + K - 1) / K : min(p.plan.seg_tiles, p.tiles - rank * p.plan.seg_tiles);
 
   constexpr int H = TMA ? 1 : S;
   Two<T, PAIR> rx[H], rg[H], ri[H], rd[H];
@@ -69,8 +132,8 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
   T *const dgate = p.dgate ? static_cast<T *>(p.dgate) + b * p.sdg[0] + c0 : nullptr;
   T *const digate = IG && p.digate ? static_cast<T *>(p.digate) + b * p.sdi[0] + c0 : nullptr;
   bool fine = true;
-  // turns count up while the tiles go down: turn k has tile (rounds - 1 - k) K + rank
-  auto tile_of = [&](int turn) { return (rounds - 1 - turn) * K + rank; };
+  // turns count up while the tiles go down
+  auto tile_of = [&](int turn) { return CL ? (rounds - 1 - turn) * K + rank : rank * p.plan.seg_tiles + rounds - 1 - turn; };
   auto load = [&](int turn) {
     const int first = tile_of(turn) * kGatedTile;
     if constexpr (TMA) {
@@ -98,6 +161,14 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
     const int tile = tile_of(turn);
     return tile < p.tiles ? pair_at(p.kept + ((long long)b * p.tiles + tile) * p.dim) : 0;
   };
+  auto expect_maps = [&](int turn) { mbar_arrive_expect_tx(&here[turn & 1], K * sizeof(tiles[0][0])); };
+  if constexpr (CL) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < 2; ++s) mbar_init(&here[s], 1);
+      fence_barrier_init();
+      for (int s = 0; s < 2 && s < rounds; ++s) expect_maps(s);
+    }
+  }
   if constexpr (TMA) {
     if (threadIdx.x == 0) {
       for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1);
@@ -106,11 +177,31 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
     }
   }
   f2 next = kept_of(0);  // the state before the tile that comes next
-  f2 e, sum = 0;
-  // what comes back from past the last token, as if from a turn before the first
-  if (threadIdx.x < 16) carry[1][l] = p.dlast ? pair_at(p.dlast + (long long)b * p.dim) : 0;
-  if constexpr (CL) cluster_sync();
-  else __syncthreads();
+  // what comes back from past the last token; !CL: as if from a turn before the first
+  f2 back = p.dlast ? pair_at(p.dlast + (long long)b * p.dim) : 0, e = 0, sum = 0;
+  if constexpr (CL) {
+    cluster_sync();
+  } else {
+    const int after = share - 1 - rank;  // segments after this one: a part of them for each half warp
+    if (after > 0) {
+      wait_for_previous();
+      const int per = (after + kRuns - 1) / kRuns, from = rank + 1 + run * per, to = min(share, from + per);
+      const ulonglong2 *seg = segment_maps(p.maps, unit, share, 0) + l;
+      f2 N = 0, R = 0;
+#pragma unroll 4
+      for (int k = to - 1; k >= from; --k) {
+        const ulonglong2 q = seg[k * 16];
+        R = step2(q.x, R, q.y);
+        N = step2(q.x, N, q.x);
+      }
+      maps[0][run][l] = make_ulonglong2(N, R);
+      __syncthreads();
+#pragma unroll
+      for (int r = kRuns - 1; r >= 0; --r) back = step2(maps[0][r][l].x, back, maps[0][r][l].y);
+    }
+    if (threadIdx.x < 16) carry[1][l] = back;
+    __syncthreads();
+  }
   const f2 one = both(1.f), minus = both(-1.f);
   for (int turn = 0; turn < rounds; ++turn) {
     const int buf = turn & 1, stage = turn % kStages, t0 = tile_of(turn) * kGatedTile + run * S;
@@ -132,14 +223,39 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
       }
       return v.widen();
     };
-    // past the end: L = 0, a = 1, and x = dout = 0
-    auto open_of = [&](int j) { return whole || t0 + j < p.tokens ? sigmoid2(get(1, j)) : 0; };
+#pragma unroll
+    for (int k = 0; k < S; k += G) {
+      f2 L[G], u[G], part[G], root[G], inverse[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) L[j] = get(1, k + j);
+      sigmoid2(L);
+#pragma unroll
+      for (int j = 0; j < G; ++j) L[j] = mul2(open, L[j]);
+      decay2(L, near, part);
+      root2(part, root, inverse);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        n[k + j] = part[j];
+        inv[k + j] = inverse[j];
+        root[j] = mul2(root[j], get(0, k + j));
+      }
+      if constexpr (IG) {
+#pragma unroll
+        for (int j = 0; j < G; ++j) u[j] = get(2, k + j);
+        sigmoid2(u);
+#pragma unroll
+        for (int j = 0; j < G; ++j) root[j] = mul2(root[j], u[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j) h[k + j] = root[j];  // b; the state before later
+    }
+    if (!whole) {  // past the end the state and what comes back stay (x and dout are 0 there)
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+        if (t0 + j >= p.tokens) n[j] = 0;
+    }
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-      n[j] = decay2(mul2(open, open_of(j)), near);
-      f2 u = get(0, j);
-      if constexpr (IG) u = mul2(u, sigmoid2(get(2, j)));
-      h[j] = mul2(root2(n[j], inv[j]), u);  // b; the state before later
       N = step2(n[j], N, n[j]);
       E = step2(n[j], E, h[j]);
     }
@@ -163,17 +279,18 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
           all.y = step2(q, all.y, backs[buf][r][l]);
           all.x = step2(q, all.x, q);
         }
-        for (int r = half; r < K; r += 2) store_remote(&tiles[buf][rank][l], r, all);
+        // its place there was read in the turn before the last, and every CTA has begun the last one
+        for (int r = half; r < K; r += 2) send(&tiles[buf][rank][l], &here[buf], r, all);
       }
-      __syncwarp();
-      cluster_sync();
-    }
-    e = carry[buf ^ 1][l];
-    if constexpr (CL) {
-      for (int c = K - 1; c > rank; --c) {
+      fine = mbar_wait(&here[buf], (turn >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
+      if (threadIdx.x == 0 && turn + 2 < rounds) expect_maps(turn + 2);
+      for (int c = K - 1; c >= 0; --c) {
+        if (c == rank) e = back;
         const ulonglong2 q = tiles[buf][c][l];
-        e = step2(q.x, e, q.y);
+        back = step2(q.x, back, q.y);
       }
+    } else {
+      e = carry[buf ^ 1][l];
     }
 #pragma unroll
     for (int w = kGatedWarps - 1; w >= 0; --w) {
@@ -201,33 +318,53 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
       h[j] = start;
       start = step2(n[j], start, v);
     }
+    if (!whole) {  // nothing for the decay's gradient: G = 0
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+        if (t0 + j >= p.tokens) h[j] = 0;
+    }
     if constexpr (TMA) {  // the rows before these have left
       if (lane == 0) stores_read();
       __syncwarp();
     }
 #pragma unroll
-    for (int j = S - 1; j >= 0; --j) {
-      const f2 r = open_of(j), xv = get(0, j);
-      f2 i = one;
-      if constexpr (IG) i = sigmoid2(get(2, j));
-      const f2 g = add2(get(3, j), e), a = add2(n[j], one), u = mul2(i, xv);
-      e = fma2(n[j], g, g);
-      // G = g L a (h - u a / sqrt(1 - a^2))
-      const f2 G = mul2(mul2(g, mul2(mul2(open, r), a)), fma2(mul2(mul2(u, a), inv[j]), minus, h[j]));
-      sum = add2(sum, G);
-      // sqrt(1 - a^2) = (1 - a^2) / sqrt(1 - a^2)
-      const f2 gr = mul2(g, mul2(fma2(n[j], fma2(n[j], minus, both(-2.f)), both(1e-36f)), inv[j]));
-      const f2 vx = mul2(gr, i), vg = mul2(G, fma2(r, minus, one)), vi = mul2(mul2(gr, u), fma2(i, minus, one));
-      if constexpr (TMA) {
-        const int row = half * S + j;
-        Two<T, PAIR>::store(&sm.out[warp][0][row][2 * l], upk(vx), true, true);
-        Two<T, PAIR>::store(&sm.out[warp][1][row][2 * l], upk(vg), true, true);
-        if constexpr (IG) Two<T, PAIR>::store(&sm.out[warp][2][row][2 * l], upk(vi), true, true);
-      } else if (t0 + j < p.tokens) {
-        const long long t = t0 + j;
-        if (dx) Two<T, PAIR>::store(dx + t * p.sdx[1], upk(vx), ok0, ok1);
-        if (dgate) Two<T, PAIR>::store(dgate + t * p.sdg[1], upk(vg), ok0, ok1);
-        if (IG && digate) Two<T, PAIR>::store(digate + t * p.sdi[1], upk(vi), ok0, ok1);
+    for (int k = S - G; k >= 0; k -= G) {
+      f2 r[G], i[G], g[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) r[j] = get(1, k + j);
+      sigmoid2(r);
+#pragma unroll
+      for (int j = 0; j < G; ++j) i[j] = one;
+      if constexpr (IG) {
+#pragma unroll
+        for (int j = 0; j < G; ++j) i[j] = get(2, k + j);
+        sigmoid2(i);
+      }
+#pragma unroll
+      for (int j = G - 1; j >= 0; --j) {
+        g[j] = add2(get(3, k + j), e);
+        e = fma2(n[k + j], g[j], g[j]);
+      }
+#pragma unroll
+      for (int j = G - 1; j >= 0; --j) {
+        const f2 m = n[k + j], a = add2(m, one), u = mul2(i[j], get(0, k + j));
+        // G = g L a (h - u a / sqrt(1 - a^2))
+        const f2 Gr = mul2(mul2(g[j], mul2(mul2(open, r[j]), a)), fma2(mul2(mul2(u, a), inv[k + j]), minus, h[k + j]));
+        sum = add2(sum, Gr);
+        // sqrt(1 - a^2) = (1 - a^2) / sqrt(1 - a^2)
+        const f2 gr = mul2(g[j], mul2(fma2(m, fma2(m, minus, both(-2.f)), both(1e-36f)), inv[k + j]));
+        const f2 vx = mul2(gr, i[j]), vg = mul2(Gr, fma2(r[j], minus, one)), vi = mul2(mul2(gr, u), fma2(i[j], minus, one));
+        if constexpr (TMA) {
+          const int row = half * S + k + j;
+          Two<T, PAIR>::store(&sm.out[warp][0][row][2 * l], upk(vx), true, true);
+          Two<T, PAIR>::store(&sm.out[warp][1][row][2 * l], upk(vg), true, true);
+          if constexpr (IG) Two<T, PAIR>::store(&sm.out[warp][2][row][2 * l], upk(vi), true, true);
+        } else if (t0 + k + j < p.tokens) {
+          const long long t = t0 + k + j;
+          if (dx) Two<T, PAIR>::store(dx + t * p.sdx[1], upk(vx), ok0, ok1);
+          if (dgate) Two<T, PAIR>::store(dgate + t * p.sdg[1], upk(vg), ok0, ok1);
+          if (IG && digate) Two<T, PAIR>::store(digate + t * p.sdi[1], upk(vi), ok0, ok1);
+        }
       }
     }
     if constexpr (TMA) {
@@ -240,13 +377,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
         commit_stores();
       }
     }
-    if constexpr (!CL) {
-      if (threadIdx.x < 16) carry[buf][l] = e;
-    } else {
-      if (rank == 0 && threadIdx.x < 16) {
-        for (int c = 0; c < K; ++c) store_remote(&carry[buf][l], c, e);
-      }
-    }
+    if (!CL && threadIdx.x < 16) carry[buf][l] = e;
   }
   if (p.dinit && rank == 0 && threadIdx.x < 16) put_pair(p.dinit + (long long)b * p.dim, e);
   __syncthreads();
@@ -255,7 +386,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
   if (p.parts && threadIdx.x < 16) {
     f2 s = backs[0][0][l];
     for (int r = 1; r < kRuns; ++r) s = add2(s, backs[0][r][l]);
-    put_pair(p.parts + ((long long)b * K + rank) * p.dim, s);
+    put_pair(p.parts + ((long long)b * share + rank) * p.dim, s);
   }
   if constexpr (TMA) {
     if (lane == 0) stores_done();
@@ -296,23 +427,33 @@ cudaError_t launch(const GatedBwdParams &p, const BwdMaps &tm, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
+  const long long units = (long long)p.batch * p.channel_tiles;
+  if (!CL) {
+    if (p.plan.segs > 1) {
+      ss_gated_bwd_maps_kernel<T, ROWS != kSingles><<<(unsigned)(units * (p.plan.segs - 1)), kGatedThreads, 0, s>>>(p);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    return launch_after(kernel, dim3((unsigned)(units * p.plan.segs)), kGatedThreads, smem, s, p.plan.segs > 1, p, tm);
+  }
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.cluster;
+  attr.val.clusterDim.x = p.plan.cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((long long)p.batch * p.channel_tiles * p.cluster));
+  cfg.gridDim = dim3((unsigned)(units * p.plan.cluster));
   cfg.blockDim = dim3(kGatedThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = CL;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, tm);
 }
 template <typename T, int ROWS>
 cudaError_t form(const GatedBwdParams &p, const BwdMaps &tm, cudaStream_t s) {
-  if (p.igate) return p.cluster > 1 ? launch<T, ROWS, true, true>(p, tm, s) : launch<T, ROWS, true, false>(p, tm, s);
-  return p.cluster > 1 ? launch<T, ROWS, false, true>(p, tm, s) : launch<T, ROWS, false, false>(p, tm, s);
+  const bool cl = p.plan.cluster > 1;
+  if (p.igate) return cl ? launch<T, ROWS, true, true>(p, tm, s) : launch<T, ROWS, true, false>(p, tm, s);
+  return cl ? launch<T, ROWS, false, true>(p, tm, s) : launch<T, ROWS, false, false>(p, tm, s);
 }
 template <typename T>
 cudaError_t pick(int rows, TensorMapEncode enc, const GatedBwdParams &p, cudaStream_t s) {
@@ -333,13 +474,12 @@ cudaError_t pick(int rows, TensorMapEncode enc, const GatedBwdParams &p, cudaStr
 
 }  // namespace
 
-cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, GatedBwdParams p, int sms, cudaStream_t s) {
-  p.cluster = gated_cluster((long long)p.batch * p.channel_tiles, p.tiles, sms, kResident);
+cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, const GatedBwdParams &p, cudaStream_t s) {
   cudaError_t e = dtype == 0   ? pick<float>(rows, enc, p, s)
                   : dtype == 1 ? pick<__half>(rows, enc, p, s)
                                : pick<__nv_bfloat16>(rows, enc, p, s);
   if (e != cudaSuccess || !p.ddecay) return e;
-  ss_gated_ddecay_kernel<<<(p.dim + 31) / 32, 256, 0, s>>>(p.parts, p.batch * p.cluster, p.dim, p.decay, p.ddecay);
+  ss_gated_ddecay_kernel<<<(p.dim + 31) / 32, 256, 0, s>>>(p.parts, p.batch * p.plan.cluster * p.plan.segs, p.dim, p.decay, p.ddecay);
   return cudaGetLastError();
 }
 

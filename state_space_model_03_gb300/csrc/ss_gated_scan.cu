@@ -21,8 +21,8 @@ namespace ssk {
 namespace {
 
 constexpr int kStages = 2;
-constexpr int kResident = 4;  // CTAs of a cluster that an SM holds
 constexpr int kBuffers = 3;   // of maps: one is written while the one before is read, up to a barrier later
+constexpr int G = 4;          // tokens whose gates are taken side by side
 constexpr float kCut = 1.f;   // no decay's n, which lies in [-1, 0]
 
 struct ScanMaps {
@@ -48,26 +48,230 @@ __device__ __forceinline__ f2 through(ulonglong2 q, f2 h) {
 }
 
 // PACKED, of a lane's run: bit j of last (first) says that token j ends (starts) a
-// request; of cut, that it starts one or is past the last. request: lane j + 1 of the
-// half has token j's; any: the bits of last of both halves.
+// request; of cut, that it starts one or is past the last. from, to: the slots of the first
+// request that starts (-1: it starts from 0; kKept: from the state that the workspace has)
+// and of the first that ends in the run, looked up a tile ahead; a run rarely has more.
+constexpr int kKept = -2;
 struct Marks {
-  uint32_t cut, first, last, any;
-  int request;
+  uint32_t cut, first, last;
+  int from, to;
+  bool any;  // whether either half has any of these
 };
-__device__ __forceinline__ Marks marks_of(int request, int lane) {
-  const int l = lane & 15, half = lane & 16;
-  const int before = __shfl_up_sync(~0u, request, 1), after = __shfl_down_sync(~0u, request, 1);
-  const bool mine = l >= 1 && l <= kRun;
-  const uint32_t first = __ballot_sync(~0u, mine && request >= 0 && before != request);
-  const uint32_t last = __ballot_sync(~0u, mine && request >= 0 && after != request);
-  const uint32_t none = __ballot_sync(~0u, mine && request < 0);
-  Marks m;
-  m.first = first >> (half + 1) & 0xffu;
-  m.last = last >> (half + 1) & 0xffu;
-  m.cut = m.first | (none >> (half + 1) & 0xffu);
-  m.any = (last >> 1 | last >> 17) & 0xffu;
-  m.request = request;
+
+// q after m, as one map.
+template <bool PACKED>
+__device__ __forceinline__ ulonglong2 then(ulonglong2 m, ulonglong2 q) {
+  const bool cuts = PACKED && (upk(q.x).x == kCut || upk(m.x).x == kCut);
+  return make_ulonglong2(cuts ? both(kCut) : step2(q.x, m.x, q.x), through<PACKED>(q, m.y));
+}
+
+// PACKED: a run's requests and marks. ids: lane j + 1 of a half has the request of its
+// run's token j.
+struct Requests {
+  const GatedScanParams &p;
+  int l, half;
+  int over;  // a request that goes on after the segment (-1: none): another CTA may already have replaced its state
+  __device__ __forceinline__ int ids(int t0) const {
+    const int t = t0 + l - 1;
+    return l < kRun + 2 && t >= 0 && t < p.tokens ? p.token_request[t] : -1;
+  }
+  __device__ __forceinline__ int slot_of(int r) const {
+    const int slot = r >= 0 && p.state ? p.slot_map[r] : -1;
+    return slot < p.slots ? slot : -1;
+  }
+  __device__ __forceinline__ int start_of(int r) const {
+    if (r >= 0 && r == over) return kKept;
+    return r >= 0 && p.context && p.context[r] > 0 ? slot_of(r) : -1;
+  }
+  __device__ __forceinline__ Marks marks(int ids) const {
+    const int before = __shfl_up_sync(~0u, ids, 1), after = __shfl_down_sync(~0u, ids, 1);
+    const bool mine = l >= 1 && l <= kRun;
+    const uint32_t first = __ballot_sync(~0u, mine && ids >= 0 && before != ids);
+    const uint32_t last = __ballot_sync(~0u, mine && ids >= 0 && after != ids);
+    const uint32_t none = __ballot_sync(~0u, mine && ids < 0);
+    Marks m;
+    m.first = first >> (16 * half + 1) & 0xffu;
+    m.last = last >> (16 * half + 1) & 0xffu;
+    m.cut = m.first | (none >> (16 * half + 1) & 0xffu);
+    m.any = (first | last | none) != 0;
+    const int r0 = __shfl_sync(~0u, ids, 16 * half + __ffs(m.first)), r1 = __shfl_sync(~0u, ids, 16 * half + __ffs(m.last));
+    m.from = start_of(m.first ? r0 : -1);
+    m.to = slot_of(m.last ? r1 : -1);
+    return m;
+  }
+};
+
+// n and b of a run's tokens, from their x, gate and input gate.
+template <bool IG, typename Get>
+__device__ __forceinline__ void run_gates(f2 open, bool near, Get get, f2 *n, f2 *e) {
+#pragma unroll
+  for (int k = 0; k < kRun; k += G) {
+    f2 L[G], root[G], inverse[G], part[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) L[j] = get(1, k + j);
+    sigmoid2(L);
+#pragma unroll
+    for (int j = 0; j < G; ++j) L[j] = mul2(open, L[j]);
+    decay2(L, near, part);
+    root2(part, root, inverse);
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      n[k + j] = part[j];
+      root[j] = mul2(root[j], get(0, k + j));
+    }
+    if constexpr (IG) {
+      f2 u[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) u[j] = get(2, k + j);
+      sigmoid2(u);
+#pragma unroll
+      for (int j = 0; j < G; ++j) root[j] = mul2(root[j], u[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j) e[k + j] = root[j];
+  }
+}
+// PACKED: start states into b where requests start, zeros past the last. start: the first
+// one's, afterwards the last one's; of: the state of a slot, or the kept one.
+template <typename Of>
+__device__ __forceinline__ void run_starts(const Requests &req, const Marks &m, int t0, f2 &start, Of of, const f2 *n, f2 *e) {
+#pragma unroll
+  for (int j = 0; j < kRun; ++j) {
+    if (m.first >> j & 1) {
+      if (m.first & ((1u << j) - 1)) start = of(req.start_of(req.p.token_request[t0 + j]));
+      e[j] = step2(n[j], start, e[j]);
+    } else if (m.cut >> j & 1) {
+      e[j] = 0;
+    }
+  }
+}
+// A run's tokens after the map m.
+template <bool PACKED>
+__device__ __forceinline__ ulonglong2 run_map(ulonglong2 m, const Marks &marks, const f2 *n, const f2 *e) {
+  const f2 before = m.y;
+#pragma unroll
+  for (int j = 0; j < kRun; ++j) {
+    m.x = step2(n[j], m.x, n[j]);
+    m.y = step2(n[j], m.y, e[j]);
+  }
+  if constexpr (PACKED) {
+    if (marks.any) {  // again, with the cuts
+      m.y = before;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) m.y = marks.cut >> j & 1 ? e[j] : step2(n[j], m.y, e[j]);
+      if (marks.cut) m.x = both(kCut);
+    }
+  }
   return m;
+}
+
+// What a thread's lane has: two channels of a unit.
+template <bool PAIR>
+struct Lane {
+  int l, half, c0, c1;
+  bool ok0, ok1, near;
+  f2 open;  // L of an open gate
+  __device__ __forceinline__ Lane(const GatedScanParams &p, int ct) {
+    l = threadIdx.x & 15;
+    half = threadIdx.x >> 4 & 1;
+    c0 = ct * kGatedCh + (PAIR ? 2 * l : l);
+    c1 = c0 + (PAIR ? 1 : 16);
+    ok0 = c0 < p.dim;
+    ok1 = c1 < p.dim;
+    const float2 most = make_float2(ok0 ? -p.rate * softplus_f(p.decay[c0]) : 0.f, ok1 ? -p.rate * softplus_f(p.decay[c1]) : 0.f);
+    near = __all_sync(~0u, most.x >= -0.5f && most.y >= -0.5f);
+    open = pk(most);
+  }
+  __device__ __forceinline__ f2 pair_at(const float *q) const { return pk(ok0 ? q[c0] : 0.f, ok1 ? q[c1] : 0.f); }
+  __device__ __forceinline__ void put_pair(float *q, f2 v) const {
+    const float2 w = upk(v);
+    if (ok0) q[c0] = w.x;
+    if (ok1) q[c1] = w.y;
+  }
+};
+
+__device__ __forceinline__ f2 *segment_starts(const GatedScanParams &p, long long unit, int seg) {
+  const long long units = (long long)p.batch * p.channel_tiles;
+  return reinterpret_cast<f2 *>(segment_maps(p.maps, units, p.plan.segs, 0)) + (unit * p.plan.segs + seg) * 16;
+}
+
+// The maps of all segments but the last, and the start state of the last request that
+// starts in each: it may end in another segment, whose CTA then replaces it. Each half warp takes a part of the segment's
+// tokens that no other comes between.
+template <typename T, bool PAIR, bool IG, bool PACKED>
+__global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_maps_kernel(const __grid_constant__ GatedScanParams p) {
+  __shared__ ulonglong2 maps[kRuns][16];
+  __shared__ f2 starts[kRuns][16];
+  __shared__ int started[kRuns];
+  let_next_start();
+  const int segs = p.plan.segs - 1, seg = blockIdx.x % segs, unit = blockIdx.x / segs;
+  const int ct = unit % p.channel_tiles, b = unit / p.channel_tiles;
+  const Lane<PAIR> me(p, ct);
+  const int run = threadIdx.x >> 4;
+  const Requests req{p, me.l, me.half, -1};
+  auto of = [&](int slot) { return slot >= 0 ? me.pair_at(p.state + slot * p.state_stride) : 0; };
+  f2 latest = 0;  // PACKED: the start state of the last request that starts in the segment
+  bool any = false;
+  const T *const x = static_cast<const T *>(p.x) + b * p.sx[0] + me.c0;
+  const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + me.c0;
+  const T *const igate = IG ? static_cast<const T *>(p.igate) + b * p.si[0] + me.c0 : nullptr;
+  const int first = (seg * kRuns + run) * p.plan.seg_tiles * kRun;
+  Two<T, PAIR> rx[kRun], rg[kRun], ri[kRun];
+  int ids = -1;
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const bool in = t0 + j < p.tokens;
+      const long long t = t0 + j;
+      rx[j].load(x + t * p.sx[1], me.ok0 && in, me.ok1 && in);
+      rg[j].load(gate + t * p.sg[1], me.ok0 && in, me.ok1 && in);
+      if constexpr (IG) ri[j].load(igate + t * p.si[1], me.ok0 && in, me.ok1 && in);
+    }
+    if constexpr (PACKED) ids = req.ids(t0);
+  };
+  load(first);
+  ulonglong2 m = make_ulonglong2(0, 0);
+#pragma unroll 1
+  for (int k = 0; k < p.plan.seg_tiles; ++k) {
+    const int t0 = first + k * kRun;
+    Marks marks{};
+    f2 start = 0, n[kRun], e[kRun];
+    if constexpr (PACKED) {
+      marks = req.marks(ids);
+      start = of(marks.from);
+    }
+    run_gates<IG>(me.open, me.near, [&](int which, int j) { return which == 0 ? rx[j].widen() : which == 1 ? rg[j].widen() : ri[j].widen(); }, n, e);
+    if (k + 1 < p.plan.seg_tiles) load(t0 + kRun);
+    if constexpr (PACKED) {
+      if (marks.any) run_starts(req, marks, t0, start, of, n, e);
+      if (marks.first) {
+        latest = start;
+        any = true;
+      }
+    }
+    const ulonglong2 old = m;
+    m = run_map<PACKED>(m, marks, n, e);
+    if (PACKED && upk(old.x).x == kCut) m.x = both(kCut);
+  }
+  maps[run][me.l] = m;
+  if constexpr (PACKED) {
+    starts[run][me.l] = latest;
+    if (me.l == 0) started[run] = any;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    m = maps[0][me.l];
+#pragma unroll
+    for (int r = 1; r < kRuns; ++r) m = then<PACKED>(m, maps[r][me.l]);
+    *(segment_maps(p.maps, unit, p.plan.segs, seg) + me.l) = m;
+    if constexpr (PACKED) {
+      latest = 0;
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r)
+        if (started[r]) latest = starts[r][me.l];
+      *(segment_starts(p, unit, seg) + me.l) = latest;
+    }
+  }
 }
 
 // CL: a cluster's CTAs take consecutive tiles; a tile's output then waits until the next
@@ -81,23 +285,18 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
   ScanSmem<T> &sm = *reinterpret_cast<ScanSmem<T> *>(dyn);
   __shared__ ulonglong2 maps[kBuffers][kRuns][16];                         // (N, E) of the lane's channels, by run
   __shared__ ulonglong2 tiles[CL ? kBuffers : 1][kGatedMostCluster][16];   // CL: the same by CTA
+  __shared__ uint64_t here[CL ? kBuffers : 1];                             // CL: the tiles' maps have come
   __shared__ f2 carry[2][16];                                              // !CL: the state after a tile
-  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), l = lane & 15, half = lane >> 4;
-  const int K = CL ? p.cluster : 1, rank = CL ? blockIdx.x % K : 0, unit = CL ? blockIdx.x / K : blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+  // CL: a unit's CTAs are a cluster; else they have a segment each
+  const int K = CL ? p.plan.cluster : 1, share = CL ? K : p.plan.segs, rank = blockIdx.x % share, unit = blockIdx.x / share;
   const int ct = unit % p.channel_tiles, b = unit / p.channel_tiles;
-  const int run = 2 * warp + half;
-  const int c0 = ct * kGatedCh + (PAIR ? 2 * l : l), c1 = c0 + (PAIR ? 1 : 16);
-  const bool ok0 = c0 < p.dim, ok1 = c1 < p.dim;
-  const float2 most = make_float2(ok0 ? -p.rate * softplus_f(p.decay[c0]) : 0.f, ok1 ? -p.rate * softplus_f(p.decay[c1]) : 0.f);
-  const bool near = __all_sync(~0u, most.x >= -0.5f && most.y >= -0.5f);
-  const f2 open = pk(most);  // L of an open gate
-  auto pair_at = [&](const float *q) { return pk(ok0 ? q[c0] : 0.f, ok1 ? q[c1] : 0.f); };
-  auto put_pair = [&](float *q, f2 v) {
-    const float2 w = upk(v);
-    if (ok0) q[c0] = w.x;
-    if (ok1) q[c1] = w.y;
-  };
-  const int rounds = (p.tiles + K - 1) / K;
+  const Lane<PAIR> me(p, ct);
+  const int l = me.l, half = me.half, run = 2 * warp + half, c0 = me.c0;
+  const bool ok0 = me.ok0, ok1 = me.ok1;
+  auto pair_at = [&](const float *q) { return me.pair_at(q); };
+  const int rounds = CL ? (p.tiles + K - 1) / K : min(p.plan.seg_tiles, p.tiles - rank * p.plan.seg_tiles);
+  auto tile_of = [&](int it) { return CL ? it * K + rank : rank * p.plan.seg_tiles + it; };
 
   // rows: by TMA two tiles ahead, or into registers one tile ahead
   constexpr int H = TMA ? 1 : S;
@@ -108,7 +307,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
   T *const out = static_cast<T *>(p.out) + b * p.so[0] + c0;
   bool fine = true;  // no wait has given up
   auto load = [&](int it) {
-    const int first = (it * K + rank) * kGatedTile;
+    const int first = tile_of(it) * kGatedTile;
     if constexpr (TMA) {
       if (threadIdx.x == 0) {
         const int s = it % kStages;
@@ -128,11 +327,25 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
       }
     }
   };
-  int request = -1;
-  auto load_requests = [&](int it) {
-    const int t = (it * K + rank) * kGatedTile + run * S + l - 1;
-    request = l < S + 2 && t >= 0 && t < p.tokens ? p.token_request[t] : -1;
-  };
+  int over = -1;
+  if (PACKED && !CL && rank < share - 1) {
+    const int end = (rank + 1) * p.plan.seg_tiles * kGatedTile;
+    const int r = p.token_request[end - 1];
+    over = r == p.token_request[end] ? r : -1;
+  }
+  const Requests req{p, l, half, over};
+  f2 kept_start = 0;
+  auto of = [&](int slot) { return slot >= 0 ? pair_at(p.state + slot * p.state_stride) : PACKED && !CL && slot == kKept ? kept_start : 0; };
+  Marks next{};  // of the next tile; ids: of the one after
+  int ids = -1;
+  auto expect_maps = [&](int it) { mbar_arrive_expect_tx(&here[it % kBuffers], K * sizeof(tiles[0][0])); };
+  if constexpr (CL) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < kBuffers; ++s) mbar_init(&here[s], 1);
+      fence_barrier_init();
+      for (int s = 0; s < kBuffers && s < rounds; ++s) expect_maps(s);
+    }
+  }
   if constexpr (TMA) {
     if (threadIdx.x == 0) {
       for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1);
@@ -142,76 +355,77 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
   } else {
     load(0);
   }
-  if constexpr (PACKED) load_requests(0);
+  if constexpr (PACKED) {
+    next = req.marks(req.ids(tile_of(0) * kGatedTile + run * S));
+    if (rounds > 1) ids = req.ids(tile_of(1) * kGatedTile + run * S);
+  }
 
   f2 h = p.init ? pair_at(p.init + (long long)b * p.dim) : 0;  // CL: the state before the cluster's tiles; else what a run ends in
-  if (!CL && threadIdx.x < 16) carry[1][l] = h;
-  if constexpr (CL) cluster_sync();  // every CTA's shared memory is there
-  else __syncthreads();
+  if constexpr (CL) {
+    cluster_sync();  // every CTA's shared memory is there
+  } else {
+    if (PACKED && share > 1) {
+      wait_for_previous();
+      if (rank < share - 1) kept_start = segment_starts(p, unit, rank)[l];
+    }
+    if (rank > 0) {  // the segments before this one: a part of them for each half warp
+      if constexpr (!PACKED) wait_for_previous();
+      const int per = (rank + kRuns - 1) / kRuns, from = run * per, to = min(rank, from + per);
+      const ulonglong2 *seg = segment_maps(p.maps, unit, p.plan.segs, 0) + l;
+      ulonglong2 m = make_ulonglong2(0, 0);
+#pragma unroll 4
+      for (int k = from; k < to; ++k) m = then<PACKED>(m, seg[k * 16]);
+      maps[kBuffers - 1][run][l] = m;  // not written again before the third tile
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r) h = through<PACKED>(maps[kBuffers - 1][r][l], h);
+    }
+    if (threadIdx.x < 16) carry[1][l] = h;
+    __syncthreads();
+  }
 
-  f2 n[S], e[S], pn[CL ? S : 1], pe[CL ? S : 1];
-  Marks now{}, past{};
   // n, e and the map of a run's tokens in tile `it`
-  auto gates = [&](int it) {
-    const int t0 = (it * K + rank) * kGatedTile + run * S;
+  auto gates = [&](int it, f2 *n, f2 *e, Marks &now) {
+    const int t0 = tile_of(it) * kGatedTile + run * S;
+    f2 start = 0;  // PACKED: what the first request that starts in the run starts from
+    if constexpr (PACKED) {
+      now = next;
+      start = of(now.from);
+    }
     if constexpr (TMA) {
       fine = mbar_wait(&sm.full[it % kStages], (it / kStages) & 1, p.err, kErrWaitFull, fine ? kMaxWaitIters : 1) && fine;
     }
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      Two<T, PAIR> vx, vg, vi;
+    auto get = [&](int which, int j) {
+      Two<T, PAIR> v;
       if constexpr (TMA) {
-        vx.load(&sm.rows[it % kStages][0][run * S + j][2 * l], true, true);
-        vg.load(&sm.rows[it % kStages][1][run * S + j][2 * l], true, true);
-        if constexpr (IG) vi.load(&sm.rows[it % kStages][2][run * S + j][2 * l], true, true);
+        v.load(&sm.rows[it % kStages][which][run * S + j][2 * l], true, true);
       } else {
-        vx = rx[j];
-        vg = rg[j];
-        if constexpr (IG) vi = ri[j];
+        v = which == 0 ? rx[j] : which == 1 ? rg[j] : ri[j];
       }
-      n[j] = decay2(mul2(open, sigmoid2(vg.widen())), near);
-      f2 inverse, u = vx.widen();
-      if constexpr (IG) u = mul2(u, sigmoid2(vi.widen()));
-      e[j] = mul2(root2(n[j], inverse), u);
-    }
-    if ((it * K + rank + 1) * kGatedTile > p.tokens) {  // past the end the state stays
+      return v.widen();
+    };
+    run_gates<IG>(me.open, me.near, get, n, e);
+    if ((tile_of(it) + 1) * kGatedTile > p.tokens) {  // past the end the state stays
 #pragma unroll
       for (int j = 0; j < S; ++j)
         if (t0 + j >= p.tokens) n[j] = e[j] = 0;
     }
     if constexpr (PACKED) {
-      now = marks_of(request, lane);
-      if (__any_sync(~0u, now.cut != 0)) {
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          const int r = __shfl_sync(~0u, request, (lane & 16) + j + 1);
-          if (now.first >> j & 1) {
-            const int slot = p.slot_map[r];
-            if (p.state && p.context && p.context[r] > 0 && slot >= 0 && slot < p.slots)
-              e[j] = step2(n[j], pair_at(p.state + slot * p.state_stride), e[j]);
-          } else if (now.cut >> j & 1) {
-            e[j] = 0;
-          }
-        }
+      if (now.any) run_starts(req, now, t0, start, of, n, e);
+      if (it + 1 < rounds) {
+        next = req.marks(ids);
+        ids = it + 2 < rounds ? req.ids(tile_of(it + 2) * kGatedTile + run * S) : -1;
       }
-      if (it + 1 < rounds) load_requests(it + 1);
     }
     if constexpr (!TMA) {
       if (it + 1 < rounds) load(it + 1);
     }
-    ulonglong2 m = make_ulonglong2(n[0], e[0]);
-#pragma unroll
-    for (int j = 1; j < S; ++j) {
-      m.x = step2(n[j], m.x, n[j]);
-      m.y = PACKED && (now.cut >> j & 1) ? e[j] : step2(n[j], m.y, e[j]);
-    }
-    if (PACKED && now.cut) m.x = both(kCut);
-    maps[it % kBuffers][run][l] = m;
+    maps[it % kBuffers][run][l] = run_map<PACKED>(make_ulonglong2(0, 0), now, n, e);
   };
   // the output of tile `it`, from the state before the CTA's tile
   auto finish = [&](int it, f2 v, const f2 *fn, const f2 *fe, const Marks &mk) {
-    const int t0 = (it * K + rank) * kGatedTile + run * S;
-    if (p.kept && threadIdx.x < 16 && t0 < p.tokens) put_pair(p.kept + ((long long)b * p.tiles + it * K + rank) * p.dim, v);
+    const int t0 = tile_of(it) * kGatedTile + run * S;
+    if (p.kept && threadIdx.x < 16 && t0 < p.tokens) me.put_pair(p.kept + ((long long)b * p.tiles + tile_of(it)) * p.dim, v);
     const auto &map = maps[it % kBuffers];
 #pragma unroll
     for (int w = 0; w < kGatedWarps; ++w) {
@@ -222,22 +436,28 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
       if (lane == 0) stores_read();
       __syncwarp();
     }
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      v = PACKED && (mk.cut >> j & 1) ? fe[j] : step2(fn[j], v, fe[j]);
+    auto put = [&](int j) {
       if constexpr (TMA) {
         Two<T, PAIR>::store(&sm.out[warp][half * S + j][2 * l], upk(v), true, true);
       } else {
         if (t0 + j < p.tokens) Two<T, PAIR>::store(out + (t0 + j) * p.so[1], upk(v), ok0, ok1);
       }
-      if constexpr (PACKED) {
-        if (mk.any >> j & 1) {
-          const int r = __shfl_sync(~0u, mk.request, (lane & 16) + j + 1);
-          if (mk.last >> j & 1) {
-            const int slot = p.slot_map[r];
-            if (p.state && slot >= 0 && slot < p.slots) put_pair(p.state + slot * p.state_stride, v);
-          }
+    };
+    if (PACKED && mk.any) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        v = mk.cut >> j & 1 ? fe[j] : step2(fn[j], v, fe[j]);
+        put(j);
+        if (mk.last >> j & 1) {
+          const int slot = (mk.last & ((1u << j) - 1)) == 0 ? mk.to : req.slot_of(p.token_request[t0 + j]);
+          if (slot >= 0) me.put_pair(p.state + slot * p.state_stride, v);
         }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        v = step2(fn[j], v, fe[j]);
+        put(j);
       }
     }
     if constexpr (TMA) {
@@ -252,45 +472,36 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
   };
 
   if constexpr (!CL) {
+    f2 n[S], e[S];
+    Marks now{};
     for (int it = 0; it < rounds; ++it) {
-      gates(it);
+      gates(it, n, e, now);
       __syncthreads();
       if (TMA && it + kStages < rounds) load(it + kStages);
       h = finish(it, carry[(it & 1) ^ 1][l], n, e, now);
       if (threadIdx.x >= kGatedThreads - 16) carry[it & 1][l] = h;
     }
-    if (p.last && threadIdx.x >= kGatedThreads - 16) put_pair(p.last + (long long)b * p.dim, h);
+    if (p.last && rank == share - 1 && threadIdx.x >= kGatedThreads - 16) me.put_pair(p.last + (long long)b * p.dim, h);
   } else {
-    for (int it = 0; it <= rounds; ++it) {
-      if (it > 0) {
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          pn[j] = n[j];
-          pe[j] = e[j];
-        }
-        past = now;
-      }
+    // the gates of tile `it`, and the output of the one before
+    auto turn = [&](int it, f2 *n, f2 *e, Marks &now, const f2 *pn, const f2 *pe, const Marks &past) {
       if (it < rounds) {
-        gates(it);
+        gates(it, n, e, now);
         __syncthreads();
         if (TMA && it + kStages < rounds) load(it + kStages);
       }
-      if (it > 0) cluster_wait();  // the maps of the tiles before are here
-      if (it < rounds) {
-        if (warp == 0) {  // the whole tile's map, to every CTA: half of them from each half
-          const auto &map = maps[it % kBuffers];
-          ulonglong2 all = map[0][l];
+      if (it > 0) {
+        fine = mbar_wait(&here[(it - 1) % kBuffers], ((it - 1) / kBuffers) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
+        if (threadIdx.x == 0 && it - 1 + kBuffers < rounds) expect_maps(it - 1 + kBuffers);
+      }
+      // the whole tile's map, to every CTA, half of them from each half. The place that it
+      // takes there was read two turns before the maps that have just come were sent.
+      if (it < rounds && warp == 0) {
+        const auto &map = maps[it % kBuffers];
+        ulonglong2 all = map[0][l];
 #pragma unroll
-          for (int r = 1; r < kRuns; ++r) {
-            const ulonglong2 q = map[r][l];
-            const bool cuts = PACKED && (upk(q.x).x == kCut || upk(all.x).x == kCut);
-            all.y = through<PACKED>(q, all.y);
-            all.x = cuts ? both(kCut) : step2(q.x, all.x, q.x);
-          }
-          for (int r = half; r < K; r += 2) store_remote(&tiles[it % kBuffers][rank][l], r, all);
-        }
-        __syncwarp();
-        cluster_arrive();
+        for (int r = 1; r < kRuns; ++r) all = then<PACKED>(all, map[r][l]);
+        for (int r = half; r < K; r += 2) send(&tiles[it % kBuffers][rank][l], &here[it % kBuffers], r, all);
       }
       if (it > 0) {
         f2 start = h;
@@ -300,8 +511,29 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
         }
         finish(it - 1, start, pn, pe, past);
       }
+    };
+    if constexpr (!PACKED) {
+      f2 n0[S], e0[S], n1[S], e1[S];
+      Marks m0{}, m1{};
+      for (int it = 0; it <= rounds; it += 2) {
+        turn(it, n0, e0, m0, n1, e1, m1);
+        if (it < rounds) turn(it + 1, n1, e1, m1, n0, e0, m0);
+      }
+    } else {  // one copy of the longer code: two do not fit the instruction cache (16384 x 2560: 107 us, 137 with two)
+      f2 n[S] = {}, e[S] = {}, pn[S], pe[S];
+      Marks now{}, past{};
+#pragma unroll 1
+      for (int it = 0; it <= rounds; ++it) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          pn[j] = n[j];
+          pe[j] = e[j];
+        }
+        past = now;
+        turn(it, n, e, now, pn, pe, past);
+      }
     }
-    if (p.last && rank == 0 && threadIdx.x < 16) put_pair(p.last + (long long)b * p.dim, h);
+    if (p.last && rank == 0 && threadIdx.x < 16) me.put_pair(p.last + (long long)b * p.dim, h);
     cluster_sync();  // nobody leaves while its shared memory is written to
   }
   if constexpr (TMA) {
@@ -323,27 +555,36 @@ cudaError_t launch(const GatedScanParams &p, const ScanMaps &tm, cudaStream_t s)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
+  const long long units = (long long)p.batch * p.channel_tiles;
+  if (!CL) {
+    if (p.plan.segs > 1) {
+      ss_gated_maps_kernel<T, ROWS != kSingles, IG, PACKED><<<(unsigned)(units * (p.plan.segs - 1)), kGatedThreads, 0, s>>>(p);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    return launch_after(kernel, dim3((unsigned)(units * p.plan.segs)), kGatedThreads, smem, s, p.plan.segs > 1, p, tm);
+  }
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.cluster;
+  attr.val.clusterDim.x = p.plan.cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((long long)p.batch * p.channel_tiles * p.cluster));
+  cfg.gridDim = dim3((unsigned)(units * p.plan.cluster));
   cfg.blockDim = dim3(kGatedThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = CL;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, tm);
 }
 template <typename T, int ROWS, bool IG>
 cudaError_t form(const GatedScanParams &p, const ScanMaps &tm, cudaStream_t s) {
-  if (p.token_request) return p.cluster > 1 ? launch<T, ROWS, IG, true, true>(p, tm, s) : launch<T, ROWS, IG, true, false>(p, tm, s);
-  return p.cluster > 1 ? launch<T, ROWS, IG, false, true>(p, tm, s) : launch<T, ROWS, IG, false, false>(p, tm, s);
+  const bool cl = p.plan.cluster > 1;
+  if (p.token_request) return cl ? launch<T, ROWS, IG, true, true>(p, tm, s) : launch<T, ROWS, IG, true, false>(p, tm, s);
+  return cl ? launch<T, ROWS, IG, false, true>(p, tm, s) : launch<T, ROWS, IG, false, false>(p, tm, s);
 }
 template <typename T>
-cudaError_t pick(int rows, TensorMapEncode enc, GatedScanParams &p, int sms, cudaStream_t s) {
-  p.cluster = gated_cluster((long long)p.batch * p.channel_tiles, p.tiles, sms, kResident);
+cudaError_t pick(int rows, TensorMapEncode enc, const GatedScanParams &p, cudaStream_t s) {
   ScanMaps tm;
   if (rows == kTma) {
     auto map = [&](CUtensorMap *m, const void *base, const long long *st, int box) {
@@ -360,10 +601,31 @@ cudaError_t pick(int rows, TensorMapEncode enc, GatedScanParams &p, int sms, cud
 
 }  // namespace
 
-cudaError_t launch_gated_scan(int dtype, int rows, TensorMapEncode enc, GatedScanParams p, int sms, cudaStream_t s) {
-  return dtype == 0   ? pick<float>(rows, enc, p, sms, s)
-         : dtype == 1 ? pick<__half>(rows, enc, p, sms, s)
-                      : pick<__nv_bfloat16>(rows, enc, p, sms, s);
+#ifndef SS_SEG_CTAS
+#define SS_SEG_CTAS 304
+#endif
+#ifndef SS_SEG_ROUNDS
+#define SS_SEG_ROUNDS 4
+#endif
+GatedPlan gated_plan(long long units, int tiles) {
+  constexpr int kSms = 152, kResident = 4;  // CTAs of a cluster that an SM holds
+  GatedPlan plan{1, 1, tiles};
+  if (units < 1 || tiles < 2) return plan;
+  const long long k = std::min<long long>(std::min<long long>(kSms * kResident / units, kGatedMostCluster), tiles);
+  if (units * kGatedMostCluster < SS_SEG_CTAS && tiles > SS_SEG_ROUNDS * kGatedMostCluster) {
+    const long long segs = std::min<long long>(std::min<long long>((SS_SEG_CTAS + units - 1) / units, kGatedMostSegs), tiles);
+    plan.seg_tiles = (int)((tiles + segs - 1) / segs);
+    plan.segs = (tiles + plan.seg_tiles - 1) / plan.seg_tiles;
+    return plan;
+  }
+  if (k > 1) plan.cluster = (int)k;
+  return plan;
+}
+
+cudaError_t launch_gated_scan(int dtype, int rows, TensorMapEncode enc, const GatedScanParams &p, cudaStream_t s) {
+  return dtype == 0   ? pick<float>(rows, enc, p, s)
+         : dtype == 1 ? pick<__half>(rows, enc, p, s)
+                      : pick<__nv_bfloat16>(rows, enc, p, s);
 }
 
 }  // namespace ssk

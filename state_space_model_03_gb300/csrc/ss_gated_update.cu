@@ -78,10 +78,17 @@ __global__ void __launch_bounds__(kCta) ss_gated_update_kernel(const __grid_cons
     for (int j = 0; j < V; j += W) {
       float2 v = make_float2(0.f, 0.f);
       if (live[u]) {
-        f2 inverse, w = at2(xv[u].v, j);
-        const f2 n = decay2(mul2(open[j / W], sigmoid2(at2(g[u].v, j))), near);
-        if constexpr (IG) w = mul2(w, sigmoid2(at2(i[u].v, j)));
-        v = upk(step2(n, at2(h[u].v, j), mul2(root2(n, inverse), w)));
+        f2 r[1] = {at2(g[u].v, j)}, n[1], root[1], inverse[1], w = at2(xv[u].v, j);
+        sigmoid2(r);
+        r[0] = mul2(open[j / W], r[0]);
+        decay2(r, near, n);
+        root2(n, root, inverse);
+        if constexpr (IG) {
+          f2 in[1] = {at2(i[u].v, j)};
+          sigmoid2(in);
+          w = mul2(w, in[0]);
+        }
+        v = upk(step2(n[0], at2(h[u].v, j), mul2(root[0], w)));
       }
       h[u].v[j] = o.v[j] = v.x;
       if constexpr (W == 2) h[u].v[j + 1] = o.v[j + 1] = v.y;

@@ -8,15 +8,28 @@
 namespace ssk {
 
 // The recurrence runs in tiles of kGatedTile tokens by kGatedCh channels; the states
-// that the backward pass starts from are kept before each tile.
+// that the backward pass starts from are kept before each tile. How the tiles of a
+// (sequence, channel tile) pair, a unit, are shared out:
+//   cluster  CTAs that take consecutive tiles together, or
+//   segs     segments of seg_tiles tiles, each a CTA's, which one launch reduces to
+//            their maps (states in the workspace) before another runs them.
 constexpr int kGatedTile = 64;
 constexpr int kGatedCh = 32;
 constexpr int kGatedMostCluster = 8;
+constexpr int kGatedMostSegs = 128;
+struct GatedPlan {
+  int cluster, segs, seg_tiles;
+};
+GatedPlan gated_plan(long long units, int tiles);
+// Of each segment 16 lanes' maps (two pairs), and after all of these 16 lanes' start states.
+inline long long gated_map_bytes(long long units, const GatedPlan &plan) { return plan.segs > 1 ? units * plan.segs * 384 : 0; }
 
 struct GatedScanParams {
   int tokens, dim;      // per sequence
   int batch, channel_tiles;  // sequences; tiles of channels
-  int tiles, cluster;        // tiles of tokens; CTAs that take consecutive ones together (the launcher's choice)
+  int tiles;                 // of tokens
+  GatedPlan plan;
+  void *maps;  // gated_map_bytes
   float rate;
   int32_t *err;
   const void *x, *gate, *igate;
@@ -31,20 +44,22 @@ struct GatedScanParams {
   long long slots, state_stride;
 };
 // rows: a RowAccess (ss_gated.cuh); enc: the tensor-map encoder, for kTma.
-cudaError_t launch_gated_scan(int dtype, int rows, TensorMapEncode enc, GatedScanParams p, int sms, cudaStream_t s);
+cudaError_t launch_gated_scan(int dtype, int rows, TensorMapEncode enc, const GatedScanParams &p, cudaStream_t s);
 
 struct GatedBwdParams {
-  int tokens, dim, batch, channel_tiles, tiles, cluster;  // as above
+  int tokens, dim, batch, channel_tiles, tiles;  // as above
+  GatedPlan plan;
+  void *maps;
   float rate;
   int32_t *err;
   const void *x, *gate, *igate, *dout;
   const float *decay, *kept, *dlast;  // dlast (batch, dim) or NULL
   void *dx, *dgate, *digate;          // NULL: not wanted
   float *ddecay, *dinit;
-  float *parts;  // (batch * cluster, dim): sums for ddecay
+  float *parts;  // (batch * cluster * segs, dim): sums for ddecay
   long long sx[2], sg[2], si[2], sd[2], sdx[2], sdg[2], sdi[2];
 };
-cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, GatedBwdParams p, int sms, cudaStream_t s);
+cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, const GatedBwdParams &p, cudaStream_t s);
 
 struct GatedUpdateParams {
   int rows, dim, vec;  // vec: 16-byte accesses of state rows, and 4 values at once of the others

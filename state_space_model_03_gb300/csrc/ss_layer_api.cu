@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr int64_t kMaxUnits = int64_t(1) << 28;  // (sequence, channel tile) pairs: times a cluster's CTAs a grid holds them
+constexpr int64_t kMaxUnits = int64_t(1) << 24;  // (sequence, channel tile) pairs: times a cluster's CTAs or segments a grid holds them
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -113,7 +113,7 @@ int check_dense(int abi, int dtype, float rate, int64_t batch, int64_t seqlen, i
   return SS_OK;
 }
 
-int validate(const ss_gated_scan_params *p) {
+int validate_operands(const ss_gated_scan_params *p) {
   if (!p) return SS_ERR_NULL;
   int st = check_dense(p->abi_version, p->dtype, p->rate, p->batch, p->seqlen, p->dim);
   if (st != SS_OK || p->batch == 0) return st;
@@ -162,17 +162,32 @@ int validate_operands(const ss_gated_scan_bwd_params *p) {
   }
   return SS_OK;
 }
-// Parts of ddecay by sequence and CTA of a cluster, of the most CTAs that there are.
-int64_t bwd_workspace(const ss_gated_scan_bwd_params *p) {
-  return p->ddecay && p->batch > 0 ? 4 * p->batch * ssk::kGatedMostCluster * p->dim : 0;
+// How the units are shared out, and the workspace for it: the segments' maps, and for the
+// backward the parts of ddecay by sequence and CTA.
+template <typename P>
+ssk::GatedPlan dense_plan(const P *p) {
+  return ssk::gated_plan(p->batch * up(p->dim, ssk::kGatedCh), (int)up(p->seqlen, ssk::kGatedTile));
+}
+int64_t workspace_of(const ss_gated_scan_params *p) {
+  return ssk::gated_map_bytes(p->batch * up(p->dim, ssk::kGatedCh), dense_plan(p));
+}
+int64_t workspace_of(const ss_gated_scan_bwd_params *p) {
+  if (p->batch == 0) return 0;
+  const ssk::GatedPlan plan = dense_plan(p);
+  return ssk::gated_map_bytes(p->batch * up(p->dim, ssk::kGatedCh), plan) + (p->ddecay ? 4 * p->batch * plan.cluster * plan.segs * p->dim : 0);
+}
+template <typename P>
+int check_workspace(const P *p, int64_t need) {
+  if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return SS_ERR_SCRATCH;
+  return need > 0 && !aligned(p->workspace, 16) ? SS_ERR_ALIGN : SS_OK;
+}
+int validate(const ss_gated_scan_params *p) {
+  const int st = validate_operands(p);
+  return st != SS_OK ? st : check_workspace(p, workspace_of(p));
 }
 int validate(const ss_gated_scan_bwd_params *p) {
   const int st = validate_operands(p);
-  if (st != SS_OK) return st;
-  const int64_t need = bwd_workspace(p);
-  if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return SS_ERR_SCRATCH;
-  if (need > 0 && !aligned(p->workspace, 16)) return SS_ERR_ALIGN;
-  return SS_OK;
+  return st != SS_OK ? st : check_workspace(p, workspace_of(p));
 }
 
 #define SS_ROWS2(n, ptr, st, w) Rows{ptr, es, 1, n, p->dim, {0, st}, w}
@@ -201,12 +216,21 @@ int check_by_slot(const P *p, int64_t rows, const int32_t *slot_map) {
   return SS_OK;
 }
 
-int validate(const ss_packed_gated_scan_params *p) {
+int validate_operands(const ss_packed_gated_scan_params *p) {
   if (!p) return SS_ERR_NULL;
   int st = check_gated(p->abi_version, p->dtype, p->rate, p->dim);
   if (st == SS_OK) st = validate(p->tables);
   if (st != SS_OK) return st;
+  if (up(p->dim, ssk::kGatedCh) >= kMaxUnits) return SS_ERR_UNSUPPORTED;
   return check_by_slot(p, p->tables.tokens, nullptr);
+}
+ssk::GatedPlan packed_plan(const ss_packed_gated_scan_params *p) {
+  return ssk::gated_plan(up(p->dim, ssk::kGatedCh), (int)up(p->tables.tokens, ssk::kGatedTile));
+}
+int64_t workspace_of(const ss_packed_gated_scan_params *p) { return ssk::gated_map_bytes(up(p->dim, ssk::kGatedCh), packed_plan(p)); }
+int validate(const ss_packed_gated_scan_params *p) {
+  const int st = validate_operands(p);
+  return st != SS_OK ? st : check_workspace(p, workspace_of(p));
 }
 
 int validate(const ss_gated_state_update_params *p) {
@@ -334,16 +358,24 @@ extern "C" {
 
 int ss_gated_scan_validate(const ss_gated_scan_params *p) { return validate(p); }
 
+int ss_gated_scan_workspace_size(const ss_gated_scan_params *p, int64_t *bytes) {
+  if (!bytes) return SS_ERR_NULL;
+  const int st = validate_operands(p);
+  if (st != SS_OK) return st;
+  *bytes = p->batch == 0 ? 0 : workspace_of(p);
+  return SS_OK;
+}
+
 int ss_gated_scan(const ss_gated_scan_params *p, void *stream) {
   const int st = validate(p);
   if (st != SS_OK) return st;
   if (p->batch == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
-  const int sms = device_sms();
+  const bool ready = device_sms() > 0;
   const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedScanParams k{};
   k.err = ssk::packed_error_word();
-  if (!sms || !enc || !k.err) return SS_ERR_CUDA;
+  if (!ready || !enc || !k.err) return SS_ERR_CUDA;
   k.tokens = (int)p->seqlen;
   k.dim = (int)p->dim;
   k.batch = (int)p->batch;
@@ -353,13 +385,15 @@ int ss_gated_scan(const ss_gated_scan_params *p, void *stream) {
   k.x = p->x; k.gate = p->gate; k.igate = p->input_gate;
   k.decay = p->decay; k.init = p->initial_state;
   k.out = p->out; k.last = p->last_state; k.kept = p->kept;
+  k.plan = dense_plan(p);
+  k.maps = p->workspace;
   for (int i = 0; i < 2; ++i) {
     k.sx[i] = p->x_stride[i]; k.sg[i] = p->gate_stride[i]; k.si[i] = p->input_gate_stride[i]; k.so[i] = p->out_stride[i];
   }
   const int es = elem_size(p->dtype);
   const int rows = rows_kind({SS_ROWS3(p, p->x, p->x_stride, false), SS_ROWS3(p, p->gate, p->gate_stride, false),
                            SS_ROWS3(p, p->input_gate, p->input_gate_stride, false), SS_ROWS3(p, p->out, p->out_stride, true)}, p->dim);
-  return launched(ssk::launch_gated_scan(p->dtype, rows, enc, k, sms, static_cast<cudaStream_t>(stream)));
+  return launched(ssk::launch_gated_scan(p->dtype, rows, enc, k, static_cast<cudaStream_t>(stream)));
 }
 
 int ss_gated_scan_bwd_validate(const ss_gated_scan_bwd_params *p) { return validate(p); }
@@ -368,7 +402,7 @@ int ss_gated_scan_bwd_workspace_size(const ss_gated_scan_bwd_params *p, int64_t 
   if (!bytes) return SS_ERR_NULL;
   const int st = validate_operands(p);
   if (st != SS_OK) return st;
-  *bytes = bwd_workspace(p);
+  *bytes = workspace_of(p);
   return SS_OK;
 }
 
@@ -378,11 +412,11 @@ int ss_gated_scan_bwd(const ss_gated_scan_bwd_params *p, void *stream) {
   if (launch_fault()) return SS_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p->batch == 0) return p->ddecay ? launched(cudaMemsetAsync(p->ddecay, 0, 4 * p->dim, s)) : SS_OK;
-  const int sms = device_sms();
+  const bool ready = device_sms() > 0;
   const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedBwdParams k{};
   k.err = ssk::packed_error_word();
-  if (!sms || !enc || !k.err) return SS_ERR_CUDA;
+  if (!ready || !enc || !k.err) return SS_ERR_CUDA;
   k.tokens = (int)p->seqlen;
   k.dim = (int)p->dim;
   k.batch = (int)p->batch;
@@ -393,7 +427,9 @@ int ss_gated_scan_bwd(const ss_gated_scan_bwd_params *p, void *stream) {
   k.decay = p->decay; k.kept = p->kept; k.dlast = p->dlast;
   k.dx = p->dx; k.dgate = p->dgate; k.digate = p->dinput_gate;
   k.ddecay = p->ddecay; k.dinit = p->dinitial_state;
-  k.parts = p->ddecay ? static_cast<float *>(p->workspace) : nullptr;
+  k.plan = dense_plan(p);
+  k.maps = p->workspace;
+  k.parts = p->ddecay ? reinterpret_cast<float *>(static_cast<char *>(p->workspace) + ssk::gated_map_bytes((long long)k.batch * k.channel_tiles, k.plan)) : nullptr;
   for (int i = 0; i < 2; ++i) {
     k.sx[i] = p->x_stride[i]; k.sg[i] = p->gate_stride[i]; k.si[i] = p->input_gate_stride[i]; k.sd[i] = p->dout_stride[i];
     k.sdx[i] = p->dx_stride[i]; k.sdg[i] = p->dgate_stride[i]; k.sdi[i] = p->dinput_gate_stride[i];
@@ -403,10 +439,18 @@ int ss_gated_scan_bwd(const ss_gated_scan_bwd_params *p, void *stream) {
                            SS_ROWS3(p, p->input_gate, p->input_gate_stride, false), SS_ROWS3(p, p->dout, p->dout_stride, false),
                            SS_ROWS3(p, p->dx, p->dx_stride, true), SS_ROWS3(p, p->dgate, p->dgate_stride, true),
                            SS_ROWS3(p, p->dinput_gate, p->dinput_gate_stride, true)}, p->dim);
-  return launched(ssk::launch_gated_bwd(p->dtype, rows, enc, k, sms, s));
+  return launched(ssk::launch_gated_bwd(p->dtype, rows, enc, k, s));
 }
 
 int ss_packed_gated_scan_validate(const ss_packed_gated_scan_params *p) { return validate(p); }
+
+int ss_packed_gated_scan_workspace_size(const ss_packed_gated_scan_params *p, int64_t *bytes) {
+  if (!bytes) return SS_ERR_NULL;
+  const int st = validate_operands(p);
+  if (st != SS_OK) return st;
+  *bytes = workspace_of(p);
+  return SS_OK;
+}
 
 int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   const int st = validate(p);
@@ -414,11 +458,11 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   const int64_t tokens = p->tables.tokens;
   if (tokens == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
-  const int sms = device_sms();
+  const bool ready = device_sms() > 0;
   const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedScanParams k{};
   k.err = ssk::packed_error_word();
-  if (!sms || !enc || !k.err) return SS_ERR_CUDA;
+  if (!ready || !enc || !k.err) return SS_ERR_CUDA;
   k.tokens = (int)tokens;
   k.dim = (int)p->dim;
   k.batch = 1;
@@ -429,6 +473,8 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   k.decay = p->decay;
   k.out = p->out;
   k.sx[1] = p->x_stride; k.sg[1] = p->gate_stride; k.si[1] = p->input_gate_stride; k.so[1] = p->out_stride;
+  k.plan = packed_plan(p);
+  k.maps = p->workspace;
   k.token_request = p->tables.token_request;
   k.slot_map = p->tables.slot_map;
   k.context = p->tables.context;
@@ -438,7 +484,7 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   const int es = elem_size(p->dtype);
   const int rows = rows_kind({SS_ROWS2(tokens, p->x, p->x_stride, false), SS_ROWS2(tokens, p->gate, p->gate_stride, false),
                            SS_ROWS2(tokens, p->input_gate, p->input_gate_stride, false), SS_ROWS2(tokens, p->out, p->out_stride, true)}, p->dim);
-  return launched(ssk::launch_gated_scan(p->dtype, rows, enc, k, sms, static_cast<cudaStream_t>(stream)));
+  return launched(ssk::launch_gated_scan(p->dtype, rows, enc, k, static_cast<cudaStream_t>(stream)));
 }
 
 int ss_gated_state_update_validate(const ss_gated_state_update_params *p) { return validate(p); }

@@ -26,7 +26,7 @@ def _load_bind():
     global _bind_module
     names = ("ss_gated_scan", "ss_gated_scan_bwd", "ss_gated_scan_bwd_workspace_size", "ss_packed_gated_scan",
              "ss_gated_state_update", "ss_rms_norm", "ss_rms_norm_bwd", "ss_rms_norm_bwd_workspace_size",
-             "ss_rms_norm_quant", "ss_status_string")
+             "ss_rms_norm_quant", "ss_gated_scan_workspace_size", "ss_packed_gated_scan_workspace_size", "ss_status_string")
     _bind_module = _load_extension("_layer_bind", names)
     return _bind_module
 

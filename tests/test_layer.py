@@ -67,7 +67,7 @@ SHAPES = [
     (1, 1, 1), (2, 1, 64), (1, 7, 3), (3, 8, 66), (2, 63, 130), (1, 64, 128), (1, 65, 32), (2, 127, 200), (1, 128, 33),
     (1, 129, 64), (1, 513, 96), (1, 1500, 10), (2, 1025, 31), (5, 300, 2), (700, 3, 64),
     # enough sequences and channels without clusters; long ones with them, in rows of 16 bytes and not
-    (16, 200, 1288), (24, 131, 903), (350, 130, 48), (1, 5000, 64), (2, 3333, 40), (1, 2100, 81),
+    (16, 200, 1288), (24, 131, 903), (1, 16384, 24), (3, 9000, 100), (350, 130, 48), (1, 5000, 64), (2, 3333, 40), (1, 2100, 81),
 ]
 
 
@@ -286,6 +286,9 @@ def _run_packed(p, t, st, lengths, dtype, block=512):
 @pytest.mark.parametrize("lengths,dim,ig,pad", [
     (RAGGED, 96, True, 0), (RAGGED, 33, False, 13), ([1], 1, True, 0), ([0, 0, 5], 64, False, 100), ([1] * 300, 64, True, 0),
     ([700], 130, True, 0), ([64, 128, 64], 64, True, 64), ([8] * 40, 200, False, 1), ([0, 2000, 0, 1], 66, True, 3),
+    # segments of many tiles: requests that start in one and end in another, that fill some, that end where one does
+    ([5000, 64, 700, 1984, 1, 2047, 3], 40, True, 50), ([1] * 999 + [3000, 1000], 24, False, 0), ([8192, 8192], 33, True, 0),
+    (RAGGED * 40, 16, True, 0), ([64] * 100, 96, False, 0),
 ])
 def test_packed(dtype, lengths, dim, ig, pad):
     p, t, st = _packed_problem(lengths, dim, dtype, ig, pad, seed=len(lengths) + dim)
