@@ -26,8 +26,9 @@ struct BwdMaps {
 };
 template <typename T>
 struct BwdSmem {
+  // x, gate, input gate and dout of a tile; where a token's have been used, its gradients
+  // dx, dgate and dinput_gate take their place and leave from there
   T rows[kStages][4][kGatedTile][kGatedCh];
-  T out[kGatedWarps][3][2 * kRun][kGatedCh];
   uint64_t full[kStages];
 };
 
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_bwd_maps_kernel(con
 }
 
 template <typename T, int ROWS, bool IG, bool CL>
-__global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) == 4 ? 2 : 5)
+__global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) == 4 ? 3 : 5)
     ss_gated_bwd_kernel(const __grid_constant__ GatedBwdParams p, const __grid_constant__ BwdMaps tm) {
   constexpr int S = kRun;
   constexpr bool TMA = ROWS == kTma, PAIR = ROWS != kSingles;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
   const int rounds = CL ? (p.tiles + K - 1) / K : min(p.plan.seg_tiles, p.tiles - rank * p.plan.seg_tiles);
 
   constexpr int H = TMA ? 1 : S;
-  Two<T, PAIR> rx[H], rg[H], ri[H], rd[H];
+  Two<T, PAIR> rx[H] = {}, rg[H] = {}, ri[H] = {}, rd[H] = {};
   const T *const x = static_cast<const T *>(p.x) + b * p.sx[0] + c0;
   const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + c0;
   const T *const igate = IG ? static_cast<const T *>(p.igate) + b * p.si[0] + c0 : nullptr;
@@ -267,8 +268,10 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
     maps[buf][run][l] = make_ulonglong2(N, E);
     backs[buf][run][l] = R;
     if (turn + 1 < rounds) next = kept_of(turn + 1);
+    if (TMA && lane == 0) stores_read();
     __syncthreads();
-    // every warp is done with the tile before this one, whose place the next one takes
+    // every warp is done with the tile before this one, whose place the next one takes, and
+    // its gradients have left
     if (TMA && turn > 0 && turn + 1 < rounds) load(turn + 1);
     if constexpr (CL) {
       if (warp == 0) {
@@ -323,10 +326,6 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
       for (int j = 0; j < S; ++j)
         if (t0 + j >= p.tokens) h[j] = 0;
     }
-    if constexpr (TMA) {  // the rows before these have left
-      if (lane == 0) stores_read();
-      __syncwarp();
-    }
 #pragma unroll
     for (int k = S - G; k >= 0; k -= G) {
       f2 r[G], i[G], g[G];
@@ -355,10 +354,10 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
         const f2 gr = mul2(g[j], mul2(fma2(m, fma2(m, minus, both(-2.f)), both(1e-36f)), inv[k + j]));
         const f2 vx = mul2(gr, i[j]), vg = mul2(Gr, fma2(r[j], minus, one)), vi = mul2(mul2(gr, u), fma2(i[j], minus, one));
         if constexpr (TMA) {
-          const int row = half * S + k + j;
-          Two<T, PAIR>::store(&sm.out[warp][0][row][2 * l], upk(vx), true, true);
-          Two<T, PAIR>::store(&sm.out[warp][1][row][2 * l], upk(vg), true, true);
-          if constexpr (IG) Two<T, PAIR>::store(&sm.out[warp][2][row][2 * l], upk(vi), true, true);
+          const int row = run * S + k + j;
+          Two<T, PAIR>::store(&sm.rows[stage][0][row][2 * l], upk(vx), true, true);
+          Two<T, PAIR>::store(&sm.rows[stage][1][row][2 * l], upk(vg), true, true);
+          if constexpr (IG) Two<T, PAIR>::store(&sm.rows[stage][2][row][2 * l], upk(vi), true, true);
         } else if (t0 + k + j < p.tokens) {
           const long long t = t0 + k + j;
           if (dx) Two<T, PAIR>::store(dx + t * p.sdx[1], upk(vx), ok0, ok1);
@@ -371,9 +370,10 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
       fence_proxy_async();
       __syncwarp();
       if (lane == 0 && t0 < p.tokens) {
-        if (dx) store_rows(&tm.dx, sm.out[warp][0], ct * kGatedCh, t0, b);
-        if (dgate) store_rows(&tm.dgate, sm.out[warp][1], ct * kGatedCh, t0, b);
-        if (IG && digate) store_rows(&tm.digate, sm.out[warp][2], ct * kGatedCh, t0, b);
+        const int row = 2 * warp * S;
+        if (dx) store_rows(&tm.dx, sm.rows[stage][0][row], ct * kGatedCh, t0, b);
+        if (dgate) store_rows(&tm.dgate, sm.rows[stage][1][row], ct * kGatedCh, t0, b);
+        if (IG && digate) store_rows(&tm.digate, sm.rows[stage][2][row], ct * kGatedCh, t0, b);
         commit_stores();
       }
     }

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_maps_kernel(const _
   const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + me.c0;
   const T *const igate = IG ? static_cast<const T *>(p.igate) + b * p.si[0] + me.c0 : nullptr;
   const int first = (seg * kRuns + run) * p.plan.seg_tiles * kRun;
-  Two<T, PAIR> rx[kRun], rg[kRun], ri[kRun];
+  Two<T, PAIR> rx[kRun] = {}, rg[kRun] = {}, ri[kRun] = {};
   int ids = -1;
   auto load = [&](int t0) {
 #pragma unroll
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
 
   // rows: by TMA two tiles ahead, or into registers one tile ahead
   constexpr int H = TMA ? 1 : S;
-  Two<T, PAIR> rx[H], rg[H], ri[H];
+  Two<T, PAIR> rx[H] = {}, rg[H] = {}, ri[H] = {};
   const T *const x = static_cast<const T *>(p.x) + b * p.sx[0] + c0;
   const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + c0;
   const T *const igate = IG ? static_cast<const T *>(p.igate) + b * p.si[0] + c0 : nullptr;
@@ -601,23 +601,23 @@ cudaError_t pick(int rows, TensorMapEncode enc, const GatedScanParams &p, cudaSt
 
 }  // namespace
 
-#ifndef SS_SEG_CTAS
-#define SS_SEG_CTAS 304
-#endif
-#ifndef SS_SEG_ROUNDS
-#define SS_SEG_ROUNDS 4
-#endif
+// Clusters read everything once, but hold 8 CTAs at most: with fewer units than 32 they
+// leave SMs idle, and segments, which read the rows a second time, are faster from two
+// rounds of a cluster on (forward, us, clusters / segments):
+//   16 units, 1024 tiles 349 / 109     8 units, 64 tiles 12.4 / 7.6   11 units, 94 tiles, packed 25 / 14
+//   32 units, 256 tiles  50.2 / 53.8   48 units, 63 tiles 19 / 23     64 units, 128 tiles 38 / 54
+// 912 segments are what the SMs hold at once; a cluster's CTAs all have to run at once, too.
 GatedPlan gated_plan(long long units, int tiles) {
-  constexpr int kSms = 152, kResident = 4;  // CTAs of a cluster that an SM holds
+  constexpr int kSms = 152, kClusterResident = 4, kSegResident = 6;  // CTAs that an SM holds
   GatedPlan plan{1, 1, tiles};
   if (units < 1 || tiles < 2) return plan;
-  const long long k = std::min<long long>(std::min<long long>(kSms * kResident / units, kGatedMostCluster), tiles);
-  if (units * kGatedMostCluster < SS_SEG_CTAS && tiles > SS_SEG_ROUNDS * kGatedMostCluster) {
-    const long long segs = std::min<long long>(std::min<long long>((SS_SEG_CTAS + units - 1) / units, kGatedMostSegs), tiles);
+  if (units < 32 && tiles > 2 * kGatedMostCluster) {
+    const long long segs = std::min<long long>(std::min<long long>(kSms * kSegResident / units, kGatedMostSegs), tiles);
     plan.seg_tiles = (int)((tiles + segs - 1) / segs);
     plan.segs = (tiles + plan.seg_tiles - 1) / plan.seg_tiles;
     return plan;
   }
+  const long long k = std::min<long long>(std::min<long long>(kSms * kClusterResident / units, kGatedMostCluster), tiles);
   if (k > 1) plan.cluster = (int)k;
   return plan;
 }

@@ -88,8 +88,8 @@ struct NormParams {
   void *scale;      // (rows, groups)
   int groups;
 };
-cudaError_t launch_rms_norm(int dtype, int residual_dtype, bool vec, const NormParams &p, int sms, cudaStream_t s);
-cudaError_t launch_rms_norm_quant(int dtype, int residual_dtype, bool vec, const NormParams &p, int sms, cudaStream_t s);
+cudaError_t launch_rms_norm(int dtype, int residual_dtype, bool vec, const NormParams &p, cudaStream_t s);
+cudaError_t launch_rms_norm_quant(int dtype, int residual_dtype, bool vec, const NormParams &p, cudaStream_t s);
 
 struct NormBwdParams {
   long long rows;

@@ -15,13 +15,11 @@ constexpr int64_t kMaxUnits = int64_t(1) << 24;  // (sequence, channel tile) pai
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// SMs of the current device (0 on failure), whose context is made current: a thread's
-// first call (autograd runs backward passes on threads of its own) finds none, and
-// the tensor-map encoder wants one.
-int device_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
+// Makes the current device's context current: a thread's first call (autograd runs
+// backward passes on threads of its own) finds none, and the tensor-map encoder wants one.
+bool context_ready() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
 }
 
 // A (outer, rows, width) operand whose last stride is 1.
@@ -371,7 +369,7 @@ int ss_gated_scan(const ss_gated_scan_params *p, void *stream) {
   if (st != SS_OK) return st;
   if (p->batch == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
-  const bool ready = device_sms() > 0;
+  const bool ready = context_ready();
   const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedScanParams k{};
   k.err = ssk::packed_error_word();
@@ -412,7 +410,7 @@ int ss_gated_scan_bwd(const ss_gated_scan_bwd_params *p, void *stream) {
   if (launch_fault()) return SS_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p->batch == 0) return p->ddecay ? launched(cudaMemsetAsync(p->ddecay, 0, 4 * p->dim, s)) : SS_OK;
-  const bool ready = device_sms() > 0;
+  const bool ready = context_ready();
   const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedBwdParams k{};
   k.err = ssk::packed_error_word();
@@ -458,7 +456,7 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   const int64_t tokens = p->tables.tokens;
   if (tokens == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
-  const bool ready = device_sms() > 0;
+  const bool ready = context_ready();
   const ssk::TensorMapEncode enc = ssk::packed_map_encode();
   ssk::GatedScanParams k{};
   k.err = ssk::packed_error_word();
@@ -520,11 +518,9 @@ int ss_rms_norm(const ss_rms_norm_params *p, void *stream) {
   if (st != SS_OK) return st;
   if (p->rows == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
-  const int sms = device_sms();
-  if (!sms) return SS_ERR_CUDA;
   ssk::NormParams k = norm_params(p);
   k.rstd = p->rstd;
-  return launched(ssk::launch_rms_norm(p->dtype, p->residual_dtype, norm_vec(p, elem_size(p->dtype)), k, sms, static_cast<cudaStream_t>(stream)));
+  return launched(ssk::launch_rms_norm(p->dtype, p->residual_dtype, norm_vec(p, elem_size(p->dtype)), k, static_cast<cudaStream_t>(stream)));
 }
 
 int ss_rms_norm_bwd_validate(const ss_rms_norm_bwd_params *p) { return validate(p); }
@@ -568,14 +564,12 @@ int ss_rms_norm_quant(const ss_rms_norm_quant_params *p, void *stream) {
   if (st != SS_OK) return st;
   if (p->rows == 0) return SS_OK;
   if (launch_fault()) return SS_ERR_CUDA;
-  const int sms = device_sms();
-  if (!sms) return SS_ERR_CUDA;
   ssk::NormParams k = norm_params(p);
   k.group = (int)p->group;
   k.e8m0 = p->scale_type == SS_SCALE_E8M0;
   k.scale = p->scale;
   k.groups = (int)scale_groups(p);
-  return launched(ssk::launch_rms_norm_quant(p->dtype, p->residual_dtype, norm_vec(p, 1), k, sms, static_cast<cudaStream_t>(stream)));
+  return launched(ssk::launch_rms_norm_quant(p->dtype, p->residual_dtype, norm_vec(p, 1), k, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -5,108 +5,160 @@
 // to the workspace by CTA and a second launch adds them up: no atomics.
 #include "ss_norm.cuh"
 
+#ifndef SS_NB
+#define SS_NB 2
+#endif
+
 namespace ssk {
 namespace {
 
+// Up to 256 channels a warp takes a row, 8 values a lane.
+bool norm_bwd_cta_per_row(int dim) { return dim > 256; }
+
+constexpr int kKept = 8;  // values of a thread up to which it keeps the weight and takes the next row early
+
 template <typename T, typename R, int V, int N>
-__global__ void __launch_bounds__(1024) ss_rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p, bool cta) {
+__global__ void __launch_bounds__(norm_threads(N * V <= kKept)) ss_rms_norm_bwd_kernel(const __grid_constant__ NormBwdParams p, bool cta) {
+  constexpr bool KEEP = N * V <= kKept;
   __shared__ float sums[2][32];
   extern __shared__ float cols[];  // a warp per row: (warps, dim)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int me = cta ? threadIdx.x : lane, width = cta ? blockDim.x : 32;
   const long long first = cta ? blockIdx.x : (long long)blockIdx.x * warps + warp;
   const long long step = cta ? gridDim.x : (long long)gridDim.x * warps;
-  float dw[N][V], w[N][V];
+  const float inv_dim = __frcp_rn((float)p.dim);
+  int c[N];
+  bool in[N];
+  float dw[N][V], w[KEEP ? N : 1][V], next_rstd = 0.f;
+  Piece<T, V> nd[N];
+  Piece<R, V> ns[N], ne[KEEP ? N : 1];
+  auto load = [&](long long r) {
+    const T *dout = static_cast<const T *>(p.dout) + r * p.sd;
+    const R *sum = static_cast<const R *>(p.sum) + r * p.ss;
+    const R *dsum = p.dsum ? static_cast<const R *>(p.dsum) + r * p.sds : nullptr;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (in[k]) {
+        nd[k].load(dout + c[k]);
+        ns[k].load(sum + c[k]);
+        if constexpr (KEEP) {
+          if (dsum) ne[k].load(dsum + c[k]);
+        }
+      }
+    next_rstd = p.rstd[r];
+  };
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const int c = (k * width + me) * V;
+    c[k] = (k * width + me) * V;
+    in[k] = c[k] < p.dim;
+    nd[k].zero();
+    ns[k].zero();
 #pragma unroll
-    for (int i = 0; i < V; ++i) dw[k][i] = w[k][i] = 0.f;
-    if (c < p.dim) load_weight<T, V>(p.weight, p.weight_f32, c, w[k]);
+    for (int i = 0; i < V; ++i) dw[k][i] = 0.f;
+    if constexpr (KEEP) {
+      ne[k].zero();
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[k][i] = 0.f;
+      if (in[k]) load_weight<T, V>(p.weight, p.weight_f32, c[k], w[k]);
+    }
   }
+  if (KEEP && first < p.rows) load(first);
   int turn = 0;
   for (long long row = first; row < p.rows; row += step, turn ^= 1) {
-    const T *dout = static_cast<const T *>(p.dout) + row * p.sd;
-    const R *sum = static_cast<const R *>(p.sum) + row * p.ss;
-    const R *dsum = p.dsum ? static_cast<const R *>(p.dsum) + row * p.sds : nullptr;
-    const float rstd = p.rstd[row];
-    float d[N][V], n[N][V], e[N][V];
+    if constexpr (!KEEP) load(row);
+    const float rstd = next_rstd;
+    float d[N][V], n[N][V], e[KEEP ? N : 1][V];
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int c = (k * width + me) * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[k][i] = n[k][i] = e[k][i] = 0.f;
-      if (c < p.dim) {
-        load_vals<T, V>(dout + c, d[k]);
-        load_vals<R, V>(sum + c, n[k]);
-        if (dsum) load_vals<R, V>(dsum + c, e[k]);
-      }
+      nd[k].widen(d[k]);
+      ns[k].widen(n[k]);
+      if constexpr (KEEP) ne[k].widen(e[k]);
+    }
+    if constexpr (KEEP) {
+      if (row + step < p.rows) load(row + step);
     }
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+    for (int k = 0; k < N; ++k) {
+      float u[V] = {};
+      if constexpr (!KEEP) {
+        if (in[k]) load_weight<T, V>(again(p.weight), p.weight_f32, c[k], u);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         n[k][i] *= rstd;
         dw[k][i] = fmaf(d[k][i], n[k][i], dw[k][i]);
-        d[k][i] *= w[k][i];
+        d[k][i] *= KEEP ? w[KEEP ? k : 0][i] : u[i];
         dot = fmaf(d[k][i], n[k][i], dot);
       }
+    }
     // two places in turn: a row's sums are read before the row after the next writes its own
-    const float mean = __fdiv_rn(row_sum(dot, cta, sums[turn]), (float)p.dim);
+    const float mean = row_sum(dot, cta, sums[turn]) * inv_dim;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int c = (k * width + me) * V;
-      if (c >= p.dim) continue;
+      if (!in[k]) continue;
+      float v[V], f[V] = {};
+      if constexpr (!KEEP) {
+        if (p.dsum) {
+          Piece<R, V> q;
+          q.load(static_cast<const R *>(p.dsum) + row * p.sds + c[k]);
+          q.widen(f);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[k][i] = fmaf(rstd, fmaf(-n[k][i], mean, d[k][i]), e[k][i]);
-      if (p.dx) store_vals<T, V>(static_cast<T *>(p.dx) + row * p.sdx + c, d[k]);
-      if (p.dresidual) store_vals<R, V>(static_cast<R *>(p.dresidual) + row * p.sdr + c, d[k]);
+      for (int i = 0; i < V; ++i) v[i] = d[k][i] = fmaf(rstd, fmaf(-n[k][i], mean, d[k][i]), KEEP ? e[KEEP ? k : 0][i] : f[i]);
+      if (p.dx) {
+        Piece<T, V> o;
+        o.round(v);
+        o.store(static_cast<T *>(p.dx) + row * p.sdx + c[k]);
+      }
+      if (p.dresidual) {
+        Piece<R, V> o;
+        o.round(d[k]);
+        o.store(static_cast<R *>(p.dresidual) + row * p.sdr + c[k]);
+      }
     }
   }
   if (!p.parts) return;
   float *parts = p.parts + (long long)blockIdx.x * p.dim;
   if (cta) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int c = (k * width + me) * V;
-      if (c < p.dim)
+    for (int k = 0; k < N; ++k)
+      if (in[k])
 #pragma unroll
-        for (int i = 0; i < V; ++i) parts[c + i] = dw[k][i];
-    }
+        for (int i = 0; i < V; ++i) parts[c[k] + i] = dw[k][i];
   } else {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int c = (k * width + me) * V;
-      if (c < p.dim)
+    for (int k = 0; k < N; ++k)
+      if (in[k])
 #pragma unroll
-        for (int i = 0; i < V; ++i) cols[warp * p.dim + c + i] = dw[k][i];
-    }
+        for (int i = 0; i < V; ++i) cols[warp * p.dim + c[k] + i] = dw[k][i];
     __syncthreads();
-    for (int c = threadIdx.x; c < p.dim; c += blockDim.x) {
+    for (int k = threadIdx.x; k < p.dim; k += blockDim.x) {
       float s = 0.f;
-      for (int k = 0; k < warps; ++k) s += cols[k * p.dim + c];
-      parts[c] = s;
+      for (int u = 0; u < warps; ++u) s += cols[u * p.dim + k];
+      parts[k] = s;
     }
   }
 }
 
 // dweight: the sum over the parts.
 template <typename W>
-__global__ void __launch_bounds__(512) ss_rms_norm_dweight_kernel(const float *parts, int n, int dim, W *dweight) {
-  __shared__ float sums[16][32];
+__global__ void __launch_bounds__(1024) ss_rms_norm_dweight_kernel(const float *parts, int n, int dim, W *dweight) {
+  __shared__ float sums[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < dim)
-#pragma unroll 4
-    for (int k = warp; k < n; k += 16) s += parts[(long long)k * dim + c];
+  if (c < dim) {
+#pragma unroll 10
+    for (int k = warp; k < n; k += 32) s += parts[(long long)k * dim + c];
+  }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < dim) {
-    s = 0.f;
-    for (int w = 0; w < 16; ++w) s += sums[w][lane];
-    dweight[c] = from_f<W>(s);
-  }
+  // column `warp`: its 32 sums, one a lane
+  s = sums[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < dim) dweight[blockIdx.x * 32 + warp] = from_f<W>(s);
 }
 
 template <typename T, typename R, int V, int N>
@@ -116,49 +168,42 @@ cudaError_t launch(const NormBwdParams &p, const RowPlan &plan, cudaStream_t s) 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.dweight) return e;
   const int grid = (p.dim + 31) / 32;
-  if (p.weight_f32) ss_rms_norm_dweight_kernel<float><<<grid, 512, 0, s>>>(p.parts, p.ctas, p.dim, static_cast<float *>(p.dweight));
-  else ss_rms_norm_dweight_kernel<T><<<grid, 512, 0, s>>>(p.parts, p.ctas, p.dim, static_cast<T *>(p.dweight));
+  if (p.weight_f32) ss_rms_norm_dweight_kernel<float><<<grid, 1024, 0, s>>>(p.parts, p.ctas, p.dim, static_cast<float *>(p.dweight));
+  else ss_rms_norm_dweight_kernel<T><<<grid, 1024, 0, s>>>(p.parts, p.ctas, p.dim, static_cast<T *>(p.dweight));
   return cudaGetLastError();
+}
+template <typename T, typename R, int V>
+cudaError_t by_values(const NormBwdParams &p, const RowPlan &plan, cudaStream_t s) {
+  switch (plan.values) {
+    case 8: return launch<T, R, V, 8 / V>(p, plan, s);
+    case 16: return launch<T, R, V, 16 / V>(p, plan, s);
+    case 32: return launch<T, R, V, 32 / V>(p, plan, s);
+    case 64: return launch<T, R, V, 64 / V>(p, plan, s);
+  }
+  return cudaErrorInvalidValue;
 }
 template <typename T, typename R>
 cudaError_t pick(bool vec, const NormBwdParams &p, cudaStream_t s) {
   constexpr int V = sizeof(T) == 4 ? 4 : 8;
-  const int pieces = (p.dim + (vec ? V : 1) - 1) / (vec ? V : 1);
-  RowPlan plan;
-  auto spread = [&](int n) { plan.threads = ((pieces + n - 1) / n + 31) / 32 * 32; };
-  if (vec) {
-    plan.cta = pieces > 64;
-    plan.threads = 128;
-    plan.pieces = plan.cta ? (pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : pieces <= 4096 ? 4 : 8) : pieces <= 32 ? 1 : 2;
-    if (plan.cta) spread(plan.pieces);
-    switch (plan.pieces) {
-      case 1: return launch<T, R, V, 1>(p, plan, s);
-      case 2: return launch<T, R, V, 2>(p, plan, s);
-      case 4: return launch<T, R, V, 4>(p, plan, s);
-    }
-    if constexpr (V == 4) return launch<T, R, V, 8>(p, plan, s);
-    return cudaErrorInvalidValue;
-  }
-  plan.cta = pieces > 256;
-  plan.threads = 128;
-  plan.pieces = pieces <= 8192 ? 8 : 32;
-  if (plan.cta) spread(plan.pieces);
-  return plan.pieces == 8 ? launch<T, R, 1, 8>(p, plan, s) : launch<T, R, 1, 32>(p, plan, s);
+  const RowPlan plan = row_plan(p.dim, p.rows, vec ? V : 1, !norm_bwd_cta_per_row(p.dim), 8, kKept, p.ctas);
+  return vec ? by_values<T, R, V>(p, plan, s) : by_values<T, R, 1>(p, plan, s);
 }
 template <typename T>
 cudaError_t residual(int residual_dtype, bool vec, const NormBwdParams &p, cudaStream_t s) {
-  if constexpr (sizeof(T) == 2)
+  if constexpr (sizeof(T) == 2) {
     if (residual_dtype == 0) return pick<T, float>(vec, p, s);
+  }
   return pick<T, T>(vec, p, s);
 }
 
 }  // namespace
 
-// Each of 152 SMs four CTAs, as far as there are rows; a row's worth of dw per CTA is
-// what the second launch has to read.
+// Each SM two CTAs (of 320 threads at 2560 channels), four of them where a warp has a
+// row, as far as there are rows; a row's worth of dw per CTA is what the second launch has
+// to read.
 int norm_bwd_ctas(long long rows, int dim) {
-  const long long rows_at_once = dim <= 256 ? 4 : 1;
-  return (int)std::max<long long>(1, std::min<long long>((rows + rows_at_once - 1) / rows_at_once, 4 * 152));
+  const bool cta = norm_bwd_cta_per_row(dim);
+  return (int)std::max<long long>(1, std::min<long long>(cta ? rows : (rows + 3) / 4, (cta ? SS_NB : 4) * kNormSms));
 }
 
 cudaError_t launch_rms_norm_bwd(int dtype, int residual_dtype, bool vec, const NormBwdParams &p, cudaStream_t s) {
