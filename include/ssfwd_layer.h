@@ -15,7 +15,9 @@
  * The pages that the scan operators cite describe neither; formulas stand at each
  * declaration. Conventions are those of ssfwd.h: device pointers owned by the
  * caller, work enqueued on `stream`, nothing allocated, every check before
- * anything is enqueued, strides in elements. Statuses are ss_status.
+ * anything is enqueued, strides in elements. Statuses are ss_status. A wait of a kernel
+ * of the recurrence (for a copy, or for a CTA of its cluster) gives up after about a
+ * second, sets the error word of ss_device_error and runs on.
  */
 #ifndef SSFWD_LAYER_H_
 #define SSFWD_LAYER_H_
@@ -34,7 +36,9 @@ extern "C" {
  *     h = a * h + sqrt(1 - a^2) * i * x[t,c],   out[t,c] = h
  *
  * h starts from initial_state (zero when NULL) and is held in fp32; out is h
- * rounded once.
+ * rounded once. What a state loses is 2^-24 of the largest before it per token. decay
+ * is finite; a gate may be infinite (open or shut). A NaN, or an infinite state, is a
+ * NaN from its next token on, in its channel and sequence alone.
  *
  *   x, gate, input_gate, out  (batch, seqlen, dim) in dtype, dim stride 1; stride
  *                {batch, token}. input_gate may be NULL.

@@ -6,13 +6,18 @@
 // one that the forward kept before each tile of 64 tokens (1/32 of an operand in 16
 // bits), so that both recurrences are local to a tile but for e.
 //
-// Tiles, runs and clusters are the forward's, the tiles in falling order. A run's map
+// Tiles, runs, clusters and segments are the forward's, the tiles in falling order. A run's map
 // has three parts: N (both directions'), the forward's end and the backward's. Of a
 // token, n, the state before it and 1 / sqrt(1 - a^2) stay in registers; its gates are
 // taken again from the tile in shared memory for the gradients, which costs less than
 // registers that would halve the CTAs of an SM. The sum over tokens for the decay's
 // gradient stays in registers, then goes by CTA to the workspace and is added up by a
 // second launch: no atomics, the same result in every call.
+//
+// 8 x 2048 x 2560 bf16: 120 us, 4.9 TB/s (72% of the copy), five CTAs an SM, so that 640
+// run at once; with places of their own for the gradients (four an SM, two rounds) 142.
+// Bound by instruction issue: 130 a token and pair of channels, 18 of them on the
+// special-function unit.
 #include "ss_gated.cuh"
 
 namespace ssk {

@@ -8,20 +8,31 @@
 // shared memory; every run then starts from the tile's first state taken through the
 // maps before its own and goes over its 8 tokens once more. So inputs are read once and
 // the gates' arithmetic, which is most of the work, is spread over all warps, whatever
-// the chain. Where sequences and channels alone leave SMs idle, the CTAs of a cluster
-// take consecutive tiles and hand on their tiles' maps through distributed shared
-// memory: nothing is read twice, no workspace, and no wait on memory.
+// the chain. Tiles come and go by TMA, the loads two tiles ahead.
+//
+// Where sequences and channels alone leave SMs idle, the CTAs of a cluster take
+// consecutive tiles and send one another their tiles' maps (st.async, counted by the
+// receiver's mbarrier): nothing is read twice, no workspace, no wait on memory. Where
+// there are too few of them for that too, a first launch reduces segments of a sequence
+// to their maps, and the second starts each from those before it (gated_plan).
 //
 // A packed request's first token takes the request's start state in its b, and cuts:
 // what comes out of it does not depend on what came before, NaN or not. A map with a
 // cut in it has N = kCut.
+//
+// 8 x 2048 x 2560 bf16 64 us, 5.3 TB/s (78% of the copy); 65536 x 2048 in clusters 271
+// us, 4.0 TB/s; 16384 packed tokens x 2560 109 us. Bound by instruction issue (62 a
+// token and pair of channels, 0.6 of the issue rate at the 17 warps an SM that 640 CTAs
+// make): 32 for the gates, the sigmoids' and the root's 10 on the special-function unit
+// among them, 7 for the scan, 6 to widen 16 bits, the rest for tiles and maps. Tiles of 64
+// channels (320 CTAs, 2 or 3 an SM) 78 us; loads into registers instead of TMA (103
+// instructions, half of them for addresses and ends) 128.
 #include "ss_gated.cuh"
 
 namespace ssk {
 namespace {
 
 constexpr int kStages = 2;
-constexpr int kBuffers = 3;   // of maps: one is written while the one before is read, up to a barrier later
 constexpr int G = 4;          // tokens whose gates are taken side by side
 constexpr float kCut = 1.f;   // no decay's n, which lies in [-1, 0]
 
@@ -274,18 +285,17 @@ __global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_maps_kernel(const _
   }
 }
 
-// CL: a cluster's CTAs take consecutive tiles; a tile's output then waits until the next
-// tile's gates are done, so that the exchange is under way meanwhile.
+// CL: a cluster's CTAs take consecutive tiles.
 template <typename T, int ROWS, bool IG, bool PACKED, bool CL>
-__global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : sizeof(T) == 4 ? 4 : 6)
+__global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 6 : sizeof(T) == 4 ? 4 : 6)
     ss_gated_scan_kernel(const __grid_constant__ GatedScanParams p, const __grid_constant__ ScanMaps tm) {
   constexpr int S = kRun;
   constexpr bool TMA = ROWS == kTma, PAIR = ROWS != kSingles;
   extern __shared__ __align__(128) unsigned char dyn[];
   ScanSmem<T> &sm = *reinterpret_cast<ScanSmem<T> *>(dyn);
-  __shared__ ulonglong2 maps[kBuffers][kRuns][16];                         // (N, E) of the lane's channels, by run
-  __shared__ ulonglong2 tiles[CL ? kBuffers : 1][kGatedMostCluster][16];   // CL: the same by CTA
-  __shared__ uint64_t here[CL ? kBuffers : 1];                             // CL: the tiles' maps have come
+  __shared__ ulonglong2 maps[2][kRuns][16];                                // (N, E) of the lane's channels, by run
+  __shared__ ulonglong2 tiles[CL ? 2 : 1][kGatedMostCluster][16];          // CL: the same by CTA
+  __shared__ uint64_t here[2];                                             // CL: the tiles' maps have come
   __shared__ f2 carry[2][16];                                              // !CL: the state after a tile
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   // CL: a unit's CTAs are a cluster; else they have a segment each
@@ -338,12 +348,12 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
   auto of = [&](int slot) { return slot >= 0 ? pair_at(p.state + slot * p.state_stride) : PACKED && !CL && slot == kKept ? kept_start : 0; };
   Marks next{};  // of the next tile; ids: of the one after
   int ids = -1;
-  auto expect_maps = [&](int it) { mbar_arrive_expect_tx(&here[it % kBuffers], K * sizeof(tiles[0][0])); };
+  auto expect_maps = [&](int it) { mbar_arrive_expect_tx(&here[it & 1], K * sizeof(tiles[0][0])); };
   if constexpr (CL) {
     if (threadIdx.x == 0) {
-      for (int s = 0; s < kBuffers; ++s) mbar_init(&here[s], 1);
+      for (int s = 0; s < 2; ++s) mbar_init(&here[s], 1);
       fence_barrier_init();
-      for (int s = 0; s < kBuffers && s < rounds; ++s) expect_maps(s);
+      for (int s = 0; s < 2 && s < rounds; ++s) expect_maps(s);
     }
   }
   if constexpr (TMA) {
@@ -375,10 +385,10 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
       ulonglong2 m = make_ulonglong2(0, 0);
 #pragma unroll 4
       for (int k = from; k < to; ++k) m = then<PACKED>(m, seg[k * 16]);
-      maps[kBuffers - 1][run][l] = m;  // not written again before the third tile
+      maps[1][run][l] = m;  // not written again before the second tile
       __syncthreads();
 #pragma unroll
-      for (int r = 0; r < kRuns; ++r) h = through<PACKED>(maps[kBuffers - 1][r][l], h);
+      for (int r = 0; r < kRuns; ++r) h = through<PACKED>(maps[1][r][l], h);
     }
     if (threadIdx.x < 16) carry[1][l] = h;
     __syncthreads();
@@ -420,13 +430,13 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
     if constexpr (!TMA) {
       if (it + 1 < rounds) load(it + 1);
     }
-    maps[it % kBuffers][run][l] = run_map<PACKED>(make_ulonglong2(0, 0), now, n, e);
+    maps[it & 1][run][l] = run_map<PACKED>(make_ulonglong2(0, 0), now, n, e);
   };
   // the output of tile `it`, from the state before the CTA's tile
   auto finish = [&](int it, f2 v, const f2 *fn, const f2 *fe, const Marks &mk) {
     const int t0 = tile_of(it) * kGatedTile + run * S;
     if (p.kept && threadIdx.x < 16 && t0 < p.tokens) me.put_pair(p.kept + ((long long)b * p.tiles + tile_of(it)) * p.dim, v);
-    const auto &map = maps[it % kBuffers];
+    const auto &map = maps[it & 1];
 #pragma unroll
     for (int w = 0; w < kGatedWarps; ++w) {
       if (w < warp) v = through<PACKED>(map[2 * w + 1][l], through<PACKED>(map[2 * w][l], v));
@@ -471,68 +481,39 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 4 : siz
     return v;
   };
 
-  if constexpr (!CL) {
-    f2 n[S], e[S];
-    Marks now{};
-    for (int it = 0; it < rounds; ++it) {
-      gates(it, n, e, now);
-      __syncthreads();
-      if (TMA && it + kStages < rounds) load(it + kStages);
+  f2 n[S], e[S];
+  Marks now{};
+#pragma unroll 1
+  for (int it = 0; it < rounds; ++it) {
+    gates(it, n, e, now);
+    __syncthreads();
+    if (TMA && it + kStages < rounds) load(it + kStages);
+    if constexpr (!CL) {
       h = finish(it, carry[(it & 1) ^ 1][l], n, e, now);
       if (threadIdx.x >= kGatedThreads - 16) carry[it & 1][l] = h;
-    }
-    if (p.last && rank == share - 1 && threadIdx.x >= kGatedThreads - 16) me.put_pair(p.last + (long long)b * p.dim, h);
-  } else {
-    // the gates of tile `it`, and the output of the one before
-    auto turn = [&](int it, f2 *n, f2 *e, Marks &now, const f2 *pn, const f2 *pe, const Marks &past) {
-      if (it < rounds) {
-        gates(it, n, e, now);
-        __syncthreads();
-        if (TMA && it + kStages < rounds) load(it + kStages);
-      }
-      if (it > 0) {
-        fine = mbar_wait(&here[(it - 1) % kBuffers], ((it - 1) / kBuffers) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
-        if (threadIdx.x == 0 && it - 1 + kBuffers < rounds) expect_maps(it - 1 + kBuffers);
-      }
+    } else {
       // the whole tile's map, to every CTA, half of them from each half. The place that it
-      // takes there was read two turns before the maps that have just come were sent.
-      if (it < rounds && warp == 0) {
-        const auto &map = maps[it % kBuffers];
+      // takes there was read two rounds ago, before the maps of the last round were sent.
+      if (warp == 0) {
+        const auto &map = maps[it & 1];
         ulonglong2 all = map[0][l];
 #pragma unroll
         for (int r = 1; r < kRuns; ++r) all = then<PACKED>(all, map[r][l]);
-        for (int r = half; r < K; r += 2) send(&tiles[it % kBuffers][rank][l], &here[it % kBuffers], r, all);
+        for (int r = half; r < K; r += 2) send(&tiles[it & 1][rank][l], &here[it & 1], r, all);
       }
-      if (it > 0) {
-        f2 start = h;
-        for (int r = 0; r < K; ++r) {
-          if (r == rank) start = h;
-          h = through<PACKED>(tiles[(it - 1) % kBuffers][r][l], h);
-        }
-        finish(it - 1, start, pn, pe, past);
+      fine = mbar_wait(&here[it & 1], (it >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
+      if (threadIdx.x == 0 && it + 2 < rounds) expect_maps(it + 2);
+      f2 start = h;
+      for (int r = 0; r < K; ++r) {
+        if (r == rank) start = h;
+        h = through<PACKED>(tiles[it & 1][r][l], h);
       }
-    };
-    if constexpr (!PACKED) {
-      f2 n0[S], e0[S], n1[S], e1[S];
-      Marks m0{}, m1{};
-      for (int it = 0; it <= rounds; it += 2) {
-        turn(it, n0, e0, m0, n1, e1, m1);
-        if (it < rounds) turn(it + 1, n1, e1, m1, n0, e0, m0);
-      }
-    } else {  // one copy of the longer code: two do not fit the instruction cache (16384 x 2560: 107 us, 137 with two)
-      f2 n[S] = {}, e[S] = {}, pn[S], pe[S];
-      Marks now{}, past{};
-#pragma unroll 1
-      for (int it = 0; it <= rounds; ++it) {
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          pn[j] = n[j];
-          pe[j] = e[j];
-        }
-        past = now;
-        turn(it, n, e, now, pn, pe, past);
-      }
+      finish(it, start, n, e, now);
     }
+  }
+  if constexpr (!CL) {
+    if (p.last && rank == share - 1 && threadIdx.x >= kGatedThreads - 16) me.put_pair(p.last + (long long)b * p.dim, h);
+  } else {
     if (p.last && rank == 0 && threadIdx.x < 16) me.put_pair(p.last + (long long)b * p.dim, h);
     cluster_sync();  // nobody leaves while its shared memory is written to
   }
@@ -601,23 +582,29 @@ cudaError_t pick(int rows, TensorMapEncode enc, const GatedScanParams &p, cudaSt
 
 }  // namespace
 
-// Clusters read everything once, but hold 8 CTAs at most: with fewer units than 32 they
-// leave SMs idle, and segments, which read the rows a second time, are faster from two
-// rounds of a cluster on (forward, us, clusters / segments):
-//   16 units, 1024 tiles 349 / 109     8 units, 64 tiles 12.4 / 7.6   11 units, 94 tiles, packed 25 / 14
-//   32 units, 256 tiles  50.2 / 53.8   48 units, 63 tiles 19 / 23     64 units, 128 tiles 38 / 54
-// 912 segments are what the SMs hold at once; a cluster's CTAs all have to run at once, too.
-GatedPlan gated_plan(long long units, int tiles) {
-  constexpr int kSms = 152, kClusterResident = 4, kSegResident = 6;  // CTAs that an SM holds
+// Clusters read everything once, but have 8 CTAs at most (of 16, which not every device
+// runs, 32 units and fewer would gain, 64 and more lose); with few units they leave SMs
+// idle, and segments, which read the rows a second time, are faster from two rounds of a
+// cluster on. Forward / forward and backward in us, bf16:
+//                              clusters    segments
+//   11 units, 94 tiles, packed  25           14
+//   16 units, 1024 tiles       349 / 782    113 / 284
+//   32 units, 256 tiles         53 / 149     54 / 127
+//   48 units, 63 tiles          19 / 53      23 / 58
+//   64 units, 128 tiles         39 / 111     54 / 128
+// All CTAs of a cluster run at once: as many of them as leave all clusters resident.
+GatedPlan gated_plan(int dtype, long long units, int tiles) {
+  constexpr int kSms = 152, kSegCtas = 6;           // segments that an SM holds
+  const int kClusterCtas = dtype == 0 ? 3 : 5;      // CTAs of clusters that it holds, by shared memory
   GatedPlan plan{1, 1, tiles};
   if (units < 1 || tiles < 2) return plan;
-  if (units < 32 && tiles > 2 * kGatedMostCluster) {
-    const long long segs = std::min<long long>(std::min<long long>(kSms * kSegResident / units, kGatedMostSegs), tiles);
+  if (units < 40 && tiles > 2 * kGatedMostCluster) {
+    const long long segs = std::min<long long>(std::min<long long>(kSms * kSegCtas / units, kGatedMostSegs), tiles);
     plan.seg_tiles = (int)((tiles + segs - 1) / segs);
     plan.segs = (tiles + plan.seg_tiles - 1) / plan.seg_tiles;
     return plan;
   }
-  const long long k = std::min<long long>(std::min<long long>(kSms * kClusterResident / units, kGatedMostCluster), tiles);
+  const long long k = std::min<long long>(std::min<long long>(kSms * kClusterCtas / units, kGatedMostCluster), tiles);
   if (k > 1) plan.cluster = (int)k;
   return plan;
 }

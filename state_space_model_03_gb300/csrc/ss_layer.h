@@ -20,7 +20,7 @@ constexpr int kGatedMostSegs = 128;
 struct GatedPlan {
   int cluster, segs, seg_tiles;
 };
-GatedPlan gated_plan(long long units, int tiles);
+GatedPlan gated_plan(int dtype, long long units, int tiles);
 // Of each segment 16 lanes' maps (two pairs), and after all of these 16 lanes' start states.
 inline long long gated_map_bytes(long long units, const GatedPlan &plan) { return plan.segs > 1 ? units * plan.segs * 384 : 0; }
 

@@ -164,7 +164,7 @@ int validate_operands(const ss_gated_scan_bwd_params *p) {
 // backward the parts of ddecay by sequence and CTA.
 template <typename P>
 ssk::GatedPlan dense_plan(const P *p) {
-  return ssk::gated_plan(p->batch * up(p->dim, ssk::kGatedCh), (int)up(p->seqlen, ssk::kGatedTile));
+  return ssk::gated_plan(p->dtype, p->batch * up(p->dim, ssk::kGatedCh), (int)up(p->seqlen, ssk::kGatedTile));
 }
 int64_t workspace_of(const ss_gated_scan_params *p) {
   return ssk::gated_map_bytes(p->batch * up(p->dim, ssk::kGatedCh), dense_plan(p));
@@ -223,7 +223,7 @@ int validate_operands(const ss_packed_gated_scan_params *p) {
   return check_by_slot(p, p->tables.tokens, nullptr);
 }
 ssk::GatedPlan packed_plan(const ss_packed_gated_scan_params *p) {
-  return ssk::gated_plan(up(p->dim, ssk::kGatedCh), (int)up(p->tables.tokens, ssk::kGatedTile));
+  return ssk::gated_plan(p->dtype, up(p->dim, ssk::kGatedCh), (int)up(p->tables.tokens, ssk::kGatedTile));
 }
 int64_t workspace_of(const ss_packed_gated_scan_params *p) { return ssk::gated_map_bytes(up(p->dim, ssk::kGatedCh), packed_plan(p)); }
 int validate(const ss_packed_gated_scan_params *p) {

@@ -117,7 +117,7 @@ constexpr int kNormSms = 152;
 // to keep the weight and the next row beside them, else 512 with 128.
 constexpr int norm_threads(bool keeps) { return keeps ? 640 : 512; }
 // by_warp: a warp has a row; least: values of a thread to begin with; kept: up to which
-// the weight is kept; ctas: 0 for as many as 1024 threads an SM make.
+// the weight is kept; ctas: 0 for as many as 2048 threads an SM make.
 inline RowPlan row_plan(int dim, long long rows, int v, bool by_warp, int least, int kept, int ctas) {
   RowPlan plan{least, 128, ctas, !by_warp};
   if (plan.cta) {
@@ -126,7 +126,7 @@ inline RowPlan row_plan(int dim, long long rows, int v, bool by_warp, int least,
     plan.threads = ((accesses + n - 1) / n + 31) / 32 * 32;
   }
   const long long at_once = plan.cta ? 1 : plan.threads / 32;
-  if (!ctas) ctas = kNormSms * std::max(1, 1024 / plan.threads);
+  if (!ctas) ctas = kNormSms * std::max(1, 2048 / plan.threads);
   plan.ctas = (int)std::max<long long>(1, std::min<long long>((rows + at_once - 1) / at_once, ctas));
   return plan;
 }

@@ -682,12 +682,13 @@ def test_streams_and_repeats():
             assert torch.equal(a, b)
 
 
-def test_graphs_share_no_workspace():
+@pytest.mark.parametrize("lengths", [[40, 0, 25], [1500, 0, 900]])  # clusters; segments with a workspace
+def test_graphs_share_no_workspace(lengths):
     """Two captured graphs, replayed in turn with new inputs: serving, and a training step."""
-    lengths = [40, 0, 25]
+    n = sum(lengths)
     p, t, st = _packed_problem(lengths, 64, torch.bfloat16, seed=44, spare=0)
-    q = _norm_problem((65, 64), torch.bfloat16, "same", seed=45)
-    tables = ssm.request_tables(_i32(lengths), 65, **t)
+    q = _norm_problem((n, 64), torch.bfloat16, "same", seed=45)
+    tables = ssm.request_tables(_i32(lengths), n, **t)
     leaves = {k: v[None].clone().requires_grad_() if k != "decay" else v.clone().requires_grad_() for k, v in p.items()}
     norm = {k: v.clone().requires_grad_() for k, v in q.items()}
     dout = torch.ones_like(leaves["x"])
