@@ -51,21 +51,22 @@ __global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_bwd_maps_kernel(con
   const bool near = __all_sync(~0u, most.x >= -0.5f && most.y >= -0.5f);
   const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + c0;
   const T *const dout = static_cast<const T *>(p.dout) + b * p.sd[0] + c0;
-  const int first = (seg * kRuns + run) * p.plan.seg_tiles * kRun;
+  const int tokens = p.plan.seg_tiles * kGatedTile, end = min(p.tokens, (seg + 1) * tokens);
+  const int steps = (tokens + kGatedTile - 1) / kGatedTile, first = seg * tokens + run * steps * kRun;
   Two<T, PAIR> rg[kRun], rd[kRun];
   auto load = [&](int k) {
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       const long long t = first + k * kRun + j;
-      const bool in = t < p.tokens;
+      const bool in = t < end;
       rg[j].load(gate + t * p.sg[1], ok0 && in, ok1 && in);
       rd[j].load(dout + t * p.sd[1], ok0 && in, ok1 && in);
     }
   };
-  load(p.plan.seg_tiles - 1);
+  load(steps - 1);
   f2 N = 0, R = 0;
 #pragma unroll 1
-  for (int k = p.plan.seg_tiles - 1; k >= 0; --k) {
+  for (int k = steps - 1; k >= 0; --k) {
     f2 L[kRun], n[kRun], d[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_bwd_maps_kernel(con
     if (k > 0) load(k - 1);
     sigmoid2(L);
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) L[j] = first + k * kRun + j < p.tokens ? mul2(pk(most), L[j]) : 0;
+    for (int j = 0; j < kRun; ++j) L[j] = first + k * kRun + j < end ? mul2(pk(most), L[j]) : 0;
     decay2(L, near, n);
 #pragma unroll
     for (int j = kRun - 1; j >= 0; --j) {

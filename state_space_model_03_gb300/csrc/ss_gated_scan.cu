@@ -21,7 +21,7 @@
 // cut in it has N = kCut.
 //
 // 8 x 2048 x 2560 bf16 64 us, 5.3 TB/s (78% of the copy); 65536 x 2048 in clusters 271
-// us, 4.0 TB/s; 16384 packed tokens x 2560 109 us. Bound by instruction issue (62 a
+// us, 4.0 TB/s; 16384 packed tokens x 2560 107 us. Bound by instruction issue (62 a
 // token and pair of channels, 0.6 of the issue rate at the 17 warps an SM that 640 CTAs
 // make): 32 for the gates, the sigmoids' and the root's 10 on the special-function unit
 // among them, 7 for the scan, 6 to widen 16 bits, the rest for tiles and maps. Tiles of 64
@@ -95,6 +95,9 @@ struct Requests {
     return r >= 0 && p.context && p.context[r] > 0 ? slot_of(r) : -1;
   }
   __device__ __forceinline__ Marks marks(int ids) const {
+    // mostly all of a warp's tokens, and those beside them, are of one request
+    const int one = __shfl_sync(~0u, ids, 16 * half);
+    if (!__any_sync(~0u, one < 0 || (l < kRun + 2 && ids != one))) return Marks{0, 0, 0, -1, -1, false};
     const int before = __shfl_up_sync(~0u, ids, 1), after = __shfl_down_sync(~0u, ids, 1);
     const bool mine = l >= 1 && l <= kRun;
     const uint32_t first = __ballot_sync(~0u, mine && ids >= 0 && before != ids);
@@ -206,82 +209,74 @@ __device__ __forceinline__ f2 *segment_starts(const GatedScanParams &p, long lon
   return reinterpret_cast<f2 *>(segment_maps(p.maps, units, p.plan.segs, 0)) + (unit * p.plan.segs + seg) * 16;
 }
 
-// The maps of all segments but the last, and the start state of the last request that
-// starts in each: it may end in another segment, whose CTA then replaces it. Each half warp takes a part of the segment's
-// tokens that no other comes between.
+// The maps of all segments but the last: each half warp takes a part of the segment's
+// tokens that no other comes between. PACKED: only the request that goes on after the
+// segment has to be carried over its end, from its first token or the segment's; its
+// start state is kept besides, because the CTA of the segment that it ends in replaces it.
 template <typename T, bool PAIR, bool IG, bool PACKED>
 __global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_maps_kernel(const __grid_constant__ GatedScanParams p) {
   __shared__ ulonglong2 maps[kRuns][16];
-  __shared__ f2 starts[kRuns][16];
-  __shared__ int started[kRuns];
   let_next_start();
   const int segs = p.plan.segs - 1, seg = blockIdx.x % segs, unit = blockIdx.x / segs;
   const int ct = unit % p.channel_tiles, b = unit / p.channel_tiles;
   const Lane<PAIR> me(p, ct);
-  const int run = threadIdx.x >> 4;
-  const Requests req{p, me.l, me.half, -1};
-  auto of = [&](int slot) { return slot >= 0 ? me.pair_at(p.state + slot * p.state_stride) : 0; };
-  f2 latest = 0;  // PACKED: the start state of the last request that starts in the segment
-  bool any = false;
+  const int run = threadIdx.x >> 4, end = (seg + 1) * p.plan.seg_tiles * kGatedTile;
+  int begin = end - p.plan.seg_tiles * kGatedTile;
+  ulonglong2 m = make_ulonglong2(0, 0);
+  if constexpr (PACKED) {
+    const int r = p.token_request[end - 1];
+    bool starts = true;
+    f2 start = 0;
+    if (r < 0 || p.token_request[end] != r) {
+      begin = end;  // what follows starts by itself
+    } else if (p.offsets[r] >= begin) {
+      begin = p.offsets[r];
+      const int slot = p.state && p.context && p.context[r] > 0 ? p.slot_map[r] : -1;
+      if (slot >= 0 && slot < p.slots) start = me.pair_at(p.state + slot * p.state_stride);
+    } else {
+      starts = false;
+    }
+    if (starts && run == 0) m = make_ulonglong2(both(kCut), start);
+    if (threadIdx.x < 16) *(segment_starts(p, unit, seg) + me.l) = start;
+  }
   const T *const x = static_cast<const T *>(p.x) + b * p.sx[0] + me.c0;
   const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + me.c0;
   const T *const igate = IG ? static_cast<const T *>(p.igate) + b * p.si[0] + me.c0 : nullptr;
-  const int first = (seg * kRuns + run) * p.plan.seg_tiles * kRun;
+  const int steps = (end - begin + kGatedTile - 1) / kGatedTile, first = begin + run * steps * kRun;
   Two<T, PAIR> rx[kRun] = {}, rg[kRun] = {}, ri[kRun] = {};
-  int ids = -1;
   auto load = [&](int t0) {
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const bool in = t0 + j < p.tokens;
+      const bool in = t0 + j < end;
       const long long t = t0 + j;
       rx[j].load(x + t * p.sx[1], me.ok0 && in, me.ok1 && in);
       rg[j].load(gate + t * p.sg[1], me.ok0 && in, me.ok1 && in);
       if constexpr (IG) ri[j].load(igate + t * p.si[1], me.ok0 && in, me.ok1 && in);
     }
-    if constexpr (PACKED) ids = req.ids(t0);
   };
-  load(first);
-  ulonglong2 m = make_ulonglong2(0, 0);
+  if (steps > 0) load(first);
 #pragma unroll 1
-  for (int k = 0; k < p.plan.seg_tiles; ++k) {
+  for (int k = 0; k < steps; ++k) {
     const int t0 = first + k * kRun;
-    Marks marks{};
-    f2 start = 0, n[kRun], e[kRun];
-    if constexpr (PACKED) {
-      marks = req.marks(ids);
-      start = of(marks.from);
-    }
+    f2 n[kRun], e[kRun];
     run_gates<IG>(me.open, me.near, [&](int which, int j) { return which == 0 ? rx[j].widen() : which == 1 ? rg[j].widen() : ri[j].widen(); }, n, e);
-    if (k + 1 < p.plan.seg_tiles) load(t0 + kRun);
-    if constexpr (PACKED) {
-      if (marks.any) run_starts(req, marks, t0, start, of, n, e);
-      if (marks.first) {
-        latest = start;
-        any = true;
-      }
+    if (k + 1 < steps) load(t0 + kRun);
+    if (t0 + kRun > end) {
+#pragma unroll
+      for (int j = 0; j < kRun; ++j)
+        if (t0 + j >= end) n[j] = e[j] = 0;
     }
-    const ulonglong2 old = m;
-    m = run_map<PACKED>(m, marks, n, e);
-    if (PACKED && upk(old.x).x == kCut) m.x = both(kCut);
+    const bool cut = PACKED && upk(m.x).x == kCut;
+    m = run_map<false>(m, Marks{}, n, e);
+    if (cut) m.x = both(kCut);
   }
   maps[run][me.l] = m;
-  if constexpr (PACKED) {
-    starts[run][me.l] = latest;
-    if (me.l == 0) started[run] = any;
-  }
   __syncthreads();
   if (threadIdx.x < 16) {
     m = maps[0][me.l];
 #pragma unroll
     for (int r = 1; r < kRuns; ++r) m = then<PACKED>(m, maps[r][me.l]);
     *(segment_maps(p.maps, unit, p.plan.segs, seg) + me.l) = m;
-    if constexpr (PACKED) {
-      latest = 0;
-#pragma unroll
-      for (int r = 0; r < kRuns; ++r)
-        if (started[r]) latest = starts[r][me.l];
-      *(segment_starts(p, unit, seg) + me.l) = latest;
-    }
   }
 }
 
@@ -374,22 +369,6 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 6 : siz
   if constexpr (CL) {
     cluster_sync();  // every CTA's shared memory is there
   } else {
-    if (PACKED && share > 1) {
-      wait_for_previous();
-      if (rank < share - 1) kept_start = segment_starts(p, unit, rank)[l];
-    }
-    if (rank > 0) {  // the segments before this one: a part of them for each half warp
-      if constexpr (!PACKED) wait_for_previous();
-      const int per = (rank + kRuns - 1) / kRuns, from = run * per, to = min(rank, from + per);
-      const ulonglong2 *seg = segment_maps(p.maps, unit, p.plan.segs, 0) + l;
-      ulonglong2 m = make_ulonglong2(0, 0);
-#pragma unroll 4
-      for (int k = from; k < to; ++k) m = then<PACKED>(m, seg[k * 16]);
-      maps[1][run][l] = m;  // not written again before the second tile
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < kRuns; ++r) h = through<PACKED>(maps[1][r][l], h);
-    }
     if (threadIdx.x < 16) carry[1][l] = h;
     __syncthreads();
   }
@@ -481,12 +460,42 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 6 : siz
     return v;
   };
 
+  // !CL: what the launch before this one has left: the state that the segment starts from,
+  // through the maps of the segments before it, a part of them for each half warp
+  auto enter = [&] {
+    wait_for_previous();
+    if (PACKED && rank < share - 1) kept_start = segment_starts(p, unit, rank)[l];
+    const int per = (rank + kRuns - 1) / kRuns, from = run * per, to = min(rank, from + per);
+    const ulonglong2 *seg = segment_maps(p.maps, unit, p.plan.segs, 0) + l;
+    ulonglong2 m = make_ulonglong2(0, 0);
+#pragma unroll 4
+    for (int k = from; k < to; ++k) m = then<PACKED>(m, seg[k * 16]);
+    maps[1][run][l] = m;  // not written again before the second tile
+    __syncthreads();
+    if (threadIdx.x < 16) {
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r) h = through<PACKED>(maps[1][r][l], h);
+      carry[1][l] = h;
+    }
+    __syncthreads();
+  };
+  // after the first tile's gates, unless a request starts there from what is left
+  bool entered = CL || share == 1 || (!PACKED && rank == 0);
+  if (PACKED && !entered && over >= 0 && p.offsets[over] < (tile_of(0) + 1) * kGatedTile) {
+    enter();
+    entered = true;
+  }
   f2 n[S], e[S];
   Marks now{};
 #pragma unroll 1
   for (int it = 0; it < rounds; ++it) {
     gates(it, n, e, now);
-    __syncthreads();
+    if (!CL && !entered) {
+      enter();
+      entered = true;
+    } else {
+      __syncthreads();
+    }
     if (TMA && it + kStages < rounds) load(it + kStages);
     if constexpr (!CL) {
       h = finish(it, carry[(it & 1) ^ 1][l], n, e, now);
@@ -587,7 +596,7 @@ cudaError_t pick(int rows, TensorMapEncode enc, const GatedScanParams &p, cudaSt
 // idle, and segments, which read the rows a second time, are faster from two rounds of a
 // cluster on. Forward / forward and backward in us, bf16:
 //                              clusters    segments
-//   11 units, 94 tiles, packed  25           14
+//   11 units, 94 tiles, packed  25           13
 //   16 units, 1024 tiles       349 / 782    113 / 284
 //   32 units, 256 tiles         53 / 149     54 / 127
 //   48 units, 63 tiles          19 / 53      23 / 58

@@ -39,7 +39,7 @@ struct GatedScanParams {
   float *kept;  // (batch, tiles, dim) or NULL
   long long sx[2], sg[2], si[2], so[2];  // sequence, token
   // packed requests (token_request given): one sequence, states by slot
-  const int32_t *token_request, *slot_map, *context;
+  const int32_t *token_request, *offsets, *slot_map, *context;
   float *state;
   long long slots, state_stride;
 };

@@ -474,6 +474,7 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream) {
   k.plan = packed_plan(p);
   k.maps = p->workspace;
   k.token_request = p->tables.token_request;
+  k.offsets = p->tables.offsets;
   k.slot_map = p->tables.slot_map;
   k.context = p->tables.context;
   k.state = p->state;
