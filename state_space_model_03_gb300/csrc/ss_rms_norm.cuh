@@ -8,7 +8,7 @@
 // lanes that hold it, its bits as integers, so that a NaN is the largest of all.
 //
 // 16384 x 2560 bf16 with the residual in fp32: 78 us, 6.5 TB/s (95% of the copy); 16384 x
-// 5120 bf16 in 8 bits, a scale of each 32 channels: 109 us, 5.4 TB/s. A quotient by
+// 5120 bf16 in 8 bits, a scale of each 32 channels: 95 us, 6.2 TB/s (92%). A quotient by
 // division took 139 instead (380 instructions for 8 values). CTAs that make 2048 threads
 // an SM 181 us for norm and backward, 1024 187, 640 185.
 #include <cuda_fp8.h>
@@ -18,21 +18,35 @@
 namespace ssk {
 namespace {
 
-// The scale of a group with `most` as its largest, and its reciprocal.
-__device__ __forceinline__ float scale_of(float most, bool e8m0, uint8_t &byte, float &inverse) {
-  float s = __fdiv_rn(most, 448.f);
-  s = isnan(s) ? s : fmaxf(s, 1.17549435e-38f);
-  if (e8m0) {  // the least power of two not below it
-    uint32_t w = __float_as_uint(s);
-    if (isnan(s)) {
-      byte = 255;
-    } else {
-      w = (w + 0x7fffffu) & 0x7f800000u;
-      byte = (uint8_t)(w >> 23);
-      s = __uint_as_float(w);
-    }
+// The larger of two absolute values; a NaN where one is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+// The scale of a group with `most` as its largest (NaN: it has one), and its reciprocal.
+// The least power of two not below most / 448 = most / (1.75 2^8): its exponent is most's
+// less 8, and one more where most's fraction is above 1.75; at least 2^-126.
+struct Scale {
+  float scale, inverse;
+  uint8_t byte;
+};
+__device__ __forceinline__ Scale scale_of(float most, bool e8m0) {
+  Scale s;
+  if (e8m0) {
+    const uint32_t w = __float_as_uint(most);
+    const uint32_t p = max((w + 0x1fffffu) >> 23, 9u) - 8;
+    const bool fine = w < 0x7f800000u;
+    s.byte = fine ? p : 255;
+    s.scale = 0.f;
+    s.inverse = __uint_as_float(fine ? (254 - p) << 23 : 0x7fffffffu);
+  } else {
+    s.scale = most * (1.f / 448.f);
+    if (s.scale < 1.17549435e-38f) s.scale = 1.17549435e-38f;
+    s.inverse = __frcp_rn(s.scale);
+    s.byte = 0;
   }
-  inverse = __frcp_rn(s);
   return s;
 }
 
@@ -42,14 +56,14 @@ template <typename T, typename R, bool RES, int V, int N, bool QUANT>
 __global__ void __launch_bounds__(norm_threads(N * V <= kKept)) ss_rms_norm_kernel(const __grid_constant__ NormParams p, bool cta) {
   constexpr bool KEEP = N * V <= kKept;
   __shared__ float sums[2][32];
-  extern __shared__ uint32_t most[];  // QUANT: largest values, by warp or by group
+  extern __shared__ float most[];  // QUANT: largest values, by warp or by group
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int me = cta ? threadIdx.x : lane, width = cta ? blockDim.x : 32;
   const long long step = cta ? gridDim.x : (long long)gridDim.x * warps;
   long long row = cta ? blockIdx.x : (long long)blockIdx.x * warps + warp;
   if (row >= p.rows) return;  // the whole CTA, or a warp of one whose warps have rows of their own
   const float inv_dim = __frcp_rn((float)p.dim);
-  int c[N];
+  int c[N], group[N];  // first channel, and QUANT its group
   bool in[N];
   float w[KEEP ? N : 1][V];
   Piece<T, V> nx[N];
@@ -68,6 +82,7 @@ __global__ void __launch_bounds__(norm_threads(N * V <= kKept)) ss_rms_norm_kern
   for (int k = 0; k < N; ++k) {
     c[k] = (k * width + me) * V;
     in[k] = c[k] < p.dim;
+    group[k] = QUANT && p.group > 0 ? c[k] / p.group : 0;
     nx[k].zero();
     if constexpr (RES) nr[k].zero();
     if constexpr (KEEP) {
@@ -127,62 +142,69 @@ __global__ void __launch_bounds__(norm_threads(N * V <= kKept)) ss_rms_norm_kern
           o.store(out + c[k]);
         }
     } else {
-      uint32_t m[N];
+      float m[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        m[k] = 0;
+        m[k] = fabsf(v[k][0]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) m[k] = max(m[k], __float_as_uint(v[k][i]) & 0x7fffffffu);
+        for (int i = 1; i < V; ++i) m[k] = larger(m[k], v[k][i]);
       }
-      const int lanes = p.group / V;  // that share a group, where it is part of a warp's access
-      if (p.group > 0 && lanes <= 32) {
+      auto over = [&](int lanes) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           if (o >= lanes) break;
 #pragma unroll
-          for (int k = 0; k < N; ++k) m[k] = max(m[k], __shfl_xor_sync(~0u, m[k], o));
+          for (int k = 0; k < N; ++k) m[k] = larger(m[k], __shfl_xor_sync(~0u, m[k], o));
         }
+      };
+      const int lanes = p.group / V;  // that share a group, where it is part of a warp's access
+      if (p.group > 0 && lanes <= 32) {
+        over(lanes);
       } else if (p.group == 0) {
 #pragma unroll
-        for (int k = 1; k < N; ++k) m[0] = max(m[0], m[k]);
-        m[0] = __reduce_max_sync(~0u, m[0]);
+        for (int k = 1; k < N; ++k) m[0] = larger(m[0], m[k]);
+        over(32);
         if (cta) {
           if (lane == 0) most[32 * turn + warp] = m[0];
           __syncthreads();
-          m[0] = __reduce_max_sync(~0u, lane < warps ? most[32 * turn + lane] : 0u);
+          m[0] = lane < warps ? most[32 * turn + lane] : 0.f;
+          over(32);
         }
 #pragma unroll
         for (int k = 1; k < N; ++k) m[k] = m[0];
-      } else {  // single values, groups of two or four warps' accesses
-        uint32_t *mine = most + (cta ? 0 : warp * p.groups);
+      } else {  // single values, groups of two or four warps' accesses: what the warps of a group have
+        over(32);
+        float *mine = most + (cta ? 0 : warp * 4 * p.groups);
+        const int per = p.group / 32;
         if (cta) __syncthreads();  // the row before has read them
         __syncwarp();
-        for (int g = me; g < p.groups; g += width) mine[g] = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (lane == 0 && c[k] < p.dim) mine[c[k] / 32] = m[k];
         if (cta) __syncthreads();
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          const uint32_t q = __reduce_max_sync(~0u, m[k]);
-          const int first = k * width + (me & ~31);
-          if (lane == 0 && first < p.dim) atomicMax(&mine[first / p.group], q);
+          m[k] = 0.f;
+          if (in[k])
+            for (int q = 0; q < per; ++q) {
+              const int at = group[k] * per + q;
+              if (at * 32 < p.dim) m[k] = larger(m[k], mine[at]);
+            }
         }
-        if (cta) __syncthreads();
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < N; ++k) m[k] = in[k] ? mine[c[k] / p.group] : 0;
       }
       uint8_t *out = static_cast<uint8_t *>(p.out) + row * p.so;
-      float scale = 0.f, inverse = 0.f;
-      uint8_t byte = 0;
+      Scale scale{};
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        if (k == 0 || p.group > 0) scale = scale_of(__uint_as_float(m[k]), p.e8m0, byte, inverse);
+        if (k == 0 || p.group > 0) scale = scale_of(m[k], p.e8m0);
         if (!in[k]) continue;
-        if (p.group > 0 ? (c[k] & (p.group - 1)) == 0 : c[k] == 0) {
-          const long long at = row * p.groups + (p.group > 0 ? c[k] / p.group : 0);
-          if (p.e8m0) static_cast<uint8_t *>(p.scale)[at] = byte;
-          else static_cast<float *>(p.scale)[at] = scale;
+        if ((c[k] & (p.group - 1)) == 0 && (p.group > 0 || c[k] == 0)) {
+          const long long at = row * p.groups + group[k];
+          if (p.e8m0) static_cast<uint8_t *>(p.scale)[at] = scale.byte;
+          else static_cast<float *>(p.scale)[at] = scale.scale;
         }
+        const float inverse = scale.inverse;
         // by the reciprocal, exact for a power of two; else within 2^-23 of the quotient
         if constexpr (V == 1) {
           out[c[k]] = __nv_cvt_float_to_fp8(v[k][0] * inverse, __NV_SATFINITE, __NV_E4M3);
@@ -207,7 +229,8 @@ __global__ void __launch_bounds__(norm_threads(N * V <= kKept)) ss_rms_norm_kern
 
 template <typename T, typename R, bool RES, int V, int N, bool QUANT>
 cudaError_t launch(const NormParams &p, const RowPlan &plan, cudaStream_t s) {
-  const int smem = QUANT ? 4 * std::max(64, p.groups * (plan.cta ? 1 : plan.threads / 32)) : 0;
+  // largest values: two rows' by warp; or by 32 channels
+  const int smem = QUANT ? 4 * std::max(64, 4 * p.groups * (plan.cta ? 1 : plan.threads / 32)) : 0;
   ss_rms_norm_kernel<T, R, RES, V, N, QUANT><<<plan.ctas, plan.threads, smem, s>>>(p, plan.cta);
   return cudaGetLastError();
 }
@@ -224,9 +247,10 @@ cudaError_t by_values(const NormParams &p, const RowPlan &plan, cudaStream_t s) 
 template <typename T, typename R, bool RES, bool QUANT>
 cudaError_t pick(bool vec, const NormParams &p, cudaStream_t s) {
   constexpr int V = sizeof(T) == 4 ? 4 : 8;
-  // few rows: a CTA for each, 8 values a thread; else a warp for short ones, and 16 values
-  const bool few = p.rows < 4 * kNormSms, by_warp = p.dim <= (few ? 256 : 512);
-  const RowPlan plan = row_plan(p.dim, p.rows, vec ? V : 1, by_warp, by_warp ? (p.dim <= 256 ? 8 : 16) : few ? 8 : 16, kKept, 0);
+  // few rows, or single values: a CTA for each, 8 values a thread; else a warp for short
+  // ones, and 16 values
+  const bool fine = !vec || p.rows < 4 * kNormSms, by_warp = p.dim <= (fine ? 256 : 512);
+  const RowPlan plan = row_plan(p.dim, p.rows, vec ? V : 1, by_warp, p.dim <= 256 || fine ? 8 : 16, kKept, 0);
   return vec ? by_values<T, R, RES, V, QUANT>(p, plan, s) : by_values<T, R, RES, 1, QUANT>(p, plan, s);
 }
 template <typename T, bool QUANT>
