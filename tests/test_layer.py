@@ -168,6 +168,28 @@ def test_scan_strides(dtype):
     _close(leaf.grad, oracle.gated_scan_bwd(torch.ones_like(gate), None, x, gate, decay)["gate"], GTOL[dtype])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,d", [(200, 64), (1200, 48)])  # clusters; segments
+def test_scan_of_rows_that_share_memory(dtype, n, d):
+    """Tokens of one row, windows of one buffer that overlap, a gradient that all tokens share, one tensor as x and gate."""
+    b = 2
+    g = _gen(11)
+    decay = _decay(g, d)
+    rest = {k: _rand(g, b, n, d, dtype=dtype) for k in ("gate", "input_gate")}
+    buffer = _rand(g, (n + 8) * d + 64, dtype=dtype)
+    for name, x in (("one row", buffer[:d].expand(b, n, d)), ("rows", buffer.as_strided((b, n, d), (8 * d, 16, 1))),
+                    ("sequences", buffer.as_strided((b, n, d), (8 * d, d, 1))), ("channels", buffer.as_strided((b, n, d), (16, d, 1)))):
+        want, _ = oracle.gated_scan(x, decay=decay, **rest)
+        _close(ssm.gated_scan_fn(x, decay=decay, **rest), want, TOL[dtype], name)
+        gate = rest["gate"].clone().requires_grad_()
+        dout = x[:, :1].expand(b, n, d)
+        got, = torch.autograd.grad(ssm.gated_scan_fn(x, gate, decay, rest["input_gate"]), [gate], dout)
+        _close(got, oracle.gated_scan_bwd(dout, None, x, decay=decay, **rest)["gate"], GTOL[dtype], name)
+    x = rest["gate"]
+    want, _ = oracle.gated_scan(x, x, decay, x)
+    _close(ssm.gated_scan_fn(x, x, decay, x), want, TOL[dtype])
+
+
 def test_far_offsets():
     """Rows past 2^31 elements, and past 2^31 bytes of a smaller tensor."""
     n, d = 70, 64
@@ -490,6 +512,25 @@ def test_norm_gradients_of_parts():
     ds, dw = oracle.rms_norm_bwd(dout, None, torch.zeros_like(p["x"]), p["weight"], s.detach())
     _close(got[0], ds, GTOL[torch.float32])
     _close(got[1], dw, GTOL[torch.float32])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_of_broadcast_gradients_and_of_one_tensor_twice(dtype):
+    """A gradient that all rows share, one for all of the output, and a tensor that is its own residual."""
+    p = _norm_problem((37, 520), dtype, "none", seed=36)
+    row = _rand(_gen(37), 520, dtype=dtype)
+    for dout in (row.expand(37, 520), row[:1].expand(37, 520)):
+        leaves = {k: v.clone().requires_grad_() for k, v in p.items() if v is not None}
+        grads = torch.autograd.grad(ssm.rms_norm_fn(**leaves), list(leaves.values()), dout)
+        ds, dw = oracle.rms_norm_bwd(dout, None, p["x"], p["weight"])
+        _close(grads[0], ds, GTOL[dtype])
+        _close(grads[1], dw, GTOL[torch.float32])
+    # x + x is exact, and so is the sum of the two gradients, which are the same
+    x = p["x"].clone().requires_grad_()
+    dout = _rand(_gen(38), 37, 520, dtype=dtype)
+    got, = torch.autograd.grad(ssm.rms_norm_fn(x, p["weight"], residual=x), [x], dout)
+    ds, _ = oracle.rms_norm_bwd(dout, None, 2 * p["x"].double(), p["weight"])
+    _close(got, 2 * ds, GTOL[dtype])
 
 
 @pytest.mark.parametrize("dtype", TYPES)
