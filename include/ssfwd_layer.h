@@ -226,8 +226,10 @@ int ss_rms_norm_bwd(const ss_rms_norm_bwd_params *p, void *stream);
  *     scale = the least power of two not below that   (SS_SCALE_E8M0)
  *     out = v / scale rounded to nearest even, so that v is about out * scale
  *
- * A group with a NaN has scale NaN and is NaN throughout; a row with an infinity has
- * NaN in its place and zeros beside it.
+ * The quotient is v times the scale's reciprocal: exact for a power of two, within 2^-23
+ * of it for an fp32 scale, which itself is most times the nearest fp32 to 1/448. A group
+ * with a NaN has scale NaN and is NaN throughout; so has the group of an infinity, beside
+ * which its row's groups are zeros.
  *
  *   out          (rows, dim) bytes, dim stride 1.
  *   scale        (rows, ceil(dim / group)) fp32, or bytes of e8m0; contiguous.

@@ -591,9 +591,10 @@ cudaError_t pick(int rows, TensorMapEncode enc, const GatedScanParams &p, cudaSt
 
 }  // namespace
 
-// Clusters read everything once, but have 8 CTAs at most (of 16, which not every device
-// runs, 32 units and fewer would gain, 64 and more lose); with few units they leave SMs
-// idle, and segments, which read the rows a second time, are faster from two rounds of a
+// Clusters read everything once, but have 8 CTAs at most. Wider ones, which not every
+// device runs, gain forward where sequences are long (64 units of 1024 tiles 252 us
+// instead of 271) and lose in shorter ones (48 units of 63 tiles 28 instead of 19) and
+// backward (64 units of 128 tiles 129 instead of 111). With few units they leave SMs idle, and segments, which read the rows a second time, are faster from two rounds of a
 // cluster on. Forward / forward and backward in us, bf16:
 //                              clusters    segments
 //   11 units, 94 tiles, packed  25           13

@@ -2,7 +2,7 @@
 //   h = h + (n h + b),  n = a - 1, b = sqrt(1 - a^2) sigmoid(input_gate) x,  out = h.
 // Bound by the traffic of the fp32 states, read and written once, and of the rows
 // beside them. A thread has V neighbouring channels, whose decay it takes once, of
-// up to kRows rows. 512 x 5120 bf16: 8.8 us in a graph, 4.8 TB/s; 4 x 2560 3.5.
+// up to kRows rows. 512 x 5120 bf16: 8.3 us in a graph, 5.1 TB/s; 4 x 2560 3.2.
 #include "ss_gated.cuh"
 
 namespace ssk {

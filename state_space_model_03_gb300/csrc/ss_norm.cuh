@@ -1,6 +1,6 @@
 // What the kernels of the root-mean-square norm share: a row's values by thread.
 //
-// A row is a warp's (G of them in a CTA), or a CTA's; a thread has N accesses of V
+// A row is a warp's (a CTA's warps have rows of their own), or a CTA's; a thread has N accesses of V
 // values of it, always the same columns, and goes from row to row with the weight in
 // registers and the next row's values on their way while it works on this one's.
 #pragma once
