@@ -75,7 +75,7 @@ void no_grad(std::initializer_list<const at::Tensor *> ts) {
   const bool backward = c10::GradMode::is_enabled();
   for (const at::Tensor *t : ts)
     if (t && ((backward && t->requires_grad()) || t->_fw_grad(0).defined()))
-      refuse(PyExc_NotImplementedError, "the packed operators are forward only: no gradients and no tangents");
+      refuse(PyExc_NotImplementedError, "this operator is forward only: no gradients and no tangents");
 }
 // A cache was updated in place: what autograd has saved of it is known to be old.
 void changed(const at::Tensor *t) {

@@ -10,7 +10,9 @@ Rows have their channels last, as projections leave them.
 
 As in packed.py this is argument marshalling only, on the current stream, and there
 is no CPU fallback. ``gated_scan_fn`` and ``rms_norm_fn`` are differentiable (once);
-the others are forward only and refuse inputs that require a gradient.
+the others are forward only and refuse inputs that require a gradient. A training step
+is captured into a CUDA graph as with any of torch's operators: with no eager graph of
+the same leaves alive, whose gradients torch accumulates on that graph's stream.
 """
 from __future__ import annotations
 

@@ -723,6 +723,32 @@ def test_streams_and_repeats():
             assert torch.equal(a, b)
 
 
+def test_calls_at_once():
+    """Two streams at the same time, each in clusters and in segments with a workspace, forward and backward."""
+    problems = [[_scan_problem(shape, torch.bfloat16, seed=60 + i) for shape in ((2, 700, 640), (1, 5000, 64))] for i in range(2)]
+
+    def work(ps):
+        got = []
+        for p in ps:
+            leaves = {k: v.detach().requires_grad_() for k, v in p.items()}
+            out = ssm.gated_scan_fn(**leaves)
+            got += [out.detach(), *torch.autograd.grad(out, list(leaves.values()), torch.ones_like(out))]
+        return got
+
+    want = [work(ps) for ps in problems]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in problems]
+    got = []
+    for _ in range(20):
+        for s, ps in zip(streams, problems):
+            with torch.cuda.stream(s):
+                got.append(work(ps))
+    torch.cuda.synchronize()
+    for i, run in enumerate(got):
+        for a, b in zip(run, want[i % 2]):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("lengths", [[40, 0, 25], [1500, 0, 900]])  # clusters; segments with a workspace
 def test_graphs_share_no_workspace(lengths):
     """Two captured graphs, replayed in turn with new inputs: serving, and a training step."""
@@ -828,7 +854,7 @@ def test_refusals():
         ssm.rms_norm_fn(p["x"], w, eps=-1.0)
     with pytest.raises(ssm_error()):
         ssm.rms_norm_fn(torch.zeros(1, 32769, device="cuda"), torch.ones(32769, device="cuda"))
-    with pytest.raises(NotImplementedError):
+    with pytest.raises(NotImplementedError, match="this operator is forward only"):
         ssm.rms_norm_quant_fn(p["x"], w.clone().requires_grad_())
     with pytest.raises(ValueError, match="group_size"):
         ssm.rms_norm_quant_fn(p["x"], w, group_size=16)
