@@ -162,6 +162,21 @@ __device__ __forceinline__ void send(ulonglong2 *p, uint64_t *bar, int rank, ulo
                "l"(v.x), "l"(v.y), "r"(remote_of(bar, rank))
                : "memory");
 }
+// mbar_wait for what others have sent: it acquires at the scope that their stores'
+// arrivals release at, which mbar_wait, of a CTA's own copies, does not.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, int32_t *err, int32_t code, uint32_t limit) {
+  for (uint32_t i = 0; i < limit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs) : "memory");
+    if (ok) return true;
+  }
+  atomicCAS(err, 0, code);
+  return false;
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {

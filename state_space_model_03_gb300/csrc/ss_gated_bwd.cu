@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
         // its place there was read in the turn before the last, and every CTA has begun the last one
         for (int r = half; r < K; r += 2) send(&tiles[buf][rank][l], &here[buf], r, all);
       }
-      fine = mbar_wait(&here[buf], (turn >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
+      fine = mbar_wait_cluster(&here[buf], (turn >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
       if (threadIdx.x == 0 && turn + 2 < rounds) expect_maps(turn + 2);
       for (int c = K - 1; c >= 0; --c) {
         if (c == rank) e = back;

@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 6 : siz
         for (int r = 1; r < kRuns; ++r) all = then<PACKED>(all, map[r][l]);
         for (int r = half; r < K; r += 2) send(&tiles[it & 1][rank][l], &here[it & 1], r, all);
       }
-      fine = mbar_wait(&here[it & 1], (it >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
+      fine = mbar_wait_cluster(&here[it & 1], (it >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
       if (threadIdx.x == 0 && it + 2 < rounds) expect_maps(it + 2);
       f2 start = h;
       for (int r = 0; r < K; ++r) {
