@@ -67,14 +67,15 @@ bool pairs(std::initializer_list<Rows> all, int64_t dim) {
     if (r.ptr && (!aligned(r.ptr, 2 * r.es) || (r.rows > 1 && r.stride[1] % 2) || (r.outer > 1 && r.stride[0] % 2))) return false;
   return true;
 }
-// How the recurrence's rows come and go: by TMA where every row starts on 16 bytes and
-// ends before the next (rows that are broadcast or windows of one buffer do not: a tensor
+// How the recurrence's rows come and go: by TMA where every row is whole pieces of 16
+// bytes (a store writes the last one to its end, whatever of it is the row's) and ends
+// before the next (rows that are broadcast or windows of one buffer do not: a tensor
 // map's strides are those of whole rows), else in pairs or single values.
 int rows_kind(std::initializer_list<Rows> all, int64_t dim) {
   auto off = [](int64_t bytes, int64_t row) { return bytes < row || bytes % 16 || bytes >> 40; };
   bool tma = true;
   for (const Rows &r : all)
-    if (r.ptr && (!aligned(r.ptr, 16) || (r.rows > 1 && off(r.stride[1] * r.es, r.width * r.es)) ||
+    if (r.ptr && (!aligned(r.ptr, 16) || r.width * r.es % 16 || (r.rows > 1 && off(r.stride[1] * r.es, r.width * r.es)) ||
                   (r.outer > 1 && off(r.stride[0] * r.es, r.width * r.es))))
       tma = false;
   return tma ? 2 : pairs(all, dim) ? 1 : 0;

@@ -1,0 +1,72 @@
+"""The layer operators at the ends of sequences, rows and types, against the fp64 oracle.
+Tolerances are test_layer.py's."""
+import numpy as np
+import pytest
+import torch
+
+import layer_abi
+import state_space_model_03_gb300 as ssm
+from oracle import layer as oracle
+from test_layer import GTOL, STATE_TOL, TOL, TYPES, _close, _gen, _i32, _norm_problem, _packed_problem, _rand, _scan_problem
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- odd widths in rows of 16 bytes ----
+
+def _padded(t, step):
+    """t in rows `step` apart that end with the buffer, NaN between them."""
+    *outer, n, d = t.shape
+    rows = int(np.prod(outer)) * n
+    flat = torch.full(((rows - 1) * step + d,), float("nan"), dtype=t.dtype, device="cuda")
+    strides = (n * step, step, 1)[-t.dim():]
+    return flat.as_strided(t.shape, strides).copy_(t)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,d", [(1200, 333), (1153, 33), (1100, 1)])
+def test_odd_widths_in_rows_of_16_bytes(dtype, n, d):
+    """Rows that start on 16 bytes, of an odd number of channels, in segments: nothing beyond a row's last channel counts
+    or is written."""
+    step = (d + 8) // 8 * 8
+    p = _scan_problem((2, n, d), dtype, seed=n)
+    dout = _rand(_gen(3), 2, n, d, dtype=dtype)
+    q = {k: v if k == "decay" else _padded(v, step) for k, v in p.items()}
+    outs = {k: _padded(torch.zeros_like(p["x"]), step) for k in ("out", "dx", "dgate", "dinput_gate")}
+    f32 = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    last, kept, ddecay, dinit = f32(2, d), f32(2, -(-n // 64), d), f32(d), f32(2, d)
+    sizes = dict(rate=8.0, batch=2, seqlen=n, dim=d)
+    assert layer_abi.run("gated_scan", layer_abi.params("gated_scan", dtype, **sizes, **q, out=outs["out"], last_state=last, kept=kept)) == 0
+    want, wlast = oracle.gated_scan(**p)
+    _close(outs["out"], want, TOL[dtype], "out")
+    _close(last, wlast, STATE_TOL, "last")
+    grads = {k: outs[k] for k in ("dx", "dgate", "dinput_gate")} | {"ddecay": ddecay, "dinitial_state": dinit}
+    args = sizes | q | {"dout": _padded(dout, step), "kept": kept}
+    assert layer_abi.run("gated_scan_bwd", layer_abi.params("gated_scan_bwd", dtype, **args, **grads)) == 0
+    ref = oracle.gated_scan_bwd(dout, None, **p)
+    for k, v in grads.items():
+        _close(v, ref[k[1:]], GTOL[v.dtype], k)
+    for v in outs.values():
+        flat = torch.empty(0, dtype=dtype, device="cuda").set_(v.untyped_storage())
+        assert int(torch.isnan(flat).sum()) == (2 * n - 1) * (step - d)
+    # the decay's gradient alone, from Python: nothing is written in rows
+    leaf = p["decay"].clone().requires_grad_()
+    got, = torch.autograd.grad(ssm.gated_scan_fn(**(q | {"decay": leaf})), leaf, args["dout"])
+    _close(got, ref["decay"], GTOL[got.dtype])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [333, 33])
+def test_packed_odd_widths_in_rows_of_16_bytes(dtype, dim):
+    lengths = [500, 3, 700, 64, 200]
+    n, step = sum(lengths), (dim + 8) // 8 * 8
+    p, t, st = _packed_problem(lengths, dim, dtype, seed=dim)
+    want, wst = oracle.packed_gated_scan(**p, lengths=lengths, state=st, **t)
+    tables = ssm.request_tables(_i32(lengths), n, **t)
+    q = {k: v if k == "decay" else _padded(v, step) for k, v in p.items()}
+    out = _padded(torch.zeros_like(p["x"]), step)
+    a = layer_abi.params("packed_gated_scan", dtype, rate=8.0, dim=dim, slots=st.shape[0], **q, state=st, out=out)
+    a.tables = layer_abi.packed_tables(tables)
+    assert layer_abi.run("packed_gated_scan", a) == 0
+    _close(out, want, TOL[dtype], "out")
+    _close(st, wst, STATE_TOL, "state")
