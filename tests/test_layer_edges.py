@@ -70,3 +70,83 @@ def test_packed_odd_widths_in_rows_of_16_bytes(dtype, dim):
     assert layer_abi.run("packed_gated_scan", a) == 0
     _close(out, want, TOL[dtype], "out")
     _close(st, wst, STATE_TOL, "state")
+
+
+# ---- packed segments ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("times", [1, 8])  # segments of one tile, of two
+def test_packed_neighbours_do_not_leak_over_segments(dtype, bad, times):
+    """test_layer.py's, over segments: a bad request that crosses their ends, good ones that start in the segment that it
+    ends in and go on into the next, one that starts where a segment does, and bad padding of whole segments."""
+    lengths = [times * v for v in (50, 300, 150, 12, 128, 60, 600)]
+    total, pad = sum(lengths), times * 300
+    p, t, st = _packed_problem(lengths, 70, dtype, pad=pad, seed=21, spare=1)
+    t["context"] = _i32([3, 0, 5, 0, 4, 0, 0])
+    tables = ssm.request_tables(_i32(lengths), total + pad, **t)
+    st2 = st.clone()
+    clean = ssm.packed_gated_scan_fn(**p, tables=tables, state=st2)
+    want, wst = oracle.packed_gated_scan(**p, lengths=lengths, state=st, **t)
+    _close(clean, want, TOL[dtype])
+    _close(st2, wst, STATE_TOL)
+    slots, starts = t["slots"].tolist(), np.concatenate([[0], np.cumsum(lengths)])
+    rows = torch.ones(total + pad, dtype=torch.bool, device="cuda")
+    for r in (1, 5):
+        rows[starts[r]:starts[r + 1]] = False
+    for k in ("x", "gate", "input_gate"):
+        p[k][~rows] = bad
+        p[k][total:] = bad
+    for r in (1, 3, 5, 6):
+        st[slots[r]] = bad  # not read: without context
+    got = ssm.packed_gated_scan_fn(**p, tables=tables, state=st)
+    assert torch.equal(got[rows], clean[rows])
+    for r in (0, 2, 3, 4, 6):
+        assert torch.equal(st[slots[r]], st2[slots[r]])
+
+
+# ---- graphs at once ----
+
+def test_graphs_replayed_at_once():
+    """Two graphs of a training step and two of a packed batch, all in segments with workspaces, on a stream each, again
+    and again: every one has its own."""
+    lengths, n = [1500, 0, 3500], 5000
+
+    def problem(i):
+        if i < 2:
+            p = _scan_problem((1, n, 64), torch.bfloat16, seed=70 + i)
+            leaves = {k: v.requires_grad_() for k, v in p.items()}
+            dout = _rand(_gen(72 + i), 1, n, 64, dtype=torch.bfloat16)
+
+            def train():
+                out = ssm.gated_scan_fn(**leaves)
+                return [out.detach(), *torch.autograd.grad(out, list(leaves.values()), dout)]
+            return train
+        p, t, st = _packed_problem(lengths, 64, torch.bfloat16, seed=70 + i, spare=0)
+        t["context"] = _i32([0, 0, 0])  # so that a replay does not go on from the one before
+        tables = ssm.request_tables(_i32(lengths), n, **t)
+        return lambda: [ssm.packed_gated_scan_fn(**p, tables=tables, state=st), st.clone()]
+
+    work = [problem(i) for i in range(4)]
+    want = [[v.clone() for v in w()] for w in work]
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for w, s in zip(work, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            held.append(w())
+        graphs.append(graph)
+    for _ in range(4):
+        for outs in held:
+            for v in outs:
+                v.zero_()
+        torch.cuda.synchronize()
+        for _ in range(25):
+            for graph, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for outs, wanted in zip(held, want):
+            for a, b in zip(outs, wanted):
+                assert torch.equal(a, b)
