@@ -280,9 +280,11 @@ __global__ void __launch_bounds__(kGatedThreads, 4) ss_gated_maps_kernel(const _
   }
 }
 
-// CL: a cluster's CTAs take consecutive tiles.
+// CL: a cluster's CTAs take consecutive tiles. Single values of three tensors are addresses
+// enough for 150 registers: held to 128, a spill of 100 bytes took 6001 packed tokens x 1301
+// from 52 us to 86.
 template <typename T, int ROWS, bool IG, bool PACKED, bool CL>
-__global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 6 : sizeof(T) == 4 ? 4 : 6)
+__global__ void __launch_bounds__(kGatedThreads, ROWS == kSingles && IG ? 3 : ROWS != kTma ? 4 : CL ? 6 : sizeof(T) == 4 ? 4 : 6)
     ss_gated_scan_kernel(const __grid_constant__ GatedScanParams p, const __grid_constant__ ScanMaps tm) {
   constexpr int S = kRun;
   constexpr bool TMA = ROWS == kTma, PAIR = ROWS != kSingles;
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 6 : siz
       return v.widen();
     };
     run_gates<IG>(me.open, me.near, get, n, e);
-    if ((tile_of(it) + 1) * kGatedTile > p.tokens) {  // past the end the state stays
+    if ((tile_of(it) + 1) * kGatedTile > p.tokens) {  // past the end a finite state stays
 #pragma unroll
       for (int j = 0; j < S; ++j)
         if (t0 + j >= p.tokens) n[j] = e[j] = 0;
@@ -520,11 +522,21 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 4 : CL ? 6 : siz
       finish(it, start, n, e, now);
     }
   }
-  if constexpr (!CL) {
-    if (p.last && rank == share - 1 && threadIdx.x >= kGatedThreads - 16) me.put_pair(p.last + (long long)b * p.dim, h);
-  } else {
-    if (p.last && rank == 0 && threadIdx.x < 16) me.put_pair(p.last + (long long)b * p.dim, h);
-    cluster_sync();  // nobody leaves while its shared memory is written to
+  if constexpr (CL) cluster_sync();  // nobody leaves while its shared memory is written to
+  if constexpr (!PACKED) {
+    // The last token's state, from the half warp that has the token. Over tokens past the
+    // end an infinite state does not stay (0 * inf): there the output has it.
+    const int left = p.tokens - (tile_of(rounds - 1) * kGatedTile + run * S);
+    if (p.last && left > 0 && left <= S) {
+      Two<T, PAIR> o;
+      if constexpr (TMA) {
+        o.load(&sm.out[warp][half * S + left - 1][2 * l], true, true);
+      } else {
+        o.load(out + (p.tokens - 1) * p.so[1], ok0, ok1);
+      }
+      const float2 w = upk(h), q = upk(o.widen());
+      me.put_pair(p.last + (long long)b * p.dim, pk(w.x == w.x ? w.x : q.x, w.y == w.y ? w.y : q.y));
+    }
   }
   if constexpr (TMA) {
     if (lane == 0) stores_done();

@@ -12,6 +12,29 @@ from test_layer import GTOL, STATE_TOL, TOL, TYPES, _close, _gen, _i32, _norm_pr
 pytestmark = pytest.mark.gpu
 
 
+# ---- the last token ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("n,d", [
+    # a part of a run of 8 tokens, a tile, one token more, a cluster of a CTA a tile, one with tiles past the end, segments
+    (1, 8), (5, 8), (8, 33), (64, 40), (65, 40), (300, 70), (1100, 1304), (1090, 1301), (1200, 48), (1216, 33),
+])
+def test_last_state_is_what_the_last_token_leaves(dtype, bad, n, d):
+    """Infinite there too: no token comes after it, whatever is left of its tile and of its cluster's."""
+    p = _scan_problem((2, n, d), dtype, seed=n + d)
+    clean, clean_last = ssm.gated_scan_fn(**p, return_last_state=True)
+    at = (1, n - 1, d // 2)
+    p["x"][at] = bad
+    out, last = ssm.gated_scan_fn(**p, return_last_state=True)
+    want = torch.tensor(bad, device="cuda")
+    torch.testing.assert_close(out[at].float(), want, equal_nan=True)
+    torch.testing.assert_close(last[1, d // 2], want, equal_nan=True)
+    out[at] = clean[at]
+    last[1, d // 2] = clean_last[1, d // 2]
+    assert torch.equal(out, clean) and torch.equal(last, clean_last)
+
+
 # ---- odd widths in rows of 16 bytes ----
 
 def _padded(t, step):
