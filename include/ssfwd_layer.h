@@ -227,9 +227,9 @@ int ss_rms_norm_bwd(const ss_rms_norm_bwd_params *p, void *stream);
  *     out = v / scale rounded to nearest even, so that v is about out * scale
  *
  * The quotient is v times the scale's reciprocal: exact for a power of two, within 2^-23
- * of it for an fp32 scale, which itself is most times the nearest fp32 to 1/448. A group
- * with a NaN has scale NaN and is NaN throughout; so has the group of an infinity, beside
- * which its row's groups are zeros.
+ * of it for an fp32 scale, which itself is rounded once. A group with a NaN or an infinity
+ * among its v has scale NaN and is NaN throughout. An infinite s makes its own v NaN and
+ * the rest of its row zeros.
  *
  *   out          (rows, dim) bytes, dim stride 1.
  *   scale        (rows, ceil(dim / group)) fp32, or bytes of e8m0; contiguous.

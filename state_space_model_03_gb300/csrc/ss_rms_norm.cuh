@@ -26,6 +26,7 @@ __device__ __forceinline__ float larger(float a, float b) {
 }
 
 // The scale of a group with `most` as its largest (NaN: it has one), and its reciprocal.
+// Both are NaN where most is infinite or NaN: no scale brings an infinity to 448.
 // The least power of two not below most / 448 = most / (1.75 2^8): its exponent is most's
 // less 8, and one more where most's fraction is above 1.75; at least 2^-126.
 struct Scale {
@@ -42,8 +43,9 @@ __device__ __forceinline__ Scale scale_of(float most, bool e8m0) {
     s.scale = 0.f;
     s.inverse = __uint_as_float(fine ? (254 - p) << 23 : 0x7fffffffu);
   } else {
-    s.scale = most * (1.f / 448.f);
+    s.scale = most / 448.f;
     if (s.scale < 1.17549435e-38f) s.scale = 1.17549435e-38f;
+    if (!(most < __uint_as_float(0x7f800000u))) s.scale = __uint_as_float(0x7fffffffu);
     s.inverse = __frcp_rn(s.scale);
     s.byte = 0;
   }

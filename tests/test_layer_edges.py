@@ -173,3 +173,41 @@ def test_graphs_replayed_at_once():
         for outs, wanted in zip(held, want):
             for a, b in zip(outs, wanted):
                 assert torch.equal(a, b)
+
+
+# ---- scales ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("e8m0", [False, True])
+@pytest.mark.parametrize("group", [None, 32, 64, 128])
+@pytest.mark.parametrize("dim", [256, 261, 1024])
+@pytest.mark.parametrize("big", [3e38, float("inf"), -float("inf")])
+def test_a_group_with_an_infinity_is_nan(dtype, e8m0, group, dim, big):
+    """Where the infinity comes of the weight: the row's other groups hold what they held."""
+    x = _rand(_gen(80), 3, dim, dtype=dtype).abs() + 2
+    w = torch.ones(dim, device="cuda")
+    x[:, 40] = 1000.0  # some 10 times the rest's root mean square: 3e38 of it is past fp32
+    kind = torch.float8_e8m0fnu if e8m0 else torch.float32
+    clean = ssm.rms_norm_quant_fn(x, w, group_size=group, scale_dtype=kind)
+    w[40] = big
+    q, scale = ssm.rms_norm_quant_fn(x, w, group_size=group, scale_dtype=kind)
+    size = group or dim
+    bad = slice(40 // size * size, (40 // size + 1) * size)
+    assert torch.isnan(q.float()[:, bad]).all() and torch.isnan(scale.float()[:, 40 // size]).all()
+    keep, groups = torch.ones(dim, dtype=torch.bool, device="cuda"), torch.ones(scale.shape[1], dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    groups[40 // size] = False
+    assert torch.equal(q.float()[:, keep], clean[0].float()[:, keep])
+    assert torch.equal(scale.float()[:, groups], clean[1].float()[:, groups])
+
+
+@pytest.mark.parametrize("group", [None, 32, 128])
+@pytest.mark.parametrize("shape", [(700, 264), (37, 769), (700, 2560)])
+def test_fp32_scales_are_rounded_once(group, shape):
+    """The largest value over 448 to the nearest fp32, from the values that the norm gives in fp32."""
+    p = _norm_problem(shape, torch.float32, "same", seed=81)
+    v = ssm.rms_norm_fn(**p)
+    _, scale = ssm.rms_norm_quant_fn(**p, group_size=group)
+    size = group or shape[1]
+    most = torch.stack([part.abs().amax(1) for part in v.split(size, 1)], 1)
+    assert torch.equal(scale, (most.double() / 448.0).float())
