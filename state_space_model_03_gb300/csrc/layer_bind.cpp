@@ -339,12 +339,13 @@ PyObject *gated_state_update(PyObject *, PyObject *const *a, Py_ssize_t given) {
 
 // ---- norm ----
 
-// (rows, dim) of a tensor of any number of dimensions, its rows at one distance.
+// (rows, dim) of a tensor of any number of dimensions, its rows at one distance: without
+// a copy where they are so already, as parts of wider rows are.
 Held rows2(const at::Tensor *t) {
   if (!t) return Held{};
   const int64_t dim = t->size(-1);
-  if (t->dim() == 2 && (dim == 1 || t->stride(1) == 1)) return Held{*t};
-  return Held{t->reshape({dim ? t->numel() / dim : 0, dim}).contiguous()};
+  const at::Tensor r = t->dim() == 2 ? *t : t->reshape({dim ? t->numel() / dim : 0, dim});
+  return Held{dim == 1 || r.stride(1) == 1 ? r : r.contiguous()};
 }
 struct Norm {
   Held x, residual, weight;

@@ -211,3 +211,47 @@ def test_fp32_scales_are_rounded_once(group, shape):
     size = group or shape[1]
     most = torch.stack([part.abs().amax(1) for part in v.split(size, 1)], 1)
     assert torch.equal(scale, (most.double() / 448.0).float())
+
+
+# ---- rows of rank 3 ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_of_parts_of_wider_rows_copies_nothing(dtype):
+    """Parts of a projection's rows in rank 3, forward and backward: what is allocated is what is returned."""
+    b, n, d = 3, 700, 640
+    g = _gen(90)
+    wide, dwide = _rand(g, b, n, 3 * d, dtype=dtype), _rand(g, b, n, 3 * d, dtype=dtype)
+    x, res, _ = wide.split(d, 2)
+    dout, dsum, _ = dwide.split(d, 2)
+    w = (_rand(g, d, std=0.1) + 1).requires_grad_()
+    one, spare = b * n * d * x.element_size(), 2 << 20  # spare: statistics, parts of the weight's gradient
+
+    def peak(call):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        got = call()
+        return got, torch.cuda.max_memory_allocated() - before
+
+    with torch.no_grad():
+        got, most = peak(lambda: ssm.rms_norm_fn(x, w, residual=res, prenorm=True))
+        assert most <= 2 * one + spare
+        want = ssm.rms_norm_fn(x.contiguous(), w, residual=res.contiguous(), prenorm=True)
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+        q, most = peak(lambda: ssm.rms_norm_quant_fn(x, w, residual=res, prenorm=True, group_size=32))
+        assert most <= one + b * n * d * 2 + spare
+        want = ssm.rms_norm_quant_fn(x.contiguous(), w, residual=res.contiguous(), prenorm=True, group_size=32)
+        assert all(torch.equal(a.float(), c.float()) for a, c in zip(q, want))
+    leaves = [x.detach().requires_grad_(), w, res.detach().requires_grad_()]
+    outs = ssm.rms_norm_fn(leaves[0], w, residual=leaves[2], prenorm=True)
+    spare += 608 * d * 4
+    got, most = peak(lambda: torch.autograd.grad(outs, leaves, (dout, dsum)))
+    assert most <= one + spare  # one tensor for both inputs
+    ds, dw = oracle.rms_norm_bwd(dout, dsum, torch.zeros_like(x), w, outs[1].detach())
+    _close(got[0], ds, GTOL[dtype])
+    _close(got[1], dw, GTOL[torch.float32])
+    _close(got[2], ds, GTOL[dtype])
+    # a last stride of another kind is copied
+    t = _rand(g, b, d, n, dtype=dtype).transpose(1, 2)
+    want, _ = oracle.rms_norm(t, w)
+    _close(ssm.rms_norm_fn(t, w), want, TOL[dtype])
