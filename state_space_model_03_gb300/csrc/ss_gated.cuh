@@ -16,6 +16,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "ss_fwd_kernel.cuh"
 #include "ss_layer.h"
@@ -148,6 +149,17 @@ constexpr int kRuns = kGatedTile / kRun;
 constexpr int kGatedWarps = kRuns / 2;
 constexpr int kGatedThreads = kGatedWarps * 32;
 enum RowAccess { kSingles, kPairs, kTma };
+
+// SSFWD_TEST_STALL=<k>, SSFWD_TEST_STALL_MAPS=<k>: a round whose copies, or whose maps in a
+// cluster, are lost, and short waits.
+inline WaitHook wait_hook() {
+  WaitHook w;
+  const char *copy = std::getenv("SSFWD_TEST_STALL"), *maps = std::getenv("SSFWD_TEST_STALL_MAPS");
+  w.limit = copy || maps ? 1u << 10 : kMaxWaitIters;
+  if (copy) w.copy = std::atoi(copy);
+  if (maps) w.maps = std::atoi(maps);
+  return w;
+}
 
 // The exchange within a cluster.
 __device__ __forceinline__ uint32_t remote_of(const void *p, int rank) {

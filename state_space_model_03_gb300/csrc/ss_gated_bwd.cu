@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
   __shared__ f2 backs[2][kRuns][16];         // R
   __shared__ ulonglong2 tiles[CL ? 2 : 1][kGatedMostCluster][16];  // CL: (N, R) of whole tiles
   __shared__ uint64_t here[2];                                     // CL: they have come
+  __shared__ int asked;  // thread 0's: turns whose copies it has asked for
   __shared__ f2 carry[2][16];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), l = lane & 15, half = lane >> 4;
   // CL: a unit's CTAs are a cluster; else they have a segment each
@@ -138,15 +139,17 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
   T *const dx = p.dx ? static_cast<T *>(p.dx) + b * p.sdx[0] + c0 : nullptr;
   T *const dgate = p.dgate ? static_cast<T *>(p.dgate) + b * p.sdg[0] + c0 : nullptr;
   T *const digate = IG && p.digate ? static_cast<T *>(p.digate) + b * p.sdi[0] + c0 : nullptr;
-  bool fine = true;
+  bool fine = true;  // no wait has given up; after one has, nothing more is asked of a barrier
   // turns count up while the tiles go down
   auto tile_of = [&](int turn) { return CL ? (rounds - 1 - turn) * K + rank : rank * p.plan.seg_tiles + rounds - 1 - turn; };
   auto load = [&](int turn) {
     const int first = tile_of(turn) * kGatedTile;
     if constexpr (TMA) {
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && fine) {
         const int s = turn % kStages;
+        asked = turn + 1;
         mbar_arrive_expect_tx(&sm.full[s], (IG ? 4 : 3) * sizeof(sm.rows[0][0]));
+        if (turn == p.wait.copy) return;
         tma_load_3d(sm.rows[s][0], &tm.x, &sm.full[s], ct * kGatedCh, first, b);
         tma_load_3d(sm.rows[s][1], &tm.gate, &sm.full[s], ct * kGatedCh, first, b);
         if constexpr (IG) tma_load_3d(sm.rows[s][2], &tm.igate, &sm.full[s], ct * kGatedCh, first, b);
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
     f2 n[S], inv[S], h[S];
     f2 N = 0, E = 0, R = 0, start = next;
     if constexpr (TMA) {
-      fine = mbar_wait(&sm.full[stage], (turn / kStages) & 1, p.err, kErrWaitFull, fine ? kMaxWaitIters : 1) && fine;
+      fine = mbar_wait(&sm.full[stage], (turn / kStages) & 1, p.err, kErrWaitFull, fine ? p.wait.limit : 1) && fine;
     } else {
       load(turn);
     }
@@ -289,10 +292,10 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
           all.x = step2(q, all.x, q);
         }
         // its place there was read in the turn before the last, and every CTA has begun the last one
-        for (int r = half; r < K; r += 2) send(&tiles[buf][rank][l], &here[buf], r, all);
+        for (int r = turn == p.wait.maps ? K : half; r < K; r += 2) send(&tiles[buf][rank][l], &here[buf], r, all);
       }
-      fine = mbar_wait_cluster(&here[buf], (turn >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
-      if (threadIdx.x == 0 && turn + 2 < rounds) expect_maps(turn + 2);
+      fine = mbar_wait_cluster(&here[buf], (turn >> 1) & 1, p.err, kErrWaitReady, fine ? p.wait.limit : 1) && fine;
+      if (threadIdx.x == 0 && fine && turn + 2 < rounds) expect_maps(turn + 2);
       for (int c = K - 1; c >= 0; --c) {
         if (c == rank) e = back;
         const ulonglong2 q = tiles[buf][c][l];
@@ -397,10 +400,8 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS != kTma ? 3 : sizeof(T) ==
   if constexpr (TMA) {
     if (lane == 0) stores_done();
     if (!fine && threadIdx.x == 0) {  // a wait gave up: the copies under way land before the CTA leaves
-      for (int s = 0; s < kStages && s < rounds; ++s) {
-        const int turn = (rounds - 1 - s) / kStages * kStages + s;
-        mbar_wait(&sm.full[s], (turn / kStages) & 1, p.err, kErrWaitFull);
-      }
+      for (int turn = max(asked - kStages, 0); turn < asked; ++turn)
+        mbar_wait(&sm.full[turn % kStages], (turn / kStages) & 1, p.err, kErrWaitFull, p.wait.limit);
     }
   }
   if constexpr (CL) cluster_sync();  // nobody leaves while its shared memory is written to
@@ -480,7 +481,9 @@ cudaError_t pick(int rows, TensorMapEncode enc, const GatedBwdParams &p, cudaStr
 
 }  // namespace
 
-cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, const GatedBwdParams &p, cudaStream_t s) {
+cudaError_t launch_gated_bwd(int dtype, int rows, TensorMapEncode enc, const GatedBwdParams &given, cudaStream_t s) {
+  GatedBwdParams p = given;
+  p.wait = wait_hook();
   cudaError_t e = dtype == 0   ? pick<float>(rows, enc, p, s)
                   : dtype == 1 ? pick<__half>(rows, enc, p, s)
                                : pick<__nv_bfloat16>(rows, enc, p, s);

@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS == kSingles && IG ? 3 : RO
   __shared__ ulonglong2 maps[2][kRuns][16];                                // (N, E) of the lane's channels, by run
   __shared__ ulonglong2 tiles[CL ? 2 : 1][kGatedMostCluster][16];          // CL: the same by CTA
   __shared__ uint64_t here[2];                                             // CL: the tiles' maps have come
+  __shared__ int asked;  // thread 0's: rounds whose copies it has asked for
   __shared__ f2 carry[2][16];                                              // !CL: the state after a tile
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   // CL: a unit's CTAs are a cluster; else they have a segment each
@@ -312,13 +313,15 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS == kSingles && IG ? 3 : RO
   const T *const gate = static_cast<const T *>(p.gate) + b * p.sg[0] + c0;
   const T *const igate = IG ? static_cast<const T *>(p.igate) + b * p.si[0] + c0 : nullptr;
   T *const out = static_cast<T *>(p.out) + b * p.so[0] + c0;
-  bool fine = true;  // no wait has given up
+  bool fine = true;  // no wait has given up; after one has, nothing more is asked of a barrier
   auto load = [&](int it) {
     const int first = tile_of(it) * kGatedTile;
     if constexpr (TMA) {
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && fine) {
         const int s = it % kStages;
+        asked = it + 1;
         mbar_arrive_expect_tx(&sm.full[s], (IG ? 3 : 2) * sizeof(sm.rows[0][0]));
+        if (it == p.wait.copy) return;
         tma_load_3d(sm.rows[s][0], &tm.x, &sm.full[s], ct * kGatedCh, first, b);
         tma_load_3d(sm.rows[s][1], &tm.gate, &sm.full[s], ct * kGatedCh, first, b);
         if constexpr (IG) tma_load_3d(sm.rows[s][2], &tm.igate, &sm.full[s], ct * kGatedCh, first, b);
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS == kSingles && IG ? 3 : RO
       start = of(now.from);
     }
     if constexpr (TMA) {
-      fine = mbar_wait(&sm.full[it % kStages], (it / kStages) & 1, p.err, kErrWaitFull, fine ? kMaxWaitIters : 1) && fine;
+      fine = mbar_wait(&sm.full[it % kStages], (it / kStages) & 1, p.err, kErrWaitFull, fine ? p.wait.limit : 1) && fine;
     }
     auto get = [&](int which, int j) {
       Two<T, PAIR> v;
@@ -510,10 +513,10 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS == kSingles && IG ? 3 : RO
         ulonglong2 all = map[0][l];
 #pragma unroll
         for (int r = 1; r < kRuns; ++r) all = then<PACKED>(all, map[r][l]);
-        for (int r = half; r < K; r += 2) send(&tiles[it & 1][rank][l], &here[it & 1], r, all);
+        for (int r = it == p.wait.maps ? K : half; r < K; r += 2) send(&tiles[it & 1][rank][l], &here[it & 1], r, all);
       }
-      fine = mbar_wait_cluster(&here[it & 1], (it >> 1) & 1, p.err, kErrWaitReady, fine ? kMaxWaitIters : 1) && fine;
-      if (threadIdx.x == 0 && it + 2 < rounds) expect_maps(it + 2);
+      fine = mbar_wait_cluster(&here[it & 1], (it >> 1) & 1, p.err, kErrWaitReady, fine ? p.wait.limit : 1) && fine;
+      if (threadIdx.x == 0 && fine && it + 2 < rounds) expect_maps(it + 2);
       f2 start = h;
       for (int r = 0; r < K; ++r) {
         if (r == rank) start = h;
@@ -541,10 +544,8 @@ __global__ void __launch_bounds__(kGatedThreads, ROWS == kSingles && IG ? 3 : RO
   if constexpr (TMA) {
     if (lane == 0) stores_done();
     if (!fine && threadIdx.x == 0) {  // a wait gave up: the copies under way land before the CTA leaves
-      for (int s = 0; s < kStages && s < rounds; ++s) {
-        const int it = (rounds - 1 - s) / kStages * kStages + s;
-        mbar_wait(&sm.full[s], (it / kStages) & 1, p.err, kErrWaitFull);
-      }
+      for (int it = max(asked - kStages, 0); it < asked; ++it)
+        mbar_wait(&sm.full[it % kStages], (it / kStages) & 1, p.err, kErrWaitFull, p.wait.limit);
     }
   }
 }
@@ -631,7 +632,9 @@ GatedPlan gated_plan(int dtype, long long units, int tiles) {
   return plan;
 }
 
-cudaError_t launch_gated_scan(int dtype, int rows, TensorMapEncode enc, const GatedScanParams &p, cudaStream_t s) {
+cudaError_t launch_gated_scan(int dtype, int rows, TensorMapEncode enc, const GatedScanParams &given, cudaStream_t s) {
+  GatedScanParams p = given;
+  p.wait = wait_hook();
   return dtype == 0   ? pick<float>(rows, enc, p, s)
          : dtype == 1 ? pick<__half>(rows, enc, p, s)
                       : pick<__nv_bfloat16>(rows, enc, p, s);

@@ -24,6 +24,14 @@ GatedPlan gated_plan(int dtype, long long units, int tiles);
 // Of each segment 16 lanes' maps (two pairs), and after all of these 16 lanes' start states.
 inline long long gated_map_bytes(long long units, const GatedPlan &plan) { return plan.segs > 1 ? units * plan.segs * 384 : 0; }
 
+// What a test makes of the recurrence's waits: limit: tries of one until it gives up (set
+// by the launch); copy, maps: the round whose copies, or whose exchange in a cluster,
+// never come (-1: none).
+struct WaitHook {
+  uint32_t limit;
+  int copy = -1, maps = -1;
+};
+
 struct GatedScanParams {
   int tokens, dim;      // per sequence
   int batch, channel_tiles;  // sequences; tiles of channels
@@ -32,6 +40,7 @@ struct GatedScanParams {
   void *maps;  // gated_map_bytes
   float rate;
   int32_t *err;
+  WaitHook wait;
   const void *x, *gate, *igate;
   const float *decay, *init;  // init (batch, dim) or NULL
   void *out;
@@ -52,6 +61,7 @@ struct GatedBwdParams {
   void *maps;
   float rate;
   int32_t *err;
+  WaitHook wait;
   const void *x, *gate, *igate, *dout;
   const float *decay, *kept, *dlast;  // dlast (batch, dim) or NULL
   void *dx, *dgate, *digate;          // NULL: not wanted
