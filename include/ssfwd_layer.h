@@ -36,9 +36,11 @@ extern "C" {
  *     h = a * h + sqrt(1 - a^2) * i * x[t,c],   out[t,c] = h
  *
  * h starts from initial_state (zero when NULL) and is held in fp32; out is h
- * rounded once. What a state loses is 2^-24 of the largest before it per token. decay
- * is finite; a gate may be infinite (open or shut). A NaN, or an infinite state, is a
- * NaN from its next token on, in its channel and sequence alone.
+ * rounded once, last_state the last token's h. What a state loses is 2^-24 of the largest
+ * before it per token. decay is finite; a gate may be infinite (open or shut). A NaN, or
+ * an infinite state, is a NaN from its next token on, in its channel and sequence alone.
+ * The factor sqrt(1 - a^2) is every token's, the first one's too: layers that take it as 1
+ * where a document starts are not this one.
  *
  *   x, gate, input_gate, out  (batch, seqlen, dim) in dtype, dim stride 1; stride
  *                {batch, token}. input_gate may be NULL.
@@ -52,7 +54,8 @@ extern "C" {
  *                sequences and channels alone fill the device): maps of parts of a
  *                sequence, which run side by side.
  *
- * batch * ceil(dim / 32) < 2^24, seqlen and dim < 2^31 - 2^20. out overlaps no input.
+ * batch * ceil(dim / 32) < 2^24, 1 <= seqlen (batch may be 0), seqlen and dim < 2^31 -
+ * 2^20. out overlaps no input.
  */
 #define SS_GATED_TILE 64
 
@@ -84,6 +87,9 @@ int ss_gated_scan(const ss_gated_scan_params *p, void *stream);
  *     G = g (a h[t-1] L + i x a^2 q),   dgate = G (1 - r)
  *     ddecay = sum over sequences and tokens of G * sigmoid(decay) / softplus(decay)
  *     dinitial_state = e before the first token
+ *
+ * An infinite or NaN dout, dlast or state makes gradients of its channel and sequence
+ * infinite or NaN, which of the two is not said.
  *
  * dx, dgate, dinput_gate (in dtype), ddecay (dim,) and dinitial_state (batch, dim)
  * fp32 may be NULL (not wanted). workspace: ss_gated_scan_bwd_workspace_size
@@ -139,7 +145,7 @@ int ss_packed_gated_scan(const ss_packed_gated_scan_params *p, void *stream);
 
 /* One token per request: row r goes with state slot_map[r] (or r, when slot_map
  * is NULL), which is read and written. A row with slot -1 gets out = 0. Two rows
- * must not share a slot. */
+ * must not share a slot. At most 65535 requests. */
 typedef struct ss_gated_state_update_params {
   int32_t abi_version, dtype;
   float rate;
@@ -163,7 +169,8 @@ int ss_gated_state_update(const ss_gated_state_update_params *p, void *stream);
  *     out = s / sqrt(mean(s^2) + eps) * weight
  *
  * The norm takes s as it is kept, so that the backward, which reads the kept sum,
- * is the gradient of what the forward computed. Squares are summed in fp32.
+ * is the gradient of what the forward computed. Squares are summed in fp32: a row whose
+ * sum of squares passes its range (values from some 2^64 / sqrt(dim) on) comes out as zeros.
  *
  *   x, out       (rows, dim) in dtype; residual, sum (rows, dim) in residual_dtype,
  *                which is dtype or fp32 and ignored without a residual. dim stride 1.
@@ -232,7 +239,8 @@ int ss_rms_norm_bwd(const ss_rms_norm_bwd_params *p, void *stream);
  * the rest of its row zeros.
  *
  *   out          (rows, dim) bytes, dim stride 1.
- *   scale        (rows, ceil(dim / group)) fp32, or bytes of e8m0; contiguous.
+ *   scale        (rows, ceil(dim / group)) fp32, or bytes of e8m0; contiguous, row by
+ *                row: a product that wants scales in tiles reorders them itself.
  */
 typedef enum ss_scale_type { SS_SCALE_F32 = 0, SS_SCALE_E8M0 = 1 } ss_scale_type;
 

@@ -16,8 +16,9 @@
 //
 // 8 x 2048 x 2560 bf16: 120 us, 4.9 TB/s (72% of the copy), five CTAs an SM, so that 640
 // run at once; with places of their own for the gradients (four an SM, two rounds) 142.
-// Bound by instruction issue: 130 a token and pair of channels, 18 of them on the
-// special-function unit.
+// Bound by latency at 17 warps an SM and by their uneven share, as the forward: 132
+// instructions a token and pair of channels, 18 of them on the special-function unit, at
+// 0.65 of the issue rate, DRAM at 0.54.
 #include "ss_gated.cuh"
 
 namespace ssk {

@@ -20,13 +20,15 @@
 // what comes out of it does not depend on what came before, NaN or not. A map with a
 // cut in it has N = kCut.
 //
-// 8 x 2048 x 2560 bf16 64 us, 5.3 TB/s (78% of the copy); 65536 x 2048 in clusters 271
-// us, 4.0 TB/s; 16384 packed tokens x 2560 107 us. Bound by instruction issue (62 a
-// token and pair of channels, 0.6 of the issue rate at the 17 warps an SM that 640 CTAs
-// make): 32 for the gates, the sigmoids' and the root's 10 on the special-function unit
-// among them, 7 for the scan, 6 to widen 16 bits, the rest for tiles and maps. Tiles of 64
-// channels (320 CTAs, 2 or 3 an SM) 78 us; loads into registers instead of TMA (103
-// instructions, half of them for addresses and ends) 128.
+// 8 x 2048 x 2560 bf16 64 us, 5.2 TB/s (77% of the copy); 65536 x 2048 in clusters 278
+// us, 3.9 TB/s; 16384 packed tokens x 2560 113 us. Nothing is at its rate (issue 0.59,
+// special functions 0.37, DRAM 0.58): what bounds the first is latency at the 17 warps an
+// SM that 640 CTAs make, and their share, five CTAs on 32 SMs and four on the others, which
+// are idle for up to a fifth of the time; in clusters the exchange of each round besides.
+// 63 instructions a token and pair of channels: 32 for the gates, the sigmoids' and the
+// root's 10 on the special-function unit among them, 7 for the scan, 6 to widen 16 bits,
+// the rest for tiles and maps. Tiles of 64 channels (320 CTAs, 2 or 3 an SM) 78 us; loads
+// into registers instead of TMA (103 instructions, half of them for addresses and ends) 128.
 #include "ss_gated.cuh"
 
 namespace ssk {
@@ -605,17 +607,28 @@ cudaError_t pick(int rows, TensorMapEncode enc, const GatedScanParams &p, cudaSt
 }  // namespace
 
 // Clusters read everything once, but have 8 CTAs at most. Wider ones, which not every
-// device runs, gain forward where sequences are long (64 units of 1024 tiles 252 us
-// instead of 271) and lose in shorter ones (48 units of 63 tiles 28 instead of 19) and
-// backward (64 units of 128 tiles 129 instead of 111). With few units they leave SMs idle, and segments, which read the rows a second time, are faster from two rounds of a
-// cluster on. Forward / forward and backward in us, bf16:
-//                              clusters    segments
-//   11 units, 94 tiles, packed  25           13
-//   16 units, 1024 tiles       349 / 782    113 / 284
-//   32 units, 256 tiles         53 / 149     54 / 127
-//   48 units, 63 tiles          19 / 53      23 / 58
-//   64 units, 128 tiles         39 / 111     54 / 128
-// All CTAs of a cluster run at once: as many of them as leave all clusters resident.
+// device runs, gain forward where sequences are long (64 units of 1024 tiles 7%) and lose
+// in shorter ones (48 units of 63 tiles 46%) and backward (64 units of 128 tiles 16%). With
+// few units they leave SMs idle, and segments, which read the rows a second time, are
+// faster from two rounds of a cluster on. Forward / forward and backward in us, bf16:
+//                                            clusters    segments
+//   16 units, 1024 tiles                    192 / 522   111 / 276
+//   32 units, 256 tiles                      54 / 143    59 / 140
+//   48 units, 63 tiles                       19 / 50     25 / 55
+//   64 units, 128 tiles                      40 / 108    58 / 139
+//   80 units, 256 tiles                      86 / 241   139 / 344
+//   11 units, 94 tiles, packed, 17 requests  35          18
+//   32 units, 256 tiles, packed, 40          85          54
+//   48 units, 256 tiles, packed, 40          90          71
+//   80 units, 256 tiles, packed, 40         114         104
+//   the same, one request                   104         143
+//   the same, one of 40 with most tokens    110         141
+// A packed segment reduces only the request that goes on after it, so segments gain for
+// more units there, but lose a third where one request has most of the tokens. The host,
+// which has to choose, does not know the lengths: the same 40 units.
+// All CTAs of a cluster run at once: as many of them as leave all clusters resident. The
+// kernel's registers leave room for a sixth CTA an SM, without which clusters of 8 or 7 do
+// not all find a place (90 units 32 us, 38 with five; packed 40, 54).
 GatedPlan gated_plan(int dtype, long long units, int tiles) {
   constexpr int kSms = 152, kSegCtas = 6;           // segments that an SM holds
   const int kClusterCtas = dtype == 0 ? 3 : 5;      // CTAs of clusters that it holds, by shared memory

@@ -45,8 +45,9 @@ def gated_scan_fn(x, gate, decay, input_gate=None, rate=8.0, initial_state=None,
     positive number; initial_state: (batch, dim) fp32 (None: zero). Per channel
     and token, with r = sigmoid(gate), i = sigmoid(input_gate) (1 without it):
     a = exp(-rate softplus(decay) r), h = a h + sqrt(1 - a^2) i x, out = h; h is
-    held in fp32. Returns out (x's dtype), or (out, last_state) with last_state
-    (batch, dim) fp32.
+    held in fp32. The factor sqrt(1 - a^2) is every token's, the first one's too. Returns
+    out (x's dtype), or (out, last_state) with last_state (batch, dim) fp32. At least one
+    token.
     """
     _cuda(x, "gated_scan_fn")
     return _bind().gated_scan(x, gate, decay, input_gate, rate, initial_state, return_last_state)
@@ -67,7 +68,8 @@ def packed_gated_scan_fn(x, gate, decay, tables, input_gate=None, rate=8.0, stat
 def gated_state_update(state, x, gate, decay, input_gate=None, rate=8.0, slots=None):
     """One token per request: x, gate, input_gate (requests, dim); row r goes with
     state[slots[r]] (slots None: r), updated in place; a row with slot -1 gets zeros.
-    Two rows must not share a slot. Returns out (requests, dim). Forward only.
+    Two rows must not share a slot. Up to 65535 requests. Returns out (requests, dim).
+    Forward only.
     """
     _cuda(x, "gated_state_update")
     return _bind().gated_state_update(state, x, gate, decay, input_gate, rate, slots)
@@ -101,8 +103,9 @@ def rms_norm_quant_fn(x, weight, residual=None, eps=1e-5, prenorm=False, residua
     scale, s). out: (..., dim) float8_e4m3fn; scale: (..., groups) with a scale for the
     row (group_size None) or for each group_size (32, 64 or 128) of its channels, so that
     the norm is about out * scale. scale_dtype float32: the group's largest value over
-    448 (2^-126 at least); float8_e8m0fnu: the least power of two not below that. Forward
-    only.
+    448 (2^-126 at least); float8_e8m0fnu: the least power of two not below that. A group
+    with a NaN or an infinity is NaN, scale and all. Scales lie row by row: a product that
+    wants them in tiles needs them reordered. Forward only.
     """
     _cuda(x, "rms_norm_quant_fn")
     if scale_dtype not in (torch.float32, torch.float8_e8m0fnu):
