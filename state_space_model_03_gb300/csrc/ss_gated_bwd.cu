@@ -11,8 +11,9 @@
 // token, n, the state before it and 1 / sqrt(1 - a^2) stay in registers; its gates are
 // taken again from the tile in shared memory for the gradients, which costs less than
 // registers that would halve the CTAs of an SM. The sum over tokens for the decay's
-// gradient stays in registers, then goes by CTA to the workspace and is added up by a
-// second launch: no atomics, the same result in every call.
+// gradient stays in registers (fp32: a lane adds an eighth of its CTA's tokens one after
+// the other, 2^-24 of the root of their number off), then goes by CTA to the workspace and
+// is added up by a second launch: no atomics, the same result in every call.
 //
 // 8 x 2048 x 2560 bf16: 120 us, 4.9 TB/s (72% of the copy), five CTAs an SM, so that 640
 // run at once; with places of their own for the gradients (four an SM, two rounds) 142.

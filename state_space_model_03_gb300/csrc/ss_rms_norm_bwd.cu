@@ -2,7 +2,8 @@
 //   ds = rstd (w dout - n mean(w dout n)) + dsum,  dw = sum over rows of dout n.
 // Bound by the traffic of its rows. A CTA (or, for short rows, each warp of it) takes
 // every so many-th row and keeps its columns' part of dw in registers; the parts go
-// to the workspace by CTA and a second launch adds them up: no atomics. 16384 x 2560 bf16
+// to the workspace by CTA and a second launch adds them up: no atomics. They are fp32: a
+// thread adds rows / CTAs terms one after the other, 2^-24 sqrt(rows / 304) off. 16384 x 2560 bf16
 // with the sum in fp32: 104 us, 6.4 TB/s (95% of the copy); three CTAs an SM 118, one 130.
 #include "ss_norm.cuh"
 
