@@ -35,6 +35,30 @@ def test_last_state_is_what_the_last_token_leaves(dtype, bad, n, d):
     assert torch.equal(out, clean) and torch.equal(last, clean_last)
 
 
+@pytest.mark.parametrize("n", [700, 1300])  # clusters; segments
+def test_gradients_beside_nan(n):
+    """Channels with a NaN or an infinity in a sequence leave the gradients of the other channels and sequences alone."""
+    shape = (3, n, 70)
+    p = _scan_problem(shape, torch.bfloat16, seed=n)
+    dout = _rand(_gen(4), *shape, dtype=torch.bfloat16)
+
+    def grads(p):
+        leaves = {k: v.clone().requires_grad_() for k, v in p.items()}
+        return dict(zip(leaves, torch.autograd.grad(ssm.gated_scan_fn(**leaves), list(leaves.values()), dout)))
+
+    clean = grads(p)
+    p["x"][0, :, 7] = float("nan")
+    p["gate"][1, 100:, 8] = float("nan")
+    p["x"][2, 50, 9] = float("inf")
+    got = grads(p)
+    same = torch.ones(shape, dtype=torch.bool, device="cuda")
+    same[0, :, 7] = same[1, :, 8] = same[2, :, 9] = False
+    for k in ("x", "gate", "input_gate"):
+        assert torch.equal(got[k][same], clean[k][same]), k
+    others = [c for c in range(70) if c not in (7, 8, 9)]
+    assert torch.equal(got["decay"][others], clean["decay"][others])
+
+
 # ---- odd widths in rows of 16 bytes ----
 
 def _padded(t, step):
@@ -211,6 +235,19 @@ def test_fp32_scales_are_rounded_once(group, shape):
     size = group or shape[1]
     most = torch.stack([part.abs().amax(1) for part in v.split(size, 1)], 1)
     assert torch.equal(scale, (most.double() / 448.0).float())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_row_whose_squares_pass_fp32_is_zeros(dtype):
+    """What the header says of it; the rows beside it are as without it."""
+    x = _rand(_gen(82), 3, 320, dtype=dtype)
+    w = torch.ones(320, device="cuda")
+    clean, q0 = ssm.rms_norm_fn(x, w), ssm.rms_norm_quant_fn(x, w, group_size=32)
+    x[1, 5] = 2e19  # its square is 4e38
+    out, q = ssm.rms_norm_fn(x, w), ssm.rms_norm_quant_fn(x, w, group_size=32)
+    for got, want in ((out, clean), (q[0].float(), q0[0].float()), (q[1], q0[1])):
+        assert torch.equal(got[::2], want[::2])
+    assert not out[1].any() and not q[0].float()[1].any() and (q[1][1] == 2.0**-126).all()
 
 
 # ---- rows of rank 3 ----
